@@ -31,6 +31,10 @@ EXPORTS = (
     "w4a8_decode_chain_workspace_bytes", "w4a8_decode_chain", "w4a8_linear_flagged", "w4a8_signal_ready",
     "w4a8_nvfp4_scale_bytes", "w4a8_nvfp4_quantize", "w4a8_nvfp4_pack_scales", "w4a8_nvfp4_gemm",
     "w4a8_nvfp4_linear_workspace_bytes", "w4a8_nvfp4_linear",
+    # include/w4a8_int8.h
+    "w4a8_int8_quantize", "w4a8_int8_linear_workspace_bytes", "w4a8_int8_gemm", "w4a8_int8_linear",
+    "w4a8_qk_norm_rope", "w4a8_kv_update", "w4a8_kv_dequant",
+    "w4a8_kv_attention_workspace_bytes", "w4a8_kv_attention",
 )
 
 
@@ -38,6 +42,32 @@ class ChainLayer(ctypes.Structure):
     """w4a8_chain_layer: one layer of a chain (device pointers)."""
     _fields_ = [("packed", ctypes.c_void_p), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
                 ("x", ctypes.c_void_p), ("y", ctypes.c_void_p)]
+
+
+class Heads(ctypes.Structure):
+    """w4a8_heads: bf16 rows [token][head][D] (element strides)."""
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("heads", ctypes.c_int32)]
+
+
+class Rope(ctypes.Structure):
+    """w4a8_rope: the position rotation (device fp64 frequencies)."""
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("factor", ctypes.c_float)]
+
+
+class CacheDesc(ctypes.Structure):
+    """w4a8_kv_cache: an int8 paged cache (device pointers)."""
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("pages", ctypes.c_int64), ("kv_heads", ctypes.c_int32),
+                ("page", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class BatchDesc(ctypes.Structure):
+    """w4a8_kv_batch: the sequences of a call (device index arrays)."""
+    _fields_ = [("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("q_start", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("batch", ctypes.c_int64), ("tokens", ctypes.c_int64)]
+
 
 _lib = None
 
@@ -91,6 +121,15 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "w4a8_nvfp4_gemm": (st, [vp, vp, vp, i64, vp, vp, vp, i64, i64, vp, vp]),
         "w4a8_nvfp4_linear_workspace_bytes": (sz, [i64, i64]),
         "w4a8_nvfp4_linear": (st, [vp, i64, i64, vp, vp, vp, i64, vp, vp, sz, vp]),
+        "w4a8_int8_quantize": (st, [vp, ctypes.c_int32, i64, i64, ctypes.c_int32, vp, vp, vp]),
+        "w4a8_int8_linear_workspace_bytes": (sz, [i64, i64, i64]),
+        "w4a8_int8_gemm": (st, [vp, vp, i64, vp, vp, i64, i64, vp, vp, sz, vp]),
+        "w4a8_int8_linear": (st, [vp, i64, i64, ctypes.c_int32, vp, vp, i64, vp, vp, sz, vp]),
+        "w4a8_qk_norm_rope": (st, [vp, vp, i64, ctypes.c_int32, vp, vp, ctypes.c_float, vp, vp, vp, vp, vp]),
+        "w4a8_kv_update": (st, [vp, vp, vp, vp, vp, vp, vp, ctypes.c_float, vp, vp, vp, vp]),
+        "w4a8_kv_dequant": (st, [vp, vp, i64, vp, vp, vp]),
+        "w4a8_kv_attention_workspace_bytes": (sz, [i64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32]),
+        "w4a8_kv_attention": (st, [vp, vp, vp, ctypes.c_float, ctypes.c_int32, vp, vp, sz, vp]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)
@@ -545,4 +584,279 @@ def nvfp4_linear(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
     _check("w4a8_nvfp4_linear", lib.w4a8_nvfp4_linear(
         x.data_ptr(), m, k, w_codes.data_ptr(), w_scales.data_ptr(), g_w.data_ptr(), n, out.data_ptr(),
         workspace.data_ptr(), workspace.numel(), _stream(stream)))
+    return out
+
+
+# ---------------------------------------------------------------- 8-bit integer path (include/w4a8_int8.h)
+
+def _here(t: torch.Tensor, dtype: torch.dtype, name: str, shape: tuple | None = None) -> torch.Tensor:
+    """A contiguous CUDA tensor of that type (and shape) on the current device."""
+    _cuda(t, dtype, name)
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{torch.cuda.current_device()}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def int8_quantize(x: torch.Tensor, rotate: bool = True, stream=None):
+    """x [R, K] (bf16 or fp32) -> (codes int8 [R, K], s fp32 [R]): one scale per
+    row (output channels of a weight, tokens of an activation)."""
+    lib = load_library()
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("x must be bf16 or fp32")
+    _here(x, x.dtype, "x")
+    r, k = x.shape
+    codes = torch.empty((r, k), dtype=torch.int8, device=x.device)
+    s = torch.empty(r, dtype=torch.float32, device=x.device)
+    _check("w4a8_int8_quantize", lib.w4a8_int8_quantize(
+        x.data_ptr(), int(x.dtype == torch.float32), r, k, int(rotate), codes.data_ptr(), s.data_ptr(),
+        _stream(stream)))
+    return codes, s
+
+
+def int8_linear_workspace(m: int, k: int, n: int, device) -> torch.Tensor:
+    """A zero-filled workspace for int8 layers of shape (M, K, N)."""
+    need = int(load_library().w4a8_int8_linear_workspace_bytes(m, k, n))
+    if need == 0:
+        raise W4A8Error("w4a8_int8_linear_workspace_bytes", 2)
+    return torch.zeros(need, dtype=torch.uint8, device=device)
+
+
+def int8_gemm(x_q: torch.Tensor, s_x: torch.Tensor, w_q: torch.Tensor, s_w: torch.Tensor,
+              workspace: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y [M, N] bf16 = s_x s_w (x_q [M, K] int8 times w_q [N, K]^T int8)."""
+    lib = load_library()
+    m, k = _here(x_q, torch.int8, "x_q").shape
+    n = w_q.shape[0]
+    _here(w_q, torch.int8, "w_q", (n, k))
+    _here(s_x, torch.float32, "s_x", (m,))
+    _here(s_w, torch.float32, "s_w", (n,))
+    if workspace is None:
+        workspace = int8_linear_workspace(m, k, n, x_q.device)
+    _here(workspace, torch.uint8, "workspace")
+    if out is None:
+        out = torch.empty((m, n), dtype=torch.bfloat16, device=x_q.device)
+    _here(out, torch.bfloat16, "out", (m, n))
+    _check("w4a8_int8_gemm", lib.w4a8_int8_gemm(
+        x_q.data_ptr(), s_x.data_ptr(), m, w_q.data_ptr(), s_w.data_ptr(), n, k, out.data_ptr(),
+        workspace.data_ptr(), workspace.numel(), _stream(stream)))
+    return out
+
+
+def int8_linear(x: torch.Tensor, w_q: torch.Tensor, s_w: torch.Tensor, rotate: bool = True,
+                workspace: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The int8 layer on bf16 x [M, K] against weights from int8_quantize(w, rotate)."""
+    lib = load_library()
+    m, k = _here(x, torch.bfloat16, "x").shape
+    n = w_q.shape[0]
+    _here(w_q, torch.int8, "w_q", (n, k))
+    _here(s_w, torch.float32, "s_w", (n,))
+    if workspace is None:
+        workspace = int8_linear_workspace(m, k, n, x.device)
+    _here(workspace, torch.uint8, "workspace")
+    if out is None:
+        out = torch.empty((m, n), dtype=torch.bfloat16, device=x.device)
+    _here(out, torch.bfloat16, "out", (m, n))
+    _check("w4a8_int8_linear", lib.w4a8_int8_linear(
+        x.data_ptr(), m, k, int(rotate), w_q.data_ptr(), s_w.data_ptr(), n, out.data_ptr(), workspace.data_ptr(),
+        workspace.numel(), _stream(stream)))
+    return out
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+                     original_length: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0, device="cuda"):
+    """(inv_freq fp64 [rot_dim / 2], attention factor) of a position rotation.
+    ``scaling``: None; "linear" (positions divided by ``factor``); "ntk" (the base
+    raised so that the slowest pair turns ``factor`` times slower); "yarn" (pairs
+    that turn less than ``beta_slow`` times over ``original_length`` positions are
+    slowed by ``factor``, those over ``beta_fast`` turns are kept, the ones between
+    are blended; attention factor 0.1 ln(factor) + 1)."""
+    import math
+    if rot_dim < 16 or rot_dim % 16:
+        raise ValueError("rot_dim must be a positive multiple of 16")
+    i = torch.arange(0, rot_dim, 2, dtype=torch.float64)
+    if scaling == "ntk":
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    inv = torch.as_tensor(float(base), dtype=torch.float64) ** (-i / rot_dim)
+    attention = 1.0
+    if scaling == "linear":
+        inv = inv / factor
+    elif scaling == "yarn":
+        if original_length <= 0:
+            raise ValueError("yarn needs original_length")
+        turns = original_length * inv / (2 * math.pi)
+        pair = lambda t: rot_dim * math.log(original_length / (t * 2 * math.pi)) / (2 * math.log(base))
+        lo, hi = max(math.floor(pair(beta_fast)), 0), min(math.ceil(pair(beta_slow)), rot_dim - 1)
+        blend = ((torch.arange(turns.numel(), dtype=torch.float64) - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+        inv = inv * (1 - blend) + inv / factor * blend
+        attention = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
+    elif scaling not in (None, "ntk"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return inv.to(device), attention
+
+
+def _heads(t: torch.Tensor | None, name: str, tokens: int | None = None, dim: int | None = None) -> Heads:
+    """bf16 [tokens, heads, D] with contiguous D -> w4a8_heads."""
+    if t is None:
+        return Heads(None, 0, 0, 0)
+    if not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 3:
+        raise ValueError(f"{name} must be a bf16 CUDA tensor [tokens, heads, D]")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{torch.cuda.current_device()}")
+    if t.stride(2) != 1:
+        raise ValueError(f"{name}: the values of a head must be contiguous")
+    if (tokens is not None and t.shape[0] != tokens) or (dim is not None and t.shape[2] != dim):
+        raise ValueError(f"{name} must be [{tokens}, heads, {dim}], got {tuple(t.shape)}")
+    # a dimension of one row has no stride of its own
+    token = t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    head = t.stride(1) if t.shape[1] > 1 else t.shape[2]
+    return Heads(t.data_ptr(), token, head, t.shape[1])
+
+
+def _rope(inv_freq, interleaved, factor) -> Rope:
+    if inv_freq is None:
+        return Rope(None, 0, 0, 1.0)
+    if inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be [rot_dim / 2]")
+    _here(inv_freq, torch.float64, "inv_freq")
+    return Rope(inv_freq.data_ptr(), 2 * inv_freq.numel(), int(interleaved), float(factor))
+
+
+def _ptr(t, dtype, name, shape):
+    return None if t is None else _here(t, dtype, name, shape).data_ptr()
+
+
+def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, positions: torch.Tensor | None = None,
+                 q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                 inv_freq: torch.Tensor | None = None, interleaved: bool = False, rope_factor: float = 1.0,
+                 q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None, stream=None):
+    """RMS norm of every head of q [T, Hq, D] and k [T, Hk, D] (a weight of None
+    leaves the norm out) and the rotation by ``positions`` [T] int32 and
+    ``inv_freq`` (rope_frequencies; None: no rotation).  Returns (q_out, k_out)."""
+    lib = load_library()
+    some = q if q is not None else k
+    if some is None:
+        raise ValueError("q or k is needed")
+    t, d = some.shape[0], some.shape[2]
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    if k is not None and k_out is None:
+        k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=k.device)
+    q_out, k_out = (q_out if q is not None else None), (k_out if k is not None else None)
+    qs, ks = _heads(q, "q", t, d), _heads(k, "k", t, d)
+    qo, ko = _heads(q_out, "q_out", t, d), _heads(k_out, "k_out", t, d)
+    rope = _rope(inv_freq, interleaved, rope_factor)
+    _check("w4a8_qk_norm_rope", lib.w4a8_qk_norm_rope(
+        ctypes.byref(qs), ctypes.byref(ks), t, d, _ptr(q_weight, torch.float32, "q_weight", (d,)),
+        _ptr(k_weight, torch.float32, "k_weight", (d,)), float(eps), _ptr(positions, torch.int32, "positions", (t,)),
+        ctypes.byref(rope), ctypes.byref(qo), ctypes.byref(ko), _stream(stream)))
+    return q_out, k_out
+
+
+class KvCache:
+    """An int8 paged cache: codes int8 [pages, kv_heads, page, D] and scales
+    fp32 [pages, kv_heads] for K and V (w4a8_kv_cache)."""
+
+    def __init__(self, pages: int, kv_heads: int, page: int, head_dim: int, device="cuda"):
+        shape = (pages, kv_heads, page, head_dim)
+        self._set(torch.zeros(shape, dtype=torch.int8, device=device), torch.zeros(shape, dtype=torch.int8, device=device),
+                  torch.zeros(shape[:2], dtype=torch.float32, device=device),
+                  torch.zeros(shape[:2], dtype=torch.float32, device=device))
+
+    @classmethod
+    def of(cls, k_codes: torch.Tensor, v_codes: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor) -> "KvCache":
+        """A cache on tensors that the caller holds."""
+        self = cls.__new__(cls)
+        self._set(k_codes, v_codes, k_scales, v_scales)
+        return self
+
+    def _set(self, k_codes, v_codes, k_scales, v_scales):
+        if k_codes.dim() != 4:
+            raise ValueError("codes must be [pages, kv_heads, page, D]")
+        shape = tuple(k_codes.shape)
+        _here(k_codes, torch.int8, "k_codes")
+        _here(v_codes, torch.int8, "v_codes", shape)
+        _here(k_scales, torch.float32, "k_scales", shape[:2])
+        _here(v_scales, torch.float32, "v_scales", shape[:2])
+        self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
+        self.pages, self.kv_heads, self.page, self.head_dim = shape
+        self.desc = CacheDesc(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), *shape)
+
+
+def _batch(block_table: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor, tokens: int) -> BatchDesc:
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [batch, pages]")
+    b, width = _here(block_table, torch.int32, "block_table").shape
+    _here(q_start, torch.int32, "q_start", (b + 1,))
+    _here(kv_len, torch.int32, "kv_len", (b,))
+    return BatchDesc(block_table.data_ptr(), width, q_start.data_ptr(), kv_len.data_ptr(), b, tokens)
+
+
+def kv_update(cache: KvCache, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor, q_start: torch.Tensor,
+              kv_len: torch.Tensor, q: torch.Tensor | None = None, positions: torch.Tensor | None = None,
+              q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+              inv_freq: torch.Tensor | None = None, interleaved: bool = False, rope_factor: float = 1.0,
+              q_out: torch.Tensor | None = None, stream=None):
+    """Write new tokens' k, v [T, kv_heads, D] into the cache (k normed and
+    rotated on the way), and norm and rotate q [T, Hq, D] in the same launch.
+    Sequence b's rows are q_start[b] .. q_start[b + 1], the last of its
+    kv_len[b] tokens; positions None: the places in the sequences.  Returns
+    q_out (None without q)."""
+    lib = load_library()
+    t, d = k.shape[0], cache.head_dim
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    q_out = q_out if q is not None else None
+    ks, vs = _heads(k, "k", t, d), _heads(v, "v", t, d)
+    qs, qo = _heads(q, "q", t, d), _heads(q_out, "q_out", t, d)
+    batch = _batch(block_table, q_start, kv_len, t)
+    rope = _rope(inv_freq, interleaved, rope_factor)
+    _check("w4a8_kv_update", lib.w4a8_kv_update(
+        ctypes.byref(cache.desc), ctypes.byref(batch), ctypes.byref(ks), ctypes.byref(vs), ctypes.byref(qs),
+        _ptr(q_weight, torch.float32, "q_weight", (d,)), _ptr(k_weight, torch.float32, "k_weight", (d,)), float(eps),
+        _ptr(positions, torch.int32, "positions", (t,)), ctypes.byref(rope), ctypes.byref(qo), _stream(stream)))
+    return q_out
+
+
+def kv_dequant(cache: KvCache, ids: torch.Tensor, stream=None):
+    """Pages ``ids`` [n] int32 -> (k, v) bf16 [n, kv_heads, page, D]."""
+    lib = load_library()
+    _here(ids, torch.int32, "ids", (ids.numel(),))
+    shape = (ids.numel(), cache.kv_heads, cache.page, cache.head_dim)
+    k = torch.empty(shape, dtype=torch.bfloat16, device=ids.device)
+    v = torch.empty(shape, dtype=torch.bfloat16, device=ids.device)
+    _check("w4a8_kv_dequant", lib.w4a8_kv_dequant(ctypes.byref(cache.desc), ids.data_ptr(), shape[0], k.data_ptr(),
+                                                  v.data_ptr(), _stream(stream)))
+    return k, v
+
+
+def kv_attention_workspace(tokens: int, q_heads: int, kv_heads: int, head_dim: int, device) -> torch.Tensor:
+    """A zero-filled workspace for kv_attention."""
+    need = int(load_library().w4a8_kv_attention_workspace_bytes(tokens, q_heads, kv_heads, head_dim))
+    if need == 0:
+        raise W4A8Error("w4a8_kv_attention_workspace_bytes", 2)
+    return torch.zeros(need, dtype=torch.uint8, device=device)
+
+
+def kv_attention(q: torch.Tensor, cache: KvCache, block_table: torch.Tensor, q_start: torch.Tensor,
+                 kv_len: torch.Tensor, scale: float | None = None, window: int = 0,
+                 workspace: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Causal attention of q [T, Hq, D] (already normed and rotated) over the
+    int8 cache that holds the same tokens; ``scale`` defaults to D ** -0.5,
+    ``window`` > 0 keeps the last so many positions.  Rows behind the last
+    sequence are left as they were."""
+    lib = load_library()
+    t, hq = q.shape[0], q.shape[1]
+    d = cache.head_dim
+    if workspace is None:
+        workspace = kv_attention_workspace(t, hq, cache.kv_heads, d, q.device)
+    _here(workspace, torch.uint8, "workspace")
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    qs, os_ = _heads(q, "q", t, d), _heads(out, "out", t, d)
+    batch = _batch(block_table, q_start, kv_len, t)
+    _check("w4a8_kv_attention", lib.w4a8_kv_attention(
+        ctypes.byref(qs), ctypes.byref(cache.desc), ctypes.byref(batch), float(d ** -0.5 if scale is None else scale),
+        int(window), ctypes.byref(os_), workspace.data_ptr(), workspace.numel(), _stream(stream)))
     return out

@@ -27,8 +27,8 @@ def nvcc() -> str:
 
 def sources() -> list[str]:
     d = os.path.join(PKG, "csrc")
-    return [os.path.join(d, f) for f in sorted(os.listdir(d)) if f.endswith((".cu", ".cuh"))] + [
-        os.path.join(ROOT, "include", "w4a8.h")]
+    return [os.path.join(d, f) for f in sorted(os.listdir(d)) if f.endswith((".cu", ".cuh", ".h"))] + [
+        os.path.join(ROOT, "include", f) for f in ("w4a8.h", "w4a8_int8.h")]
 
 
 def build(force: bool = False, verbose: bool = False) -> str:

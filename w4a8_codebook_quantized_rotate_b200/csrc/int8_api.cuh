@@ -1,0 +1,376 @@
+// C ABI of the 8-bit integer path (include/w4a8_int8.h): argument checks and
+// launches.  Part of the library's single translation unit (w4a8_api.cu),
+// whose per-device state and launch helpers it uses.
+#pragma once
+
+namespace w4a8 {
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// ------------------------------------------------------------------ int8 layer
+
+bool q8_rows_ok(int64_t R) { return R > 0 && R <= (int64_t(1) << 24); }
+bool q8_k_ok(int64_t K, int rotate) { return K > 0 && K % 16 == 0 && K <= kMaxK && (!rotate || K % kRotBlock == 0); }
+bool q8_shape_ok(int64_t M, int64_t N, int64_t K, int rotate) {
+  return M > 0 && M <= kMaxTokens && q8_rows_ok(N) && q8_k_ok(K, rotate);
+}
+
+struct Q8Plan {
+  int nt;                               // token tile
+  long long tiles;
+  size_t off_part, off_codes, off_s, total;
+};
+
+constexpr size_t kQ8ZeroBytes = 4096;  // the arrival counters
+static_assert(kQ8MaxCtas * 4 * 4 <= kQ8ZeroBytes, "counters fit");
+
+Q8Plan q8_plan(int64_t M, int64_t K, int64_t N) {
+  Q8Plan P{};
+  P.nt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
+  P.tiles = ((N + kQ8Rows - 1) / kQ8Rows) * ((M + P.nt - 1) / P.nt);
+  P.off_part = kQ8ZeroBytes;
+  P.off_codes = P.off_part + size_t(kQ8MaxCtas) * 2 * P.nt * kQ8Rows * 4;
+  P.off_s = round_up(P.off_codes + size_t(M) * K, 256);
+  P.total = P.off_s + round_up(size_t(M) * 4, 256);
+  return P;
+}
+
+cudaError_t q8_quantize(const void* x, int f32, int64_t R, int64_t K, int rotate, int8_t* codes, float* s,
+                        cudaStream_t st) {
+  const dim3 grid{unsigned(R)}, block{unsigned(q8_threads(R, K))};
+  return f32 ? launch_pdl(int8_quant_kernel<true>, grid, block, size_t(K) * 4, st, x, int(K), int(rotate), codes, s)
+             : launch_pdl(int8_quant_kernel<false>, grid, block, size_t(K) * 4, st, x, int(K), int(rotate), codes, s);
+}
+
+// 2-D map of rows of bytes, box [box_cols x box_rows].
+bool byte_map(CUtensorMap* m, const void* data, int64_t cols, int64_t rows, uint32_t box_cols, uint32_t box_rows,
+              CUtensorMapSwizzle swizzle) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dim[2] = {cuuint64_t(cols), cuuint64_t(rows)};
+  const cuuint64_t stride[1] = {cuuint64_t(cols)};
+  const cuuint32_t box[2] = {box_cols, box_rows};
+  const cuuint32_t step[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(data), dim, stride, box, step,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+w4a8_status q8_gemm(const int8_t* x_q, const float* s_x, int64_t M, const int8_t* w_q, const float* s_w, int64_t N,
+                    int64_t K, uint16_t* y, uint8_t* ws, const DeviceState* d, cudaStream_t st) {
+  const Q8Plan P = q8_plan(M, K, N);
+  CUtensorMap tw, tx;
+  if (!byte_map(&tw, w_q, K, N, kQ8BK, kQ8Rows, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !byte_map(&tx, x_q, K, M, kQ8BK, uint32_t(P.nt), CU_TENSOR_MAP_SWIZZLE_128B))
+    return W4A8_ERR_CUDA;
+  Q8Params p;
+  p.s_x = s_x;
+  p.s_w = s_w;
+  p.y = y;
+  p.counters = reinterpret_cast<unsigned*>(ws);
+  p.part = reinterpret_cast<int*>(ws + P.off_part);
+  p.err = d->err;
+  p.M = int(M);
+  p.N = int(N);
+  p.K = int(K);
+  p.KB = int((K + kQ8BK - 1) / kQ8BK);
+  p.TM = int((M + P.nt - 1) / P.nt);
+  p.items = P.tiles * p.KB;
+  const int ctas = std::min(d->sms, kQ8MaxCtas);
+  // Tiles cut between CTAs cost a partial tile's write and read; with many
+  // tiles to a CTA an uneven last round costs less.
+  p.whole = P.tiles >= 8ll * ctas;
+  p.G = int(std::min<long long>(ctas, p.items));
+  const dim3 grid{unsigned(p.G)}, block{kQ8Threads};
+  cudaError_t e;
+  switch (P.nt) {
+    case 16: e = launch_pdl(int8_gemm_kernel<16>, grid, block, Q8Cfg<16>::kSmem, st, tw, tx, p); break;
+    case 32: e = launch_pdl(int8_gemm_kernel<32>, grid, block, Q8Cfg<32>::kSmem, st, tw, tx, p); break;
+    case 64: e = launch_pdl(int8_gemm_kernel<64>, grid, block, Q8Cfg<64>::kSmem, st, tw, tx, p); break;
+    case 128: e = launch_pdl(int8_gemm_kernel<128>, grid, block, Q8Cfg<128>::kSmem, st, tw, tx, p); break;
+    default: e = launch_pdl(int8_gemm_kernel<256>, grid, block, Q8Cfg<256>::kSmem, st, tw, tx, p); break;
+  }
+  return e == cudaSuccess ? W4A8_OK : W4A8_ERR_CUDA;
+}
+
+// ------------------------------------------------------------------ heads and cache
+
+bool head_dim_ok(int64_t D) { return D == 64 || D == 128 || D == 256; }
+
+w4a8_status heads_ok(const w4a8_heads& h, int64_t D) {
+  if (h.heads < 1 || h.heads > 65536) return W4A8_ERR_SHAPE;
+  if (h.token_stride < 0 || h.head_stride < 0 || h.token_stride % 8 || h.head_stride % 8 || h.token_stride > (int64_t(1) << 40) ||
+      h.head_stride > (int64_t(1) << 40) || (h.heads > 1 && h.head_stride < D))
+    return W4A8_ERR_SHAPE;
+  return aligned16(h.data) ? W4A8_OK : W4A8_ERR_ALIGN;
+}
+HeadRows head_rows(const w4a8_heads* h) {
+  if (!h || !h->data) return HeadRows{nullptr, 0, 0, 0};
+  return HeadRows{h->data, h->token_stride, h->head_stride, h->heads};
+}
+
+w4a8_status rope_ok(const w4a8_rope* r, int64_t D) {
+  if (!r || !r->inv_freq) return W4A8_OK;
+  if (r->rot_dim < 16 || r->rot_dim % 16 || r->rot_dim > D) return W4A8_ERR_SHAPE;
+  return (reinterpret_cast<uintptr_t>(r->inv_freq) & 7u) ? W4A8_ERR_ALIGN : W4A8_OK;
+}
+RopeParams rope_params(const w4a8_rope* r) {
+  if (!r || !r->inv_freq) return RopeParams{nullptr, 0, 0, 1.f};
+  return RopeParams{r->inv_freq, r->rot_dim, r->interleaved != 0, r->factor};
+}
+
+int page_shift_of(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : page == 128 ? 7 : -1; }
+
+w4a8_status cache_ok(const w4a8_kv_cache* c) {
+  if (!c || !c->k_codes || !c->v_codes || !c->k_scales || !c->v_scales) return W4A8_ERR_NULL;
+  if (!head_dim_ok(c->head_dim) || page_shift_of(c->page) < 0 || c->kv_heads < 1 || c->kv_heads > 65536 || c->pages < 1 ||
+      c->pages > (int64_t(1) << 31) || c->pages * c->kv_heads * c->page >= (int64_t(1) << 31))
+    return W4A8_ERR_SHAPE;
+  if (!aligned16(c->k_codes) || !aligned16(c->v_codes) || !aligned16(c->k_scales) || !aligned16(c->v_scales))
+    return W4A8_ERR_ALIGN;
+  return W4A8_OK;
+}
+KvCacheParams cache_params(const w4a8_kv_cache* c) {
+  KvCacheParams p;
+  p.codes[0] = c->k_codes;
+  p.codes[1] = c->v_codes;
+  p.scales[0] = c->k_scales;
+  p.scales[1] = c->v_scales;
+  p.pages = c->pages;
+  p.kv_heads = c->kv_heads;
+  p.page_shift = page_shift_of(c->page);
+  p.D = c->head_dim;
+  return p;
+}
+
+w4a8_status batch_ok(const w4a8_kv_batch* b, int page) {
+  if (!b || !b->table || !b->q_start || !b->kv_len) return W4A8_ERR_NULL;
+  if (b->batch < 1 || b->batch > 65536 || b->tokens < 1 || b->tokens > (int64_t(1) << 24) || b->table_stride < 1 ||
+      b->table_stride * page >= (int64_t(1) << 31))
+    return W4A8_ERR_SHAPE;
+  if (!aligned4(b->table) || !aligned4(b->q_start) || !aligned4(b->kv_len)) return W4A8_ERR_ALIGN;
+  return W4A8_OK;
+}
+KvBatchParams batch_params(const w4a8_kv_batch* b) {
+  return KvBatchParams{b->table, b->table_stride, b->q_start, b->kv_len, int(b->batch), int(b->tokens)};
+}
+
+bool ka_shape_ok(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t D) {
+  return tokens >= 1 && tokens <= (int64_t(1) << 24) && head_dim_ok(D) && kv_heads >= 1 && q_heads >= 1 &&
+         q_heads <= 65536 && q_heads % kv_heads == 0 && q_heads / kv_heads <= 128 &&
+         tokens * (q_heads / kv_heads) < (int64_t(1) << 31);
+}
+
+constexpr size_t kKaZeroBytes = 1024;
+static_assert(kKaMaxCtas * 4 <= kKaZeroBytes, "counters fit");
+
+template <int D>
+cudaError_t ka_launch(const KaParams& p, const w4a8_kv_cache* c, int ctas, cudaStream_t st) {
+  using C = KaCfg<D>;
+  const int box = std::min(C::TK, int(c->page));
+  const auto swizzle = D < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+  const int64_t rows = c->pages * c->kv_heads * c->page;
+  CUtensorMap tk, tv;
+  if (!byte_map(&tk, c->k_codes, D, rows, C::kRowBytes, uint32_t(box), swizzle) ||
+      !byte_map(&tv, c->v_codes, D, rows, C::kRowBytes, uint32_t(box), swizzle))
+    return cudaErrorUnknown;
+  KaParams q = p;
+  q.box_shift = page_shift_of(box);
+  return launch_pdl(kv_attention_kernel<D>, dim3(ctas), dim3(kKaThreads), C::kSmem, st, tk, tv, q);
+}
+
+// Shared-memory opt-ins of this file's kernels, once per device.
+bool int8_allow_smem() {
+  return allow_smem(int8_quant_kernel<false>, size_t(kMaxK) * 4) == cudaSuccess &&
+         allow_smem(int8_quant_kernel<true>, size_t(kMaxK) * 4) == cudaSuccess &&
+         allow_smem(int8_gemm_kernel<16>, Q8Cfg<16>::kSmem) == cudaSuccess &&
+         allow_smem(int8_gemm_kernel<32>, Q8Cfg<32>::kSmem) == cudaSuccess &&
+         allow_smem(int8_gemm_kernel<64>, Q8Cfg<64>::kSmem) == cudaSuccess &&
+         allow_smem(int8_gemm_kernel<128>, Q8Cfg<128>::kSmem) == cudaSuccess &&
+         allow_smem(int8_gemm_kernel<256>, Q8Cfg<256>::kSmem) == cudaSuccess &&
+         allow_smem(kv_update_kernel<64>, 128 * 64 * 4) == cudaSuccess &&
+         allow_smem(kv_update_kernel<128>, 128 * 128 * 4) == cudaSuccess &&
+         allow_smem(kv_update_kernel<256>, 128 * 256 * 4) == cudaSuccess &&
+         allow_smem(kv_attention_kernel<64>, KaCfg<64>::kSmem) == cudaSuccess &&
+         allow_smem(kv_attention_kernel<128>, KaCfg<128>::kSmem) == cudaSuccess &&
+         allow_smem(kv_attention_kernel<256>, KaCfg<256>::kSmem) == cudaSuccess;
+}
+
+// device_state, and the opt-ins above the first time on a device.
+w4a8_status int8_state(DeviceState** out) {
+  if (w4a8_status st = device_state(out); st != W4A8_OK) return st;
+  std::lock_guard<std::mutex> lock(g_mutex);
+  if (!(*out)->int8_ready) {
+    if (!int8_allow_smem()) return W4A8_ERR_CUDA;
+    (*out)->int8_ready = true;
+  }
+  return W4A8_OK;
+}
+
+w4a8_status status_of(cudaError_t e) { return e == cudaSuccess ? W4A8_OK : W4A8_ERR_CUDA; }
+
+}  // namespace
+}  // namespace w4a8
+
+extern "C" {
+
+w4a8_status w4a8_int8_quantize(const void* x, int32_t x_is_f32, int64_t R, int64_t K, int32_t rotate, int8_t* codes,
+                               float* s, void* stream) {
+  if (!x || !codes || !s) return W4A8_ERR_NULL;
+  if (!q8_rows_ok(R) || !q8_k_ok(K, rotate)) return W4A8_ERR_SHAPE;
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(s)) return W4A8_ERR_ALIGN;
+  DeviceState* d = nullptr;
+  if (w4a8_status st = int8_state(&d); st != W4A8_OK) return st;
+  return status_of(q8_quantize(x, x_is_f32, R, K, rotate, codes, s, static_cast<cudaStream_t>(stream)));
+}
+
+size_t w4a8_int8_linear_workspace_bytes(int64_t M, int64_t K, int64_t N) {
+  return q8_shape_ok(M, N, K, 0) ? q8_plan(M, K, N).total : 0;
+}
+
+w4a8_status w4a8_int8_gemm(const int8_t* x_q, const float* s_x, int64_t M, const int8_t* w_q, const float* s_w,
+                           int64_t N, int64_t K, uint16_t* y, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!x_q || !s_x || !w_q || !s_w || !y || !workspace) return W4A8_ERR_NULL;
+  if (!q8_shape_ok(M, N, K, 0)) return W4A8_ERR_SHAPE;
+  if (!aligned16(x_q) || !aligned16(s_x) || !aligned16(w_q) || !aligned16(s_w) || !aligned16(y) || !aligned16(workspace))
+    return W4A8_ERR_ALIGN;
+  if (workspace_bytes < q8_plan(M, K, N).total) return W4A8_ERR_WORKSPACE;
+  DeviceState* d = nullptr;
+  if (w4a8_status st = int8_state(&d); st != W4A8_OK) return st;
+  return q8_gemm(x_q, s_x, M, w_q, s_w, N, K, y, static_cast<uint8_t*>(workspace), d, static_cast<cudaStream_t>(stream));
+}
+
+w4a8_status w4a8_int8_linear(const uint16_t* x, int64_t M, int64_t K, int32_t rotate, const int8_t* w_q,
+                             const float* s_w, int64_t N, uint16_t* y, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  if (!x || !w_q || !s_w || !y || !workspace) return W4A8_ERR_NULL;
+  if (!q8_shape_ok(M, N, K, rotate)) return W4A8_ERR_SHAPE;
+  if (!aligned16(x) || !aligned16(w_q) || !aligned16(s_w) || !aligned16(y) || !aligned16(workspace)) return W4A8_ERR_ALIGN;
+  const Q8Plan P = q8_plan(M, K, N);
+  if (workspace_bytes < P.total) return W4A8_ERR_WORKSPACE;
+  DeviceState* d = nullptr;
+  if (w4a8_status st = int8_state(&d); st != W4A8_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  int8_t* codes = reinterpret_cast<int8_t*>(ws + P.off_codes);
+  float* s_x = reinterpret_cast<float*>(ws + P.off_s);
+  if (q8_quantize(x, 0, M, K, rotate, codes, s_x, s) != cudaSuccess) return W4A8_ERR_CUDA;
+  return q8_gemm(codes, s_x, M, w_q, s_w, N, K, y, ws, d, s);
+}
+
+w4a8_status w4a8_qk_norm_rope(const w4a8_heads* q, const w4a8_heads* k, int64_t T, int32_t D, const float* q_weight,
+                              const float* k_weight, float eps, const int32_t* positions, const w4a8_rope* rope,
+                              const w4a8_heads* q_out, const w4a8_heads* k_out, void* stream) {
+  const bool has_q = q && q->data, has_k = k && k->data;
+  if ((!has_q && !has_k) || (has_q && (!q_out || !q_out->data)) || (has_k && (!k_out || !k_out->data))) return W4A8_ERR_NULL;
+  if (rope && rope->inv_freq && !positions) return W4A8_ERR_NULL;
+  if (T < 1 || T > (int64_t(1) << 24) || !head_dim_ok(D)) return W4A8_ERR_SHAPE;
+  for (const w4a8_heads* h : {has_q ? q : nullptr, has_q ? q_out : nullptr, has_k ? k : nullptr, has_k ? k_out : nullptr})
+    if (h)
+      if (w4a8_status st = heads_ok(*h, D); st != W4A8_OK) return st;
+  if ((has_q && q->heads != q_out->heads) || (has_k && k->heads != k_out->heads)) return W4A8_ERR_SHAPE;
+  if (w4a8_status st = rope_ok(rope, D); st != W4A8_OK) return st;
+  if ((q_weight && !aligned16(q_weight)) || (k_weight && !aligned16(k_weight)) || !aligned4(positions)) return W4A8_ERR_ALIGN;
+  DeviceState* d = nullptr;
+  if (w4a8_status st = int8_state(&d); st != W4A8_OK) return st;
+  QkParams p{head_rows(q), head_rows(k), head_rows(q_out), head_rows(k_out), q_weight, k_weight, eps,
+             rope_params(rope), positions, int(T)};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const dim3 grid{unsigned(T)}, block{kQkThreads};
+  return status_of(D == 64    ? launch_pdl(qk_norm_rope_kernel<64>, grid, block, 0, s, p)
+                   : D == 128 ? launch_pdl(qk_norm_rope_kernel<128>, grid, block, 0, s, p)
+                              : launch_pdl(qk_norm_rope_kernel<256>, grid, block, 0, s, p));
+}
+
+w4a8_status w4a8_kv_update(const w4a8_kv_cache* cache, const w4a8_kv_batch* batch, const w4a8_heads* k,
+                           const w4a8_heads* v, const w4a8_heads* q, const float* q_weight, const float* k_weight,
+                           float eps, const int32_t* positions, const w4a8_rope* rope, const w4a8_heads* q_out,
+                           void* stream) {
+  const bool has_q = q && q->data;
+  if (!k || !k->data || !v || !v->data || (has_q && (!q_out || !q_out->data))) return W4A8_ERR_NULL;
+  if (w4a8_status st = cache_ok(cache); st != W4A8_OK) return st;
+  if (w4a8_status st = batch_ok(batch, cache->page); st != W4A8_OK) return st;
+  const int D = cache->head_dim;
+  for (const w4a8_heads* h : {k, v, has_q ? q : nullptr, has_q ? q_out : nullptr})
+    if (h)
+      if (w4a8_status st = heads_ok(*h, D); st != W4A8_OK) return st;
+  if (k->heads != cache->kv_heads || v->heads != cache->kv_heads || (has_q && q->heads != q_out->heads)) return W4A8_ERR_SHAPE;
+  if (w4a8_status st = rope_ok(rope, D); st != W4A8_OK) return st;
+  if ((q_weight && !aligned16(q_weight)) || (k_weight && !aligned16(k_weight)) || !aligned4(positions)) return W4A8_ERR_ALIGN;
+  const int64_t units = kv_touched_bound(batch->tokens, batch->batch, cache->page);
+  const int64_t page_ctas = units * cache->kv_heads * 2;
+  if (page_ctas + batch->tokens >= (int64_t(1) << 31)) return W4A8_ERR_SHAPE;
+  DeviceState* d = nullptr;
+  if (w4a8_status st = int8_state(&d); st != W4A8_OK) return st;
+  KvUpdateParams p;
+  p.qk = QkParams{head_rows(q), head_rows(k), head_rows(q_out), HeadRows{nullptr, 0, 0, 0}, q_weight, k_weight, eps,
+                  rope_params(rope), positions, int(batch->tokens)};
+  p.v = head_rows(v);
+  p.cache = cache_params(cache);
+  p.batch = batch_params(batch);
+  p.page_ctas = int(page_ctas);
+  p.err = d->err;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const dim3 grid{unsigned(page_ctas + (has_q ? batch->tokens : 0))}, block{kKvThreads};
+  const size_t smem = size_t(cache->page) * D * 4;
+  return status_of(D == 64    ? launch_pdl(kv_update_kernel<64>, grid, block, smem, s, p)
+                   : D == 128 ? launch_pdl(kv_update_kernel<128>, grid, block, smem, s, p)
+                              : launch_pdl(kv_update_kernel<256>, grid, block, smem, s, p));
+}
+
+w4a8_status w4a8_kv_dequant(const w4a8_kv_cache* cache, const int32_t* ids, int64_t n, uint16_t* k_out, uint16_t* v_out,
+                            void* stream) {
+  if (!ids || !k_out || !v_out) return W4A8_ERR_NULL;
+  if (w4a8_status st = cache_ok(cache); st != W4A8_OK) return st;
+  if (n < 1 || n > (int64_t(1) << 31)) return W4A8_ERR_SHAPE;
+  const int64_t chunks = n * (int64_t(cache->kv_heads) * cache->page * (cache->head_dim / 16));
+  if (chunks >= (int64_t(1) << 37)) return W4A8_ERR_SHAPE;
+  if (!aligned4(ids) || !aligned16(k_out) || !aligned16(v_out)) return W4A8_ERR_ALIGN;
+  DeviceState* d = nullptr;
+  if (w4a8_status st = int8_state(&d); st != W4A8_OK) return st;
+  return status_of(launch_pdl(kv_dequant_kernel, dim3(unsigned((2 * chunks + 255) / 256)), dim3(256), 0,
+                              static_cast<cudaStream_t>(stream), cache_params(cache), ids, (long long)chunks, k_out, v_out,
+                              d->err));
+}
+
+size_t w4a8_kv_attention_workspace_bytes(int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
+  if (!ka_shape_ok(tokens, q_heads, kv_heads, head_dim)) return 0;
+  return kKaZeroBytes + size_t(kKaMaxCtas) * 2 * (size_t(kKaRows) * head_dim + 3 * kKaRows) * 4;
+}
+
+w4a8_status w4a8_kv_attention(const w4a8_heads* q, const w4a8_kv_cache* cache, const w4a8_kv_batch* batch, float scale,
+                              int32_t window, const w4a8_heads* out, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+  if (!q || !q->data || !out || !out->data || !workspace) return W4A8_ERR_NULL;
+  if (w4a8_status st = cache_ok(cache); st != W4A8_OK) return st;
+  if (w4a8_status st = batch_ok(batch, cache->page); st != W4A8_OK) return st;
+  const int D = cache->head_dim;
+  for (const w4a8_heads* h : {q, out})
+    if (w4a8_status st = heads_ok(*h, D); st != W4A8_OK) return st;
+  if (q->heads != out->heads || window < 0 || !ka_shape_ok(batch->tokens, q->heads, cache->kv_heads, D)) return W4A8_ERR_SHAPE;
+  if (!aligned16(workspace)) return W4A8_ERR_ALIGN;
+  if (workspace_bytes < w4a8_kv_attention_workspace_bytes(batch->tokens, q->heads, cache->kv_heads, D))
+    return W4A8_ERR_WORKSPACE;
+  DeviceState* d = nullptr;
+  if (w4a8_status st = int8_state(&d); st != W4A8_OK) return st;
+  KaParams p;
+  p.q = head_rows(q);
+  p.out = head_rows(out);
+  p.cache = cache_params(cache);
+  p.batch = batch_params(batch);
+  p.scale_log2 = scale * 1.44269504088896340736f;
+  p.window = window;
+  p.group = q->heads / cache->kv_heads;
+  p.box_shift = 0;
+  p.counters = static_cast<unsigned*>(workspace);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kKaZeroBytes);
+  p.err = d->err;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int ctas = std::min(d->sms, kKaMaxCtas);
+  return status_of(D == 64    ? ka_launch<64>(p, cache, ctas, s)
+                   : D == 128 ? ka_launch<128>(p, cache, ctas, s)
+                              : ka_launch<256>(p, cache, ctas, s));
+}
+
+}  // extern "C"

@@ -1,0 +1,734 @@
+// Attention of new tokens over the int8 paged cache, streaming kernel.
+//
+//   o_i = sum_j softmax_j(scale * ks[page j] * (q_i . k_j)) * vs[page j] * v_j
+//
+// over the positions j <= i of the sequence (and j > i - window), k_j and v_j
+// the int8 codes.  The codes are exact in fp16, so both products run on
+// fp16 operands with fp32 accumulation, and the page scales stay outside:
+// ks multiplies the scores, vs the probabilities.
+//   * q is taken to fp16 with a power of two per row (exact: bf16 has fewer
+//     significant bits, the power keeps its range).
+//   * p vs is taken to fp16 relative to the row's largest p vs so far, at
+//     2^15, with a running maximum of its own (page scales of one head may
+//     be far apart, and the largest p need not carry the largest share of
+//     the result), so what fp16 drops is below 2^-40 of the largest share.
+//     p itself is summed in fp32 under the usual running maximum.
+//
+// The cache is read once, so at decode sizes its bytes bound the kernel
+// (6.5 TB/s: 23 bytes a clock and SM, against which the fp16 expansion of
+// the codes costs about one instruction per byte and 32 lanes).  A row tile
+// is 16 rows, the query heads of one key head (and neighbouring new tokens,
+// if the group is smaller); work is a list of items of 8 warps x TK keys,
+// [sequence][key head][row tile][item], of which every CTA takes an equal
+// contiguous share (one CTA per SM), so ragged batches and single long
+// contexts fill the GPU alike.  Each warp keeps its own running maximum, sum
+// and accumulator over its keys; warps join through shared memory at the end
+// of a row tile, CTAs that share a row tile through partial results that the
+// last of them to arrive adds in CTA order (the result does not depend on
+// the order of arrival).
+//
+// A producer warp keeps a ring of TMA tiles per consumer warp full (8 lanes,
+// one per consumer), with the block table and the page scales of the next
+// tiles fetched ahead.  K fragments are 16-byte reads of a token's codes in
+// the order d = 64 c + 16 t + 4 s + e (q's fragments use the same order); V
+// fragments come from ldmatrix.trans on code pairs, whose even and odd codes
+// make two output tiles.  Tokens of an 8-token group are taken in the order
+// tau, which keeps the swizzled K reads free of bank conflicts.
+#pragma once
+
+#include <cuda.h>
+
+#include "common.cuh"
+#include "kv_cache.cuh"
+#include "kv_index.h"
+#include "qk_rope.cuh"
+
+namespace w4a8 {
+
+constexpr int kKaWarps = 8;                      // consumer warps
+constexpr int kKaThreads = (kKaWarps + 1) * 32;  // and a producer warp
+constexpr int kKaStages = 3;
+constexpr int kKaRows = 16;
+constexpr int kKaTileBytes = 4096;               // one warp's K (or V) tile
+constexpr int kKaMaxCtas = 160;
+
+template <int D>
+struct KaCfg {
+  static constexpr int TK = kKaTileBytes / D;  // keys of a warp's tile: 64, 32, 16
+  static constexpr int KG = TK / 16;           // groups of 16 keys
+  static constexpr int kItem = kKaWarps * TK;  // keys of an item
+  static constexpr int kSteps = D / 16;
+  static constexpr bool kQRegs = D <= 128;     // q fragments in registers
+  static constexpr uint32_t kRowBytes = D < 128 ? D : 128;  // bytes of a row in a TMA box
+  static constexpr int kColBlocks = D / int(kRowBytes);
+  static constexpr uint32_t kRing = kKaWarps * kKaStages * 2 * kKaTileBytes;
+  static constexpr uint32_t kJoin = kKaWarps * kKaRows * 32 * 4;  // 32 columns of every warp
+  static constexpr uint32_t kQ = kKaRows * D * 2;
+  static constexpr size_t kSmem = 1024 + kRing + kJoin + kQ + 4096;
+  static constexpr int kSlotFloats = kKaRows * D + 3 * kKaRows;
+};
+
+struct KaParams {
+  HeadRows q, out;
+  KvCacheParams cache;
+  KvBatchParams batch;
+  float scale_log2;  // softmax scale times log2(e)
+  int window;
+  int group;         // query heads of a key head
+  int box_shift;     // log2 of a TMA box's rows
+  float* part;       // [CTA][2][kSlotFloats]
+  unsigned* counters;  // [CTA]
+  unsigned* err;
+};
+
+struct KaShared {
+  uint64_t full[kKaWarps][kKaStages];
+  uint64_t empty[kKaWarps][kKaStages];
+  float scales[kKaWarps][kKaStages][3][4];  // ks, vs, log2(vs) of each group of 16 keys
+  float warp_m[kKaWarps][kKaRows];
+  float warp_l[kKaWarps][kKaRows];
+  float warp_v[kKaWarps][kKaRows];
+  float row_factor[kKaRows];
+  long long base;   // first item of sequence b0
+  long long total;  // items of the batch
+  int b0;
+  int last;         // this CTA joins the row tile's partial results
+  volatile int abort;
+};
+
+__device__ __forceinline__ bool ka_wait(uint64_t* bar, uint32_t parity, KaShared* sh, unsigned* err) {
+  for (uint32_t i = 0; i < (1u << 20); ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 1023u) == 1023u && sh->abort) return false;
+  }
+  sh->abort = 1;
+  record_error(err, kErrTimeout);
+  return false;
+}
+
+// A CTA's share of `total` items among the first min(ctas, total) CTAs.
+W4A8_HD long long ka_first_item(long long c, long long total, long long ctas) { return total * c / ctas; }
+W4A8_HD int ka_item_cta(long long i, long long total, long long ctas) {
+  return int(((i + 1) * ctas + total - 1) / total - 1);
+}
+
+// Row tiles of a sequence, and items of each (the same for all of them: a
+// tile skips the keys outside its own range).
+template <int D>
+__device__ __forceinline__ void ka_counts(const KvSeq& s, const KaParams& p, int& tiles, int& items) {
+  const KvRange r = kv_range(s, 0, s.q_len - 1, p.window);
+  const int lo = r.lo & ~(KaCfg<D>::TK - 1);
+  tiles = (s.q_len * p.group + kKaRows - 1) / kKaRows;
+  items = s.q_len == 0 ? 0 : (s.kv_len - lo + KaCfg<D>::kItem - 1) / KaCfg<D>::kItem;
+}
+
+// The row tile at the front of a CTA's range.
+struct KaSeg {
+  KvSeq s;
+  int b, head, tile;
+  int item0, item1, items;  // of the tile's `items`, this CTA has [item0, item1)
+  long long start;          // first item of the tile in the batch
+  int key0;                 // first key of its item 0
+  KvRange range;
+};
+
+template <int D>
+struct KaWalk {
+  long long pos, end, base;
+  int b, tiles, items;
+  KvSeq s;
+  __device__ __forceinline__ void load(const KaParams& p) {
+    s = kv_load_seq(p.batch, b, p.cache.page_shift);
+    ka_counts<D>(s, p, tiles, items);
+  }
+  __device__ __forceinline__ bool next(const KaParams& p, KaSeg& g) {
+    if (pos >= end) return false;
+    while (pos >= base + (long long)p.cache.kv_heads * tiles * items) {
+      base += (long long)p.cache.kv_heads * tiles * items;
+      ++b;
+      load(p);
+    }
+    const long long local = pos - base;
+    const long long unit = local / items;
+    g.s = s;
+    g.b = b;
+    g.items = items;
+    g.item0 = int(local - unit * items);
+    g.head = int(unit / tiles);
+    g.tile = int(unit - (long long)g.head * tiles);
+    g.start = base + unit * items;
+    const long long left = end - pos;
+    g.item1 = left < items - g.item0 ? g.item0 + int(left) : items;
+    g.key0 = kv_range(s, 0, s.q_len - 1, p.window).lo & ~(KaCfg<D>::TK - 1);
+    const int j0 = g.tile * kKaRows / p.group;
+    const int last_row = min(s.q_len * p.group, (g.tile + 1) * kKaRows) - 1;
+    g.range = kv_range(s, j0, last_row / p.group, p.window);
+    pos += g.item1 - g.item0;
+    return true;
+  }
+};
+
+__device__ __forceinline__ void ka_mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+      "%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Two int8 codes (already xor 0x80: code + 128) as fp16: the byte under the
+// high byte 0x64 is 1024 + code + 128, less 1152 (exact).
+__device__ __forceinline__ uint32_t ka_codes(uint32_t biased, uint32_t sel) {
+  const uint32_t w = prmt(biased, 0x64646464u, sel);
+  const uint32_t off = 0x64806480u;
+  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&w), *reinterpret_cast<const __half2*>(&off));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ void ka_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kKaWarps * 32) : "memory"); }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <int D>
+__device__ __forceinline__ uint32_t ka_tau(uint32_t i) {
+  return D < 128 ? i : (i >> 1) | ((i & 1u) << 2);
+}
+// Byte offset of 16-byte chunk c of row r in a swizzled tile.
+template <int D>
+__device__ __forceinline__ uint32_t ka_at(uint32_t r, uint32_t c) {
+  if constexpr (D < 128) return r * 64u + ((c ^ ((r >> 1) & 3u)) << 4);
+  return (c >> 3) * uint32_t(KaCfg<D>::TK * 128) + r * 128u + (((c & 7u) ^ (r & 7u)) << 4);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kKaThreads, 1)
+    kv_attention_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                        const KaParams p) {
+  using C = KaCfg<D>;
+  extern __shared__ __align__(1024) uint8_t ka_smem[];
+  const uint32_t ring = (smem_u32(ka_smem) + 1023u) & ~1023u;
+  uint8_t* after = ka_smem + (ring - smem_u32(ka_smem)) + C::kRing;
+  float* join = reinterpret_cast<float*>(after);
+  uint32_t* qf = reinterpret_cast<uint32_t*>(after + C::kJoin);  // [step][lane][4]
+  KaShared* sh = reinterpret_cast<KaShared*>(after + C::kJoin + C::kQ);
+  static_assert(sizeof(KaShared) <= 4096, "shared block");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  pdl_wait();
+  pdl_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int w = 0; w < kKaWarps; ++w)
+      for (int s = 0; s < kKaStages; ++s) {
+        mbar_init(&sh->full[w][s], 1);
+        mbar_init(&sh->empty[w][s], 1);
+      }
+    sh->abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0) {
+    // The batch's items, then the sequence that holds this CTA's first one.
+    long long total = 0;
+    for (int b0 = 0; b0 < p.batch.batch; b0 += 32) {
+      int tiles = 0, items = 0;
+      if (b0 + lane < p.batch.batch) {
+        const KvSeq s = kv_load_seq(p.batch, b0 + lane, p.cache.page_shift);
+        if (s.bad) record_error(p.err, kErrInput);
+        ka_counts<D>(s, p, tiles, items);
+      }
+      total += (long long)p.cache.kv_heads * tiles * items;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+    const long long ctas = total < gridDim.x ? total : gridDim.x;
+    const long long i0 = int(blockIdx.x) < ctas ? ka_first_item(blockIdx.x, total, ctas) : total;
+    long long before = 0, base = 0;
+    int at = -1;
+    for (int b0 = 0; b0 < p.batch.batch && at < 0 && i0 < total; b0 += 32) {
+      int tiles = 0, items = 0;
+      if (b0 + lane < p.batch.batch)
+        ka_counts<D>(kv_load_seq(p.batch, b0 + lane, p.cache.page_shift), p, tiles, items);
+      const long long own = (long long)p.cache.kv_heads * tiles * items;
+      long long sum = own;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, sum, off);
+        if (lane >= off) sum += o;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, before + sum > i0);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        at = b0 + l;
+        base = before + __shfl_sync(0xffffffffu, sum - own, l);
+      }
+      before += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (lane == 0) {
+      sh->total = total;
+      sh->b0 = at;
+      sh->base = base;
+    }
+  }
+  __syncthreads();
+  const long long total = sh->total;
+  const long long ctas = total < gridDim.x ? total : gridDim.x;
+  if (int(blockIdx.x) >= ctas) return;
+  const long long i0 = ka_first_item(blockIdx.x, total, ctas);
+  KaWalk<D> walk;
+  walk.pos = i0;
+  walk.end = ka_first_item(blockIdx.x + 1, total, ctas);
+  walk.base = sh->base;
+  walk.b = sh->b0;
+  walk.load(p);
+
+  if (warp == kKaWarps) {
+    // ------------------------------------------------ producer: lane w fills consumer w's ring
+    if (lane < kKaWarps) {
+      if (lane == 0) {
+        tma_prefetch_desc(&tmap_k);
+        tma_prefetch_desc(&tmap_v);
+      }
+      const int w = lane;
+      const int boxes = C::TK >> p.box_shift, per = 1 << (p.box_shift - 4);  // boxes of a tile, key groups of a box
+      struct Tile {
+        int b, head, key;  // key < 0: none
+        int end;           // keys of the sequence
+        int id[C::KG];
+        float ks[C::KG], vs[C::KG];
+      };
+      KaSeg g;
+      int item = 0, stop = 0;
+      bool more = true;
+      auto advance = [&](Tile& t) {  // the next tile of this lane, without its page ids
+        t.key = -1;
+        while (more) {
+          if (item >= stop) {
+            more = walk.next(p, g);
+            if (!more) return;
+            item = g.item0;
+            stop = g.item1;
+          }
+          const int key = g.key0 + (item * kKaWarps + w) * C::TK;
+          ++item;
+          if (key < g.range.hi && key + C::TK > g.range.lo) {
+            t.b = g.b;
+            t.head = g.head;
+            t.key = key;
+            t.end = g.s.kv_len;
+            return;
+          }
+        }
+      };
+      auto fetch_ids = [&](Tile& t) {
+#pragma unroll
+        for (int i = 0; i < C::KG; ++i) {
+          t.id[i] = -1;
+          if (t.key >= 0 && i < boxes && t.key + (i << p.box_shift) < t.end)
+            t.id[i] = __ldg(p.batch.table + (long long)t.b * p.batch.table_stride +
+                            ((t.key + (i << p.box_shift)) >> p.cache.page_shift));
+        }
+      };
+      auto fetch_scales = [&](Tile& t) {
+#pragma unroll
+        for (int i = 0; i < C::KG; ++i) {
+          t.ks[i] = t.vs[i] = 0.f;
+          if (t.key >= 0 && i < boxes && t.key + (i << p.box_shift) < t.end) {
+            if (t.id[i] >= 0 && t.id[i] < p.cache.pages) {
+              const long long at = (long long)t.id[i] * p.cache.kv_heads + t.head;
+              t.ks[i] = p.cache.scales[0][at];
+              t.vs[i] = p.cache.scales[1][at];
+            } else {
+              record_error(p.err, kErrInput);
+              t.id[i] = -1;
+            }
+          }
+        }
+      };
+      Tile t0, t1, t2;
+      advance(t0);
+      fetch_ids(t0);
+      advance(t1);
+      fetch_ids(t1);
+      fetch_scales(t0);
+      int stage = 0;
+      uint32_t phase = 0;
+      while (t0.key >= 0) {
+        advance(t2);
+        fetch_ids(t2);
+        fetch_scales(t1);
+        if (!ka_wait(&sh->empty[w][stage], phase ^ 1u, sh, p.err)) break;
+        uint32_t bytes = 0;
+#pragma unroll
+        for (int i = 0; i < C::KG; ++i)
+          if (i < boxes && t0.id[i] >= 0) bytes += 2u * (uint32_t(D) << p.box_shift);
+#pragma unroll
+        for (int i = 0; i < C::KG; ++i) {
+          const int box = i / per;
+          float ks = 0.f, vs = 0.f;
+#pragma unroll
+          for (int j = 0; j < C::KG; ++j)
+            if (j == box) ks = t0.ks[j], vs = t0.vs[j];
+          sh->scales[w][stage][0][i] = ks;
+          sh->scales[w][stage][1][i] = vs;
+          sh->scales[w][stage][2][i] = __log2f(vs);
+        }
+        mbar_arrive_expect_tx(&sh->full[w][stage], bytes);
+        const uint32_t kt = ring + uint32_t((w * kKaStages + stage) * 2) * kKaTileBytes, vt = kt + kKaTileBytes;
+#pragma unroll
+        for (int i = 0; i < C::KG; ++i) {
+          if (i < boxes && t0.id[i] >= 0) {
+            const int key = t0.key + (i << p.box_shift);
+            const int row = int((((long long)t0.id[i] * p.cache.kv_heads + t0.head) << p.cache.page_shift) +
+                                (key & ((1 << p.cache.page_shift) - 1)));
+            const uint32_t off = (uint32_t(i) << p.box_shift) * C::kRowBytes;
+#pragma unroll
+            for (int cb = 0; cb < C::kColBlocks; ++cb) {
+              tma_load_2d(kt + off + uint32_t(cb) * C::TK * 128u, &tmap_k, &sh->full[w][stage], cb * 128, row);
+              tma_load_2d(vt + off + uint32_t(cb) * C::TK * 128u, &tmap_v, &sh->full[w][stage], cb * 128, row);
+            }
+          }
+        }
+        if (++stage == kKaStages) { stage = 0; phase ^= 1u; }
+        t0 = t1;
+        t1 = t2;
+      }
+      if (sh->abort) {
+        // let the copies in flight land before the CTA exits (bounded: 50 us)
+        unsigned long long ta, tb;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(ta));
+        do {
+          asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(tb));
+        } while (tb - ta < 50000ull);
+      }
+    }
+    return;
+  }
+
+  // -------------------------------------------------- consumers
+  const int g = lane >> 2, t = lane & 3;
+  const int tid = threadIdx.x;
+  bool ok = true;  // every warp goes through every barrier below, even after a wait that gave up
+  int stage = 0;
+  uint32_t phase = 0;
+  KaSeg seg;
+  while (walk.next(p, seg)) {
+    // ---- q rows of the tile into fragments: half a warp per row
+    const int rows = seg.s.q_len * p.group;
+    {
+      const int r = 2 * warp + (lane >> 4), l16 = lane & 15;
+      const int row = seg.tile * kKaRows + r;
+      float v[D / 16];
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) v[i] = 0.f;
+      if (row < rows) {
+        const int j = row / p.group, h = seg.head * p.group + row - j * p.group;
+        const uint16_t* src = p.q.data + (long long)(seg.s.start + j) * p.q.token + h * p.q.head + l16 * (D / 16);
+#pragma unroll
+        for (int i = 0; i < D / 16; i += 4) {
+          const uint2 raw = __ldcg(reinterpret_cast<const uint2*>(src + i));
+          v[i] = __uint_as_float(raw.x << 16);
+          v[i + 1] = __uint_as_float(raw.x & 0xFFFF0000u);
+          v[i + 2] = __uint_as_float(raw.y << 16);
+          v[i + 3] = __uint_as_float(raw.y & 0xFFFF0000u);
+        }
+      }
+      float top = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) top = fmaxf(top, fabsf(v[i]));
+#pragma unroll
+      for (int off = 8; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+      // the row's power of two: its largest value lands in [2^13, 2^14)
+      const int e = min(100, max(-100, 127 + 13 - int(__float_as_uint(top) >> 23)));
+      const float up = __uint_as_float(uint32_t(127 + e) << 23);
+      if (l16 == 0) sh->row_factor[r] = __uint_as_float(uint32_t(127 - e) << 23) * p.scale_log2;
+#pragma unroll
+      for (int i = 0; i < D / 16; i += 2) {
+        const int d = l16 * (D / 16) + i;
+        const int step = (d >> 6) * 4 + ((d >> 2) & 3), ln = (r & 7) * 4 + ((d >> 4) & 3);
+        const int reg = ((d & 2) ? 2 : 0) + (r >> 3);
+        const __half2 h = __floats2half2_rn(v[i] * up, v[i + 1] * up);
+        qf[(step * 32 + ln) * 4 + reg] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+    ka_sync();
+    uint32_t qr[C::kQRegs ? C::kSteps : 1][4];
+    if constexpr (C::kQRegs) {
+#pragma unroll
+      for (int s = 0; s < C::kSteps; ++s) {
+        const uint4 f = *reinterpret_cast<const uint4*>(qf + (s * 32 + lane) * 4);
+        qr[s][0] = f.x, qr[s][1] = f.y, qr[s][2] = f.z, qr[s][3] = f.w;
+      }
+    }
+    const float f0 = sh->row_factor[g], f1 = sh->row_factor[g + 8];
+    int lim[2], low[2];  // the last key a row sees, and the first
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int row = min(seg.tile * kKaRows + g + 8 * i, rows - 1);
+      lim[i] = seg.s.kv_len - seg.s.q_len + row / p.group;
+      low[i] = p.window > 0 ? lim[i] - p.window + 1 : 0;
+    }
+    const int lim_min = seg.s.kv_len - seg.s.q_len + seg.tile * kKaRows / p.group;
+    const int low_max = p.window > 0 ? seg.range.hi - p.window : 0;
+
+    float o[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    // running maxima of the scores (m) and of score + log2(vs), less 15 (v); both as log2
+    float m0 = -INFINITY, m1 = -INFINITY, v0 = -INFINITY, v1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+
+    for (int item = seg.item0; item < seg.item1; ++item) {
+      const int key = seg.key0 + (item * kKaWarps + warp) * C::TK;
+      if (!(key < seg.range.hi && key + C::TK > seg.range.lo)) continue;
+      if (ok) ok = __all_sync(0xffffffffu, ka_wait(&sh->full[warp][stage], phase, sh, p.err));
+      if (!ok) continue;
+      const uint32_t kt = ring + uint32_t((warp * kKaStages + stage) * 2) * kKaTileBytes, vt = kt + kKaTileBytes;
+      // ---- scores
+      float s[C::TK / 8][4];
+#pragma unroll
+      for (int j = 0; j < C::TK / 8; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        uint32_t qs[4][4];
+#pragma unroll
+        for (int st = 0; st < 4; ++st) {
+          if constexpr (C::kQRegs) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) qs[st][i] = qr[4 * c + st][i];
+          } else {
+            const uint4 f = *reinterpret_cast<const uint4*>(qf + ((4 * c + st) * 32 + lane) * 4);
+            qs[st][0] = f.x, qs[st][1] = f.y, qs[st][2] = f.z, qs[st][3] = f.w;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < C::TK / 8; ++j) {
+          uint32_t w[4];
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                       : "r"(kt + ka_at<D>(uint32_t(8 * j) + ka_tau<D>(g), uint32_t(4 * c + t))));
+#pragma unroll
+          for (int st = 0; st < 4; ++st) {
+            const uint32_t x = w[st] ^ 0x80808080u;
+            ka_mma(s[j], qs[st], ka_codes(x, 0x4140u), ka_codes(x, 0x4342u));
+          }
+        }
+      }
+      // ---- running maxima and sum
+      float t0 = -INFINITY, t1 = -INFINITY, x0 = -INFINITY, x1 = -INFINITY;
+      const bool edge = key + C::TK - 1 > lim_min || key < low_max;
+#pragma unroll
+      for (int kb = 0; kb < C::KG; ++kb) {
+        const float ks = sh->scales[warp][stage][0][kb], lv = sh->scales[warp][stage][2][kb] - 15.f;
+        float g0 = -INFINITY, g1 = -INFINITY;
+#pragma unroll
+        for (int j = 2 * kb; j < 2 * kb + 2; ++j) {
+          s[j][0] *= f0 * ks;
+          s[j][1] *= f0 * ks;
+          s[j][2] *= f1 * ks;
+          s[j][3] *= f1 * ks;
+          if (edge) {
+            const int ka = key + 8 * j + int(ka_tau<D>(2 * t)), kc = key + 8 * j + int(ka_tau<D>(2 * t + 1));
+            if (ka > lim[0] || ka < low[0]) s[j][0] = -INFINITY;
+            if (kc > lim[0] || kc < low[0]) s[j][1] = -INFINITY;
+            if (ka > lim[1] || ka < low[1]) s[j][2] = -INFINITY;
+            if (kc > lim[1] || kc < low[1]) s[j][3] = -INFINITY;
+          }
+          g0 = fmaxf(g0, fmaxf(s[j][0], s[j][1]));
+          g1 = fmaxf(g1, fmaxf(s[j][2], s[j][3]));
+        }
+        t0 = fmaxf(t0, g0);
+        t1 = fmaxf(t1, g1);
+        x0 = fmaxf(x0, g0 + lv);
+        x1 = fmaxf(x1, g1 + lv);
+      }
+#pragma unroll
+      for (int off = 1; off < 4; off <<= 1) {
+        t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, off));
+        t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, off));
+        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, off));
+        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, off));
+      }
+      const float n0 = fmaxf(m0, t0), n1 = fmaxf(m1, t1), y0 = fmaxf(v0, x0), y1 = fmaxf(v1, x1);
+      const float u0 = n0 == -INFINITY ? 0.f : n0, u1 = n1 == -INFINITY ? 0.f : n1;
+      const float z0 = y0 == -INFINITY ? 0.f : y0, z1 = y1 == -INFINITY ? 0.f : y1;
+      l0 *= ex2(m0 - u0);
+      l1 *= ex2(m1 - u1);
+      const float r0 = ex2(v0 - z0), r1 = ex2(v1 - z1);
+      if (__any_sync(0xffffffffu, r0 != 1.f || r1 != 1.f)) {
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          o[i][0] *= r0;
+          o[i][1] *= r0;
+          o[i][2] *= r1;
+          o[i][3] *= r1;
+        }
+      }
+      m0 = n0;
+      m1 = n1;
+      v0 = y0;
+      v1 = y1;
+      // what takes p to the scale of v (times vs); where it is out of range, p is 0
+      const float c0 = fminf(ex2(u0 - z0), 0x1p100f), c1 = fminf(ex2(u1 - z1), 0x1p100f);
+      // ---- probabilities, and their product with V
+#pragma unroll
+      for (int kb = 0; kb < C::KG; ++kb) {
+        const float vs = sh->scales[warp][stage][1][kb];
+        const float vs0 = fminf(vs * c0, 0x1p100f), vs1 = fminf(vs * c1, 0x1p100f);
+        uint32_t a[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float* x = s[2 * kb + i];
+          const float p0 = ex2(x[0] - u0), p1 = ex2(x[1] - u0), p2 = ex2(x[2] - u1), p3 = ex2(x[3] - u1);
+          l0 += p0 + p1;
+          l1 += p2 + p3;
+          const __half2 h0 = __floats2half2_rn(p0 * vs0, p1 * vs0), h1 = __floats2half2_rn(p2 * vs1, p3 * vs1);
+          a[2 * i] = *reinterpret_cast<const uint32_t*>(&h0);
+          a[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+        }
+        const uint32_t vrow = uint32_t(16 * kb + ((lane >> 3) & 1) * 8) + ka_tau<D>(lane & 7);
+#pragma unroll
+        for (int c2 = 0; c2 < D / 32; ++c2) {
+          uint32_t r[4];
+          asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                       : "r"(vt + ka_at<D>(vrow, uint32_t(2 * c2 + (lane >> 4)))));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) r[i] ^= 0x80808080u;
+          ka_mma(o[4 * c2], a, ka_codes(r[0], 0x4240u), ka_codes(r[1], 0x4240u));
+          ka_mma(o[4 * c2 + 1], a, ka_codes(r[0], 0x4341u), ka_codes(r[1], 0x4341u));
+          ka_mma(o[4 * c2 + 2], a, ka_codes(r[2], 0x4240u), ka_codes(r[3], 0x4240u));
+          ka_mma(o[4 * c2 + 3], a, ka_codes(r[2], 0x4341u), ka_codes(r[3], 0x4341u));
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->empty[warp][stage]);
+      if (++stage == kKaStages) { stage = 0; phase ^= 1u; }
+    }
+
+    // ---- join the warps
+#pragma unroll
+    for (int off = 1; off < 4; off <<= 1) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, off);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, off);
+    }
+    if (t == 0) {
+      sh->warp_m[warp][g] = m0;
+      sh->warp_m[warp][g + 8] = m1;
+      sh->warp_l[warp][g] = l0;
+      sh->warp_l[warp][g + 8] = l1;
+      sh->warp_v[warp][g] = v0;
+      sh->warp_v[warp][g + 8] = v1;
+    }
+    ka_sync();
+    float top0 = -INFINITY, top1 = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kKaWarps; ++w) {
+      top0 = fmaxf(top0, sh->warp_v[w][g]);
+      top1 = fmaxf(top1, sh->warp_v[w][g + 8]);
+    }
+    const float w0 = v0 == -INFINITY ? 0.f : ex2(v0 - top0), w1 = v1 == -INFINITY ? 0.f : ex2(v1 - top1);
+    // this thread's place in the joined tile: row jr, columns 2 jc, 2 jc + 1 of each 32
+    const int jr = tid >> 4, jc = tid & 15;
+    float jm = -INFINITY, jv = -INFINITY, jl = 0.f;
+#pragma unroll
+    for (int w = 0; w < kKaWarps; ++w) {
+      jm = fmaxf(jm, sh->warp_m[w][jr]);
+      jv = fmaxf(jv, sh->warp_v[w][jr]);
+    }
+#pragma unroll
+    for (int w = 0; w < kKaWarps; ++w)
+      if (sh->warp_m[w][jr] != -INFINITY) jl += sh->warp_l[w][jr] * ex2(sh->warp_m[w][jr] - jm);
+    const bool whole = seg.item0 == 0 && seg.item1 == seg.items;
+    const int slot = int(blockIdx.x) * 2 + (i0 >= seg.start ? 0 : 1);
+    float* part = p.part + (size_t)slot * C::kSlotFloats;
+    const int row = seg.tile * kKaRows + jr;
+    const int oj = row / p.group, oh = seg.head * p.group + row - oj * p.group;
+    uint16_t* dst = p.out.data + (long long)(seg.s.start + oj) * p.out.token + oh * p.out.head;
+    // (sum of p vs v at 2^-jv) 2^(jv - jm) / (sum of p at 2^-jm); jv is -inf where every vs is 0
+    const float norm = jv > -INFINITY ? __fdiv_rn(ex2(jv - jm), jl) : 0.f;
+#pragma unroll
+    for (int c2 = 0; c2 < D / 32; ++c2) {
+      float* mine = join + warp * (kKaRows * 32);
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const float(&e)[4] = o[4 * c2 + 2 * hf];
+        const float(&d)[4] = o[4 * c2 + 2 * hf + 1];
+        *reinterpret_cast<float4*>(mine + g * 32 + 16 * hf + 4 * t) =
+            make_float4(e[0] * w0, d[0] * w0, e[1] * w0, d[1] * w0);
+        *reinterpret_cast<float4*>(mine + (g + 8) * 32 + 16 * hf + 4 * t) =
+            make_float4(e[2] * w1, d[2] * w1, e[3] * w1, d[3] * w1);
+      }
+      ka_sync();
+      float x = 0.f, y = 0.f;
+#pragma unroll
+      for (int w = 0; w < kKaWarps; ++w) {
+        const float2 v = *reinterpret_cast<const float2*>(join + w * (kKaRows * 32) + jr * 32 + 2 * jc);
+        x += v.x;
+        y += v.y;
+      }
+      if (!whole) {
+        *reinterpret_cast<float2*>(part + jr * D + 32 * c2 + 2 * jc) = make_float2(x, y);
+      } else if (row < rows && ok) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(x * norm, y * norm);
+        *reinterpret_cast<__nv_bfloat162*>(dst + 32 * c2 + 2 * jc) = b;
+      }
+      ka_sync();
+    }
+    if (!whole) {
+      if (jc == 0) {
+        part[kKaRows * D + jr] = jm;
+        part[kKaRows * D + kKaRows + jr] = jl;
+        part[kKaRows * D + 2 * kKaRows + jr] = jv;
+      }
+      const int c_first = ka_item_cta(seg.start, total, ctas), c_last = ka_item_cta(seg.start + seg.items - 1, total, ctas);
+      __threadfence();
+      ka_sync();
+      if (tid == 0) sh->last = atomicAdd(p.counters + c_first, 1u) == unsigned(c_last - c_first);
+      ka_sync();
+      if (sh->last) {
+        __threadfence();
+        auto slot_of = [&](int c) {
+          return p.part + (size_t)(c * 2 + (ka_first_item(c, total, ctas) >= seg.start ? 0 : 1)) * C::kSlotFloats;
+        };
+        float top = -INFINITY, vtop = -INFINITY, sum = 0.f;
+        for (int c = c_first; c <= c_last; ++c) {
+          top = fmaxf(top, __ldcg(slot_of(c) + kKaRows * D + jr));
+          vtop = fmaxf(vtop, __ldcg(slot_of(c) + kKaRows * D + 2 * kKaRows + jr));
+        }
+        float acc[D / 16];
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) acc[i] = 0.f;
+        for (int c = c_first; c <= c_last; ++c) {
+          const float* src = slot_of(c);
+          const float cm = __ldcg(src + kKaRows * D + jr), cv = __ldcg(src + kKaRows * D + 2 * kKaRows + jr);
+          const float f = cv == -INFINITY ? 0.f : ex2(cv - vtop);
+          if (cm != -INFINITY) sum += ex2(cm - top) * __ldcg(src + kKaRows * D + kKaRows + jr);
+#pragma unroll
+          for (int i = 0; i < D / 16; i += 4) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(src + jr * D + jc * 4 + i * 16));
+            acc[i] += f * v.x;
+            acc[i + 1] += f * v.y;
+            acc[i + 2] += f * v.z;
+            acc[i + 3] += f * v.w;
+          }
+        }
+        const float n = vtop > -INFINITY ? __fdiv_rn(ex2(vtop - top), sum) : 0.f;
+        if (row < rows) {
+#pragma unroll
+          for (int i = 0; i < D / 16; i += 4) {
+            const __nv_bfloat162 a = __floats2bfloat162_rn(acc[i] * n, acc[i + 1] * n);
+            const __nv_bfloat162 b = __floats2bfloat162_rn(acc[i + 2] * n, acc[i + 3] * n);
+            *reinterpret_cast<uint2*>(dst + jc * 4 + i * 16) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+          }
+        }
+        if (tid == 0) p.counters[c_first] = 0u;  // ready for the next launch on this workspace
+      }
+    }
+    ka_sync();  // q fragments, warp_m and the join buffer are free again
+  }
+}
+
+}  // namespace w4a8

@@ -1,0 +1,266 @@
+// The int8 paged cache: writing new tokens into it and reading pages back.
+//
+// codes  int8 [pages][kv_heads][page][D], scales fp32 [pages][kv_heads], one
+// set for K and one for V.  Value = code * scale of its (page, head).
+//
+// Update of one (page, head) with new rows at places [first, first + n):
+//   need = max |row value| / 127
+//   s'   = max(s, need), where s = 0 if the page starts with these rows
+//   codes of the places before `first`: rint(c * (s / s')) if s' > s
+//   new codes: clamp(rint(v / s'), -127, 127)
+// Places behind the new rows are left as they are.
+//
+// K rows are normed and rotated on the way (qk_rope.cuh) and quantised from
+// fp32, so they are rounded once.  One CTA per (touched page, head, K or V);
+// more CTAs of the same launch norm and rotate q, so a decode step's work
+// between the projection and the attention is this one launch.
+#pragma once
+
+#include "act.cuh"
+#include "common.cuh"
+#include "kv_index.h"
+#include "qk_rope.cuh"
+
+namespace w4a8 {
+
+struct KvCacheParams {
+  int8_t* codes[2];   // K, V
+  float* scales[2];
+  long long pages;
+  int kv_heads, page_shift, D;
+};
+
+struct KvBatchParams {
+  const int* table;      // [batch][table_stride]
+  long long table_stride;
+  const int* q_start;    // [batch + 1]
+  const int* kv_len;     // [batch]
+  int batch;
+  int tokens;
+};
+
+__device__ __forceinline__ KvSeq kv_load_seq(const KvBatchParams& b, int i, int page_shift) {
+  return kv_seq(__ldg(b.q_start + i), __ldg(b.q_start + i + 1), __ldg(b.kv_len + i), b.tokens,
+                b.table_stride << page_shift);
+}
+
+// Which touched page of which sequence unit u is (whole warp; the same
+// answer in every lane): sequences are scanned 32 at a time.  False past the
+// last one.
+__device__ __forceinline__ bool kv_find_page(const KvBatchParams& b, int page_shift, int u, int& seq, int& nth,
+                                             KvSeq& s, unsigned* err) {
+  const int lane = threadIdx.x & 31;
+  int before = 0;
+  for (int b0 = 0; b0 < b.batch; b0 += 32) {
+    KvSeq mine{0, 0, 0, false};
+    if (b0 + lane < b.batch) mine = kv_load_seq(b, b0 + lane, page_shift);
+    if (mine.bad && err) record_error(err, kErrInput);
+    int sum = kv_touched(mine, page_shift);
+    const int own = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, sum, off);
+      if (lane >= off) sum += o;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, before + sum > u);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      seq = b0 + l;
+      nth = u - (before + __shfl_sync(0xffffffffu, sum - own, l));
+      s.start = __shfl_sync(0xffffffffu, mine.start, l);
+      s.q_len = __shfl_sync(0xffffffffu, mine.q_len, l);
+      s.kv_len = __shfl_sync(0xffffffffu, mine.kv_len, l);
+      s.bad = false;
+      return true;
+    }
+    before += __shfl_sync(0xffffffffu, sum, 31);
+  }
+  return false;
+}
+
+// Position in its sequence of new token `row` (whole warp); -1 if it belongs
+// to none (rows behind the last sequence, or a bad sequence).
+__device__ __forceinline__ int kv_find_position(const KvBatchParams& b, int page_shift, int row) {
+  const int lane = threadIdx.x & 31;
+  for (int b0 = 0; b0 < b.batch; b0 += 32) {
+    KvSeq s{0, 0, 0, false};
+    if (b0 + lane < b.batch) s = kv_load_seq(b, b0 + lane, page_shift);
+    const unsigned in = __ballot_sync(0xffffffffu, row >= s.start && row < s.start + s.q_len);
+    if (in) return __shfl_sync(0xffffffffu, s.kv_len - s.q_len + (row - s.start), __ffs(in) - 1);
+  }
+  return -1;
+}
+
+struct KvUpdateParams {
+  QkParams qk;          // q, k (k_out unused), norm weights, rotation; positions may be NULL (the cache's)
+  HeadRows v;
+  KvCacheParams cache;
+  KvBatchParams batch;
+  int page_ctas;        // units * kv_heads * 2; the CTAs after them take a token of q each
+  unsigned* err;
+};
+
+constexpr int kKvThreads = 256;
+
+__device__ __forceinline__ float block_max_256(float v, float* warp_max) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+  if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = warp_max[0];
+#pragma unroll
+  for (int i = 1; i < kKvThreads / 32; ++i) v = fmaxf(v, warp_max[i]);
+  return v;
+}
+
+__device__ __forceinline__ uint2 quant8(const float (&v)[8], const QuantScale& qs) {
+  uint32_t lo = 0, hi = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = qs.fast ? quant_code<true>(v[i], qs) : quant_code<false>(v[i], qs);
+    const float b = qs.fast ? quant_code<true>(v[i + 4], qs) : quant_code<false>(v[i + 4], qs);
+    lo |= (uint32_t(int(a)) & 0xFFu) << (8 * i);
+    hi |= (uint32_t(int(b)) & 0xFFu) << (8 * i);
+  }
+  return make_uint2(lo, hi);
+}
+
+__device__ __forceinline__ uint32_t recode4(uint32_t w, float ratio) {
+  uint32_t out = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int c = int(int8_t(w >> (8 * i)));
+    out |= (uint32_t(int(rintf(float(c) * ratio))) & 0xFFu) << (8 * i);
+  }
+  return out;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kKvThreads) kv_update_kernel(const KvUpdateParams p) {
+  extern __shared__ __align__(16) float kv_rows[];  // [page][D]: the page's new rows, fp32
+  __shared__ float2 cs[kQkMaxPairs];
+  __shared__ float warp_max[kKvThreads / 32];
+  constexpr int LPH = D / 8, RPP = kKvThreads / LPH;  // rows per pass
+  pdl_wait();
+  pdl_launch_dependents();
+  const int g = threadIdx.x / LPH, sub = threadIdx.x & (LPH - 1);
+  const int ps = p.cache.page_shift;
+  if (int(blockIdx.x) >= p.page_ctas) {
+    // ------------------------------------------------ a token of q
+    const int token = int(blockIdx.x) - p.page_ctas;
+    const int at = kv_find_position(p.batch, ps, token);
+    if (at < 0) return;
+    const QkParams& qk = p.qk;
+    if (qk.rope.inv_freq) {
+      const int pos = qk.positions ? qk.positions[token] : at;
+      for (int i = threadIdx.x; i < qk.rope.rot_dim / 2; i += kKvThreads) cs[i] = rope_cs(qk.rope, pos, i);
+      __syncthreads();
+    }
+    for (int h0 = 0; h0 < qk.q.heads; h0 += RPP)
+      qk_head<D>(qk.q, qk.q_out, qk.q_weight, qk.eps, qk.rope, cs, token, h0 + g, h0 + g < qk.q.heads);
+    return;
+  }
+  // -------------------------------------------------- a page of a head, K or V
+  const int kind = int(blockIdx.x) & 1;
+  const int head = (int(blockIdx.x) >> 1) % p.cache.kv_heads;
+  const int unit = (int(blockIdx.x) >> 1) / p.cache.kv_heads;
+  int seq, nth;
+  KvSeq s;
+  if (!kv_find_page(p.batch, ps, unit, seq, nth, s, p.err)) return;
+  const int page = 1 << ps;
+  const int pi = kv_first_page(s, ps) + nth;                       // page of the sequence
+  const int j0 = max(0, (pi << ps) - (s.kv_len - s.q_len));        // its first new token here
+  const int first = s.kv_len - s.q_len + j0 - (pi << ps);          // and that token's place
+  const int n = min(s.q_len - j0, page - first);
+  const int id = __ldg(p.batch.table + (long long)seq * p.batch.table_stride + pi);
+  if (id < 0 || id >= p.cache.pages) {
+    if (threadIdx.x == 0) record_error(p.err, kErrInput);
+    return;
+  }
+  const HeadRows& src = kind ? p.v : p.qk.k;
+  float w[8];
+  const float* weight = kind ? nullptr : p.qk.k_weight;
+  head_weight<LPH>(weight, sub, w);
+  float amax = 0.f;
+  for (int r0 = 0; r0 < n; r0 += RPP) {  // every warp takes every pass: the norm and the rotation shuffle
+    const int r = r0 + g;
+    const bool live = r < n;
+    const int token = s.start + j0 + r;
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (live) bf16x8_to_float(__ldcg(reinterpret_cast<const uint4*>(src.data + token * src.token + head * src.head) + sub), v);
+    if (weight) head_norm<LPH>(v, w, p.qk.eps);
+    if (kind == 0 && p.qk.rope.inv_freq) {
+      const int pos = !live ? 0 : p.qk.positions ? p.qk.positions[token] : s.kv_len - s.q_len + j0 + r;
+      head_rope<LPH>(v, p.qk.rope, sub, [&](int i) { return rope_cs(p.qk.rope, pos, i); });
+    }
+    if (live) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+      float4* dst = reinterpret_cast<float4*>(kv_rows + r * D + 8 * sub);
+      dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+      dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+  }
+  const float need = quant_scale(block_max_256(amax, warp_max));
+  float* scale = p.cache.scales[kind] + (long long)id * p.cache.kv_heads + head;
+  const float old = first == 0 ? 0.f : *scale;
+  const float now = fmaxf(old, need);
+  int8_t* codes = p.cache.codes[kind] + (((long long)id * p.cache.kv_heads + head) << ps) * D;
+  if (first > 0 && now > old) {
+    const float ratio = __fdiv_rn(old, now);
+    for (int i = threadIdx.x * 16; i < first * D; i += kKvThreads * 16) {
+      uint4 c = *reinterpret_cast<uint4*>(codes + i);
+      c.x = recode4(c.x, ratio);
+      c.y = recode4(c.y, ratio);
+      c.z = recode4(c.z, ratio);
+      c.w = recode4(c.w, ratio);
+      *reinterpret_cast<uint4*>(codes + i) = c;
+    }
+  }
+  const QuantScale qs = quant_prepare(now);
+  for (int r = g; r < n; r += RPP) {  // the rows this thread staged
+    const float4 a = *reinterpret_cast<const float4*>(kv_rows + r * D + 8 * sub);
+    const float4 b = *reinterpret_cast<const float4*>(kv_rows + r * D + 8 * sub + 4);
+    const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    *reinterpret_cast<uint2*>(codes + (first + r) * D + 8 * sub) = quant8(v, qs);
+  }
+  __syncthreads();  // every thread has read the old scale
+  if (threadIdx.x == 0) *scale = now;
+}
+
+// Pages back to bf16: values code * scale of both kinds, [n][kv_heads][page][D].
+__global__ void __launch_bounds__(256) kv_dequant_kernel(KvCacheParams c, const int* __restrict__ ids, long long chunks,
+                                                         uint16_t* __restrict__ k_out, uint16_t* __restrict__ v_out,
+                                                         unsigned* err) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;  // 16 codes of one kind
+  if (i >= 2 * chunks) return;
+  const int kind = i >= chunks;
+  const long long at = (kind ? i - chunks : i) * 16;
+  const long long slab = at / ((long long)c.D << c.page_shift);  // (n, head)
+  const long long inside = at - slab * ((long long)c.D << c.page_shift);
+  const long long nth = slab / c.kv_heads;
+  const int head = int(slab - nth * c.kv_heads);
+  const int id = __ldg(ids + nth);
+  uint4 w = make_uint4(0u, 0u, 0u, 0u);
+  float s = 0.f;
+  if (id >= 0 && id < c.pages) {
+    const long long at_head = (long long)id * c.kv_heads + head;
+    w = *reinterpret_cast<const uint4*>(c.codes[kind] + (at_head << c.page_shift) * c.D + inside);
+    s = c.scales[kind][at_head];
+  } else {
+    record_error(err, kErrInput);
+  }
+  uint16_t* out = (kind ? v_out : k_out) + at;
+  const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = float(int(int8_t(ws[2 * h + (j >> 2)] >> (8 * (j & 3))))) * s;
+    reinterpret_cast<uint4*>(out)[h] = float_to_bf16x8(v);
+  }
+}
+
+}  // namespace w4a8

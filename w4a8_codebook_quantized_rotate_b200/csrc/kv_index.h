@@ -1,0 +1,68 @@
+// Index arithmetic of the paged int8 cache and of the batch that is written
+// into it or attends over it.  Plain functions without device code, so that
+// the host (argument checks, tests) and the kernels share them.
+//
+// A batch is `batch` sequences.  Sequence b has q_len = q_start[b + 1] -
+// q_start[b] new tokens, which are the last of the kv_len[b] tokens that the
+// cache holds of it; new token j sits at position kv_len - q_len + j.
+// Position t of a sequence is place t % page of page table[b][t / page].
+#pragma once
+
+#include <cstdint>
+
+#ifdef __CUDACC__
+#define W4A8_HD __host__ __device__ __forceinline__
+#else
+#define W4A8_HD inline
+#endif
+
+namespace w4a8 {
+
+struct KvSeq {
+  int start;    // row of its first new token
+  int q_len;    // new tokens
+  int kv_len;   // tokens in the cache, the new ones among them
+  bool bad;     // the batch's numbers do not fit together: nothing is done for it
+};
+
+// What a sequence's numbers say, or an empty, bad sequence where they leave
+// the buffers: rows outside [0, tokens], more new tokens than the cache
+// holds, or a length past the block table.
+W4A8_HD KvSeq kv_seq(int start, int end, int kv_len, int64_t tokens, int64_t table_tokens) {
+  KvSeq s;
+  s.bad = start < 0 || end < start || int64_t(end) > tokens || kv_len < 0 || end - start > kv_len ||
+          int64_t(kv_len) > table_tokens;
+  s.start = s.bad ? 0 : start;
+  s.q_len = s.bad ? 0 : end - start;
+  s.kv_len = s.bad ? 0 : kv_len;
+  return s;
+}
+
+// Pages that a sequence's new tokens lie in: [kv_first_page, + kv_touched).
+W4A8_HD int kv_first_page(const KvSeq& s, int page_shift) { return (s.kv_len - s.q_len) >> page_shift; }
+W4A8_HD int kv_touched(const KvSeq& s, int page_shift) {
+  return s.q_len == 0 ? 0 : ((s.kv_len - 1) >> page_shift) - kv_first_page(s, page_shift) + 1;
+}
+
+// An upper bound of the touched pages of a batch that only needs host
+// numbers: n new tokens lie in at most (n - 2) / page + 2 <= n / page + 2
+// pages of a sequence (n of them where that is fewer).
+W4A8_HD int64_t kv_touched_bound(int64_t tokens, int64_t batch, int page) {
+  const int64_t a = tokens / page + 2 * batch;
+  return a < tokens ? a : tokens;
+}
+
+// Keys that a row tile sees: of the new tokens j0 .. j1 (inclusive) the
+// first one's window starts the range and the last one's position ends it.
+struct KvRange {
+  int lo, hi;  // [lo, hi)
+};
+W4A8_HD KvRange kv_range(const KvSeq& s, int j0, int j1, int window) {
+  KvRange r;
+  const int p0 = s.kv_len - s.q_len + j0;
+  r.hi = s.kv_len - s.q_len + j1 + 1;
+  r.lo = (window > 0 && p0 - window + 1 > 0) ? p0 - window + 1 : 0;
+  return r;
+}
+
+}  // namespace w4a8

@@ -9,6 +9,7 @@
 #include <cuda.h>  // driver types for the stream write below (resolved at run time, not linked)
 
 #include "w4a8.h"
+#include "w4a8_int8.h"
 
 #include "act.cuh"
 #include "common.cuh"
@@ -17,8 +18,13 @@
 #include "gemm_tc.cuh"
 #include "gemv.cuh"
 #include "gemv1.cuh"
+#include "int8_gemm.cuh"
+#include "int8_quant.cuh"
+#include "kv_attn.cuh"
+#include "kv_cache.cuh"
 #include "nvfp4.cuh"
 #include "pack.cuh"
+#include "qk_rope.cuh"
 #include "verify.cuh"
 
 namespace w4a8 {
@@ -43,6 +49,7 @@ struct DeviceState {
   bool arch_ok = false;
   int sms = 0;
   unsigned* err = nullptr;
+  bool int8_ready = false;  // the opt-ins of int8_api.cuh's kernels are done
 };
 
 DeviceState g_devices[kMaxDevices];
@@ -1221,3 +1228,5 @@ const char* w4a8_status_string(w4a8_status status) {
 }
 
 }  // extern "C"
+
+#include "int8_api.cuh"
