@@ -47,26 +47,24 @@ w4a8_status w4a8_int8_quantize(const void* x, int32_t x_is_f32, int64_t R, int64
                                int8_t* codes, float* s, void* stream);
 
 /*
- * Workspace bytes of w4a8_int8_gemm and w4a8_int8_linear for (M, K, N), 0
- * for a bad shape.  Fill a new workspace with zeros before its first use;
- * every completed call leaves the words that must be zero so, for any shape.
- * Two calls that share a workspace must be ordered on the GPU (captured
- * graphs that are replayed at the same time need one each).  After a call
- * that reported W4A8_ERR_TIMEOUT, zero it again.
+ * y [M, N] (bf16 bits) from codes x_q [M, K], w_q [N, K] and scales s_x [M],
+ * s_w [N].  Errors: NULL, SHAPE, ALIGN, ARCH, CUDA; a bounded wait that gives
+ * up leaves y undefined and is reported by w4a8_get_device_error.
+ */
+w4a8_status w4a8_int8_gemm(const int8_t* x_q, const float* s_x, int64_t M, const int8_t* w_q,
+                           const float* s_w, int64_t N, int64_t K, uint16_t* y, void* stream);
+
+/*
+ * Workspace bytes of w4a8_int8_linear (0 for a bad shape): scratch that the
+ * quantised activations pass through, in any state.  Two calls that share a
+ * workspace must be ordered on the GPU (captured graphs that are replayed at
+ * the same time need one each).
  */
 size_t w4a8_int8_linear_workspace_bytes(int64_t M, int64_t K, int64_t N);
 
 /*
- * y [M, N] (bf16 bits) from codes x_q [M, K], w_q [N, K] and scales s_x [M],
- * s_w [N].  Errors: NULL, SHAPE, ALIGN, WORKSPACE, ARCH, CUDA.
- */
-w4a8_status w4a8_int8_gemm(const int8_t* x_q, const float* s_x, int64_t M, const int8_t* w_q,
-                           const float* s_w, int64_t N, int64_t K, uint16_t* y, void* workspace,
-                           size_t workspace_bytes, void* stream);
-
-/*
  * The layer: x [M, K] (bf16 bits) is quantised into the workspace, then
- * w4a8_int8_gemm.  Errors: as w4a8_int8_gemm.
+ * w4a8_int8_gemm.  Errors: as w4a8_int8_gemm, and WORKSPACE.
  */
 w4a8_status w4a8_int8_linear(const uint16_t* x, int64_t M, int64_t K, int32_t rotate, const int8_t* w_q,
                              const float* s_w, int64_t N, uint16_t* y, void* workspace,
@@ -181,7 +179,10 @@ w4a8_status w4a8_kv_dequant(const w4a8_kv_cache* cache, const int32_t* ids, int6
 
 /*
  * Workspace bytes of w4a8_kv_attention (0 for a bad shape); zero-filled
- * before its first use, shared and reset as the int8 layer's.
+ * before its first use; every completed call leaves the words that must be
+ * zero so, for any shape.  Two calls that share a workspace must be ordered
+ * on the GPU (captured graphs that are replayed at the same time need one
+ * each).  After a call that reported W4A8_ERR_TIMEOUT, zero it again.
  */
 size_t w4a8_kv_attention_workspace_bytes(int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t head_dim);
 

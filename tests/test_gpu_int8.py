@@ -118,13 +118,15 @@ def test_product_extremes(lib):
 
 
 def test_one_workspace_serves_every_shape(lib):
-    """Calls of different shapes on one workspace, in turn: each leaves the words that must be zero so."""
-    big = max(lib.int8_linear_workspace(m, k, n, "cuda").numel() for m, n, k in SHAPES)
-    ws = torch.zeros(big, dtype=torch.uint8, device="cuda")
-    for m, n, k in (SHAPES[12], SHAPES[5], SHAPES[13], SHAPES[0], SHAPES[10], SHAPES[12]):
-        x, sx, w, sw = operands(m, n, k, m * n + k)
-        check(lib.int8_gemm(dev(x), dev(sx), dev(w), dev(sw), workspace=ws), R.product(x, sx, w, sw))
-    assert not ws[:4096].any()
+    """Layers of different shapes on one workspace, in turn, whatever it held before."""
+    shapes = [(1, 592, 768), (300, 200, 1280), (45, 1000, 512), (1, 592, 768)]
+    ws = torch.full((max(lib.int8_linear_workspace(m, k, n, "cuda").numel() for m, n, k in shapes),), 255,
+                    dtype=torch.uint8, device="cuda")
+    for m, n, k in shapes:
+        bits, _ = acts(m, k, 75)
+        wq, sw = lib.int8_quantize(dev(synth.weights(n, k, synth.rng_for(75, n, "weight"))))
+        xq, sx = lib.int8_quantize(bf16(bits))
+        check(lib.int8_linear(bf16(bits), wq, sw, workspace=ws), R.product(*(t.cpu().numpy() for t in (xq, sx, wq, sw))))
 
 
 @pytest.mark.parametrize("m,n,k,rotate", [(1, 592, 768, True), (1, 300, 4304, False), (7, 130, 512, True),

@@ -63,12 +63,17 @@ def test_int8_layer_refusals(lib):
     for m, k, n in ((0, 512, 64), (5, 500, 64), (5, 0, 64), (5, 512, 0), (5, 32784, 64), (5, 512, 2 ** 24 + 1),
                     (65535 * 256 + 1, 512, 64)):
         assert lib.w4a8_int8_linear_workspace_bytes(m, k, n) == 0
-        assert lib.w4a8_int8_gemm(P, P, m, P, P, n, k, P, P, 1 << 40, None) == SHAPE
+        assert lib.w4a8_int8_gemm(P, P, m, P, P, n, k, P, None) == SHAPE
         assert lib.w4a8_int8_linear(P, m, k, 0, P, P, n, P, P, 1 << 40, None) == SHAPE
     assert lib.w4a8_int8_linear(P, 5, 272, 1, P, P, 64, P, P, 1 << 30, None) == SHAPE   # rotation needs K % 256
     assert lib.w4a8_int8_linear_workspace_bytes(5, 272, 64) > 0
     assert lib.w4a8_int8_linear(P, 5, 512, 1, P, P, 64, P, P, ws - 1, None) == WORKSPACE
-    assert lib.w4a8_int8_gemm(P, P, 5, P, P, 64, 512, P, P, ws - 1, None) == WORKSPACE
+    for i in (0, 1, 3, 4, 7):
+        a = [P, P, 5, P, P, 64, 512, P, None]
+        a[i] = None
+        assert lib.w4a8_int8_gemm(*a) == NULL
+        a[i] = P + 8
+        assert lib.w4a8_int8_gemm(*a) == ALIGN
     for i in (0, 4, 5, 7, 8):
         a = [P, 5, 512, 1, P, P, 64, P, P, 1 << 30, None]
         if i not in (1, 2, 3, 6):

@@ -123,7 +123,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "w4a8_nvfp4_linear": (st, [vp, i64, i64, vp, vp, vp, i64, vp, vp, sz, vp]),
         "w4a8_int8_quantize": (st, [vp, ctypes.c_int32, i64, i64, ctypes.c_int32, vp, vp, vp]),
         "w4a8_int8_linear_workspace_bytes": (sz, [i64, i64, i64]),
-        "w4a8_int8_gemm": (st, [vp, vp, i64, vp, vp, i64, i64, vp, vp, sz, vp]),
+        "w4a8_int8_gemm": (st, [vp, vp, i64, vp, vp, i64, i64, vp, vp]),
         "w4a8_int8_linear": (st, [vp, i64, i64, ctypes.c_int32, vp, vp, i64, vp, vp, sz, vp]),
         "w4a8_qk_norm_rope": (st, [vp, vp, i64, ctypes.c_int32, vp, vp, ctypes.c_float, vp, vp, vp, vp, vp]),
         "w4a8_kv_update": (st, [vp, vp, vp, vp, vp, vp, vp, ctypes.c_float, vp, vp, vp, vp]),
@@ -616,15 +616,15 @@ def int8_quantize(x: torch.Tensor, rotate: bool = True, stream=None):
 
 
 def int8_linear_workspace(m: int, k: int, n: int, device) -> torch.Tensor:
-    """A zero-filled workspace for int8 layers of shape (M, K, N)."""
+    """A workspace for int8 layers of shape (M, K, N)."""
     need = int(load_library().w4a8_int8_linear_workspace_bytes(m, k, n))
     if need == 0:
         raise W4A8Error("w4a8_int8_linear_workspace_bytes", 2)
-    return torch.zeros(need, dtype=torch.uint8, device=device)
+    return torch.empty(need, dtype=torch.uint8, device=device)
 
 
 def int8_gemm(x_q: torch.Tensor, s_x: torch.Tensor, w_q: torch.Tensor, s_w: torch.Tensor,
-              workspace: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+              out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """y [M, N] bf16 = s_x s_w (x_q [M, K] int8 times w_q [N, K]^T int8)."""
     lib = load_library()
     m, k = _here(x_q, torch.int8, "x_q").shape
@@ -632,15 +632,12 @@ def int8_gemm(x_q: torch.Tensor, s_x: torch.Tensor, w_q: torch.Tensor, s_w: torc
     _here(w_q, torch.int8, "w_q", (n, k))
     _here(s_x, torch.float32, "s_x", (m,))
     _here(s_w, torch.float32, "s_w", (n,))
-    if workspace is None:
-        workspace = int8_linear_workspace(m, k, n, x_q.device)
-    _here(workspace, torch.uint8, "workspace")
     if out is None:
         out = torch.empty((m, n), dtype=torch.bfloat16, device=x_q.device)
     _here(out, torch.bfloat16, "out", (m, n))
     _check("w4a8_int8_gemm", lib.w4a8_int8_gemm(
         x_q.data_ptr(), s_x.data_ptr(), m, w_q.data_ptr(), s_w.data_ptr(), n, k, out.data_ptr(),
-        workspace.data_ptr(), workspace.numel(), _stream(stream)))
+        _stream(stream)))
     return out
 
 

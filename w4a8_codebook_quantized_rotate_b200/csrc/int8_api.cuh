@@ -3,6 +3,8 @@
 // whose per-device state and launch helpers it uses.
 #pragma once
 
+#include <cmath>
+
 namespace w4a8 {
 namespace {
 
@@ -16,24 +18,62 @@ bool q8_shape_ok(int64_t M, int64_t N, int64_t K, int rotate) {
   return M > 0 && M <= kMaxTokens && q8_rows_ok(N) && q8_k_ok(K, rotate);
 }
 
+// Token tile, k split and CTAs per SM of a product: the choice with the least
+// estimated time (in clocks).  A CTA takes its k blocks at the slowest of
+// its loads (89 bytes a clock and SM), the latency of a pipeline that its
+// stages do not cover, and its MMAs; then an epilogue, or the joining of a
+// split tile; the rounds of CTAs that fit at once add up, and memory (2010
+// bytes a clock) bounds it all.  The constants are fitted to 1600 measured
+// (shape, choice) pairs over 70 shapes of 1 to 2048 tokens, K 64 to 17408, N
+// 16 to 17408: the choice is 2.4 % slower than the best measured one on
+// average.  For example 1 token, K = 17408, N = 5120: split 1 / 4 / 6 took
+// 38.6 / 17.3 / 16.3 us; 727 tokens, K = 512, N = 91: tiles of 16 / 256
+// tokens 4.1 / 19.7 us.
 struct Q8Plan {
-  int nt;                               // token tile
-  long long tiles;
-  size_t off_part, off_codes, off_s, total;
+  int nt, cps, split;
 };
 
-constexpr size_t kQ8ZeroBytes = 4096;  // the arrival counters
-static_assert(kQ8MaxCtas * 4 * 4 <= kQ8ZeroBytes, "counters fit");
+// Clusters of 1 .. 8 CTAs that fit at one CTA per SM (the GPU's answer,
+// cudaOccupancyMaxActiveClusters; a cluster stays inside one of its
+// processing clusters).
+constexpr int kQ8Clusters[kQ8MaxSplit + 1] = {0, 148, 74, 45, 33, 26, 22, 15, 15};
 
 Q8Plan q8_plan(int64_t M, int64_t K, int64_t N) {
-  Q8Plan P{};
-  P.nt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
-  P.tiles = ((N + kQ8Rows - 1) / kQ8Rows) * ((M + P.nt - 1) / P.nt);
-  P.off_part = kQ8ZeroBytes;
-  P.off_codes = P.off_part + size_t(kQ8MaxCtas) * 2 * P.nt * kQ8Rows * 4;
-  P.off_s = round_up(P.off_codes + size_t(M) * K, 256);
-  P.total = P.off_s + round_up(size_t(M) * 4, 256);
-  return P;
+  const int64_t kb = (K + kQ8BK - 1) / kQ8BK, rows = (N + kQ8Rows - 1) / kQ8Rows;
+  Q8Plan best{};
+  double least = 1e300;
+  for (const int nt : {16, 32, 64, 128, 256}) {
+    const int64_t tokens = (M + nt - 1) / nt;
+    if ((nt > 16 && nt >= 2 * M) || tokens > 65535) continue;
+    for (int split = 1; split <= kQ8MaxSplit && split <= kb; ++split) {
+      const double ctas = double(rows * tokens) * split, fit = kQ8Clusters[split] * split;
+      const int cps = nt <= 128 && ctas > fit ? 2 : 1;
+      const double slots = fit * cps, rounds = ctas > slots ? std::ceil(ctas / slots) : 1.0;
+      const double share = std::max(1.0, std::min(ctas, slots) / fit);
+      const double stage = double(kQ8Rows + nt) * kQ8BK;
+      const double stages = std::min(12.0, std::floor(((cps == 1 ? 232448 : 115712) - 2048) / stage));
+      const double step = std::max({stage / 89 * share, 1275 / stages, 1.1 * nt * share});
+      const double epilogue = split == 1 ? 38 + 34.0 * nt : 812 + 0.8 * nt + 89.0 * nt / split;
+      const double t = std::max(rounds * (double((kb + split - 1) / split) * step + epilogue * share),
+                                double(N * K + M * K) / 2010);
+      if (t < least) {
+        least = t;
+        best = Q8Plan{nt, cps, split};
+      }
+    }
+  }
+  return best;
+}
+
+// Workspace of the layer: the quantised activations.
+struct Q8Ws {
+  size_t off_s, total;
+};
+Q8Ws q8_ws(int64_t M, int64_t K) {
+  Q8Ws w;
+  w.off_s = round_up(size_t(M) * K, 256);
+  w.total = w.off_s + round_up(size_t(M) * 4, 256);
+  return w;
 }
 
 cudaError_t q8_quantize(const void* x, int f32, int64_t R, int64_t K, int rotate, int8_t* codes, float* s,
@@ -57,8 +97,15 @@ bool byte_map(CUtensorMap* m, const void* data, int64_t cols, int64_t rows, uint
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+template <int NT, int CPS>
+cudaError_t q8_launch(const CUtensorMap& tw, const CUtensorMap& tx, const Q8Params& p, int split, cudaStream_t st) {
+  const dim3 grid(unsigned((p.N + kQ8Rows - 1) / kQ8Rows * split), unsigned((p.M + NT - 1) / NT));
+  return launch_pdl_cluster(int8_gemm_kernel<NT, CPS>, grid, dim3(kQ8Threads), unsigned(split), Q8Cfg<NT, CPS>::kSmem, st,
+                            tw, tx, p);
+}
+
 w4a8_status q8_gemm(const int8_t* x_q, const float* s_x, int64_t M, const int8_t* w_q, const float* s_w, int64_t N,
-                    int64_t K, uint16_t* y, uint8_t* ws, const DeviceState* d, cudaStream_t st) {
+                    int64_t K, uint16_t* y, const DeviceState* d, cudaStream_t st) {
   const Q8Plan P = q8_plan(M, K, N);
   CUtensorMap tw, tx;
   if (!byte_map(&tw, w_q, K, N, kQ8BK, kQ8Rows, CU_TENSOR_MAP_SWIZZLE_128B) ||
@@ -68,28 +115,21 @@ w4a8_status q8_gemm(const int8_t* x_q, const float* s_x, int64_t M, const int8_t
   p.s_x = s_x;
   p.s_w = s_w;
   p.y = y;
-  p.counters = reinterpret_cast<unsigned*>(ws);
-  p.part = reinterpret_cast<int*>(ws + P.off_part);
   p.err = d->err;
   p.M = int(M);
   p.N = int(N);
-  p.K = int(K);
   p.KB = int((K + kQ8BK - 1) / kQ8BK);
-  p.TM = int((M + P.nt - 1) / P.nt);
-  p.items = P.tiles * p.KB;
-  const int ctas = std::min(d->sms, kQ8MaxCtas);
-  // Tiles cut between CTAs cost a partial tile's write and read; with many
-  // tiles to a CTA an uneven last round costs less.
-  p.whole = P.tiles >= 8ll * ctas;
-  p.G = int(std::min<long long>(ctas, p.items));
-  const dim3 grid{unsigned(p.G)}, block{kQ8Threads};
   cudaError_t e;
-  switch (P.nt) {
-    case 16: e = launch_pdl(int8_gemm_kernel<16>, grid, block, Q8Cfg<16>::kSmem, st, tw, tx, p); break;
-    case 32: e = launch_pdl(int8_gemm_kernel<32>, grid, block, Q8Cfg<32>::kSmem, st, tw, tx, p); break;
-    case 64: e = launch_pdl(int8_gemm_kernel<64>, grid, block, Q8Cfg<64>::kSmem, st, tw, tx, p); break;
-    case 128: e = launch_pdl(int8_gemm_kernel<128>, grid, block, Q8Cfg<128>::kSmem, st, tw, tx, p); break;
-    default: e = launch_pdl(int8_gemm_kernel<256>, grid, block, Q8Cfg<256>::kSmem, st, tw, tx, p); break;
+  switch (P.nt * 2 + P.cps - 1) {
+    case 32: e = q8_launch<16, 1>(tw, tx, p, P.split, st); break;
+    case 33: e = q8_launch<16, 2>(tw, tx, p, P.split, st); break;
+    case 64: e = q8_launch<32, 1>(tw, tx, p, P.split, st); break;
+    case 65: e = q8_launch<32, 2>(tw, tx, p, P.split, st); break;
+    case 128: e = q8_launch<64, 1>(tw, tx, p, P.split, st); break;
+    case 129: e = q8_launch<64, 2>(tw, tx, p, P.split, st); break;
+    case 256: e = q8_launch<128, 1>(tw, tx, p, P.split, st); break;
+    case 257: e = q8_launch<128, 2>(tw, tx, p, P.split, st); break;
+    default: e = q8_launch<256, 1>(tw, tx, p, P.split, st); break;
   }
   return e == cudaSuccess ? W4A8_OK : W4A8_ERR_CUDA;
 }
@@ -184,11 +224,15 @@ cudaError_t ka_launch(const KaParams& p, const w4a8_kv_cache* c, int ctas, cudaS
 bool int8_allow_smem() {
   return allow_smem(int8_quant_kernel<false>, size_t(kMaxK) * 4) == cudaSuccess &&
          allow_smem(int8_quant_kernel<true>, size_t(kMaxK) * 4) == cudaSuccess &&
-         allow_smem(int8_gemm_kernel<16>, Q8Cfg<16>::kSmem) == cudaSuccess &&
-         allow_smem(int8_gemm_kernel<32>, Q8Cfg<32>::kSmem) == cudaSuccess &&
-         allow_smem(int8_gemm_kernel<64>, Q8Cfg<64>::kSmem) == cudaSuccess &&
-         allow_smem(int8_gemm_kernel<128>, Q8Cfg<128>::kSmem) == cudaSuccess &&
-         allow_smem(int8_gemm_kernel<256>, Q8Cfg<256>::kSmem) == cudaSuccess &&
+         allow_smem(int8_gemm_kernel<16, 2>, Q8Cfg<16, 2>::kSmem) == cudaSuccess &&
+         allow_smem(int8_gemm_kernel<16, 1>, Q8Cfg<16, 1>::kSmem) == cudaSuccess &&
+         allow_smem(int8_gemm_kernel<32, 2>, Q8Cfg<32, 2>::kSmem) == cudaSuccess &&
+         allow_smem(int8_gemm_kernel<32, 1>, Q8Cfg<32, 1>::kSmem) == cudaSuccess &&
+         allow_smem(int8_gemm_kernel<64, 2>, Q8Cfg<64, 2>::kSmem) == cudaSuccess &&
+         allow_smem(int8_gemm_kernel<64, 1>, Q8Cfg<64, 1>::kSmem) == cudaSuccess &&
+         allow_smem(int8_gemm_kernel<128, 2>, Q8Cfg<128, 2>::kSmem) == cudaSuccess &&
+         allow_smem(int8_gemm_kernel<128, 1>, Q8Cfg<128, 1>::kSmem) == cudaSuccess &&
+         allow_smem(int8_gemm_kernel<256, 1>, Q8Cfg<256, 1>::kSmem) == cudaSuccess &&
          allow_smem(kv_update_kernel<64>, 128 * 64 * 4) == cudaSuccess &&
          allow_smem(kv_update_kernel<128>, 128 * 128 * 4) == cudaSuccess &&
          allow_smem(kv_update_kernel<256>, 128 * 256 * 4) == cudaSuccess &&
@@ -225,20 +269,18 @@ w4a8_status w4a8_int8_quantize(const void* x, int32_t x_is_f32, int64_t R, int64
   return status_of(q8_quantize(x, x_is_f32, R, K, rotate, codes, s, static_cast<cudaStream_t>(stream)));
 }
 
-size_t w4a8_int8_linear_workspace_bytes(int64_t M, int64_t K, int64_t N) {
-  return q8_shape_ok(M, N, K, 0) ? q8_plan(M, K, N).total : 0;
-}
-
 w4a8_status w4a8_int8_gemm(const int8_t* x_q, const float* s_x, int64_t M, const int8_t* w_q, const float* s_w,
-                           int64_t N, int64_t K, uint16_t* y, void* workspace, size_t workspace_bytes, void* stream) {
-  if (!x_q || !s_x || !w_q || !s_w || !y || !workspace) return W4A8_ERR_NULL;
+                           int64_t N, int64_t K, uint16_t* y, void* stream) {
+  if (!x_q || !s_x || !w_q || !s_w || !y) return W4A8_ERR_NULL;
   if (!q8_shape_ok(M, N, K, 0)) return W4A8_ERR_SHAPE;
-  if (!aligned16(x_q) || !aligned16(s_x) || !aligned16(w_q) || !aligned16(s_w) || !aligned16(y) || !aligned16(workspace))
-    return W4A8_ERR_ALIGN;
-  if (workspace_bytes < q8_plan(M, K, N).total) return W4A8_ERR_WORKSPACE;
+  if (!aligned16(x_q) || !aligned16(s_x) || !aligned16(w_q) || !aligned16(s_w) || !aligned16(y)) return W4A8_ERR_ALIGN;
   DeviceState* d = nullptr;
   if (w4a8_status st = int8_state(&d); st != W4A8_OK) return st;
-  return q8_gemm(x_q, s_x, M, w_q, s_w, N, K, y, static_cast<uint8_t*>(workspace), d, static_cast<cudaStream_t>(stream));
+  return q8_gemm(x_q, s_x, M, w_q, s_w, N, K, y, d, static_cast<cudaStream_t>(stream));
+}
+
+size_t w4a8_int8_linear_workspace_bytes(int64_t M, int64_t K, int64_t N) {
+  return q8_shape_ok(M, N, K, 0) ? q8_ws(M, K).total : 0;
 }
 
 w4a8_status w4a8_int8_linear(const uint16_t* x, int64_t M, int64_t K, int32_t rotate, const int8_t* w_q,
@@ -247,16 +289,15 @@ w4a8_status w4a8_int8_linear(const uint16_t* x, int64_t M, int64_t K, int32_t ro
   if (!x || !w_q || !s_w || !y || !workspace) return W4A8_ERR_NULL;
   if (!q8_shape_ok(M, N, K, rotate)) return W4A8_ERR_SHAPE;
   if (!aligned16(x) || !aligned16(w_q) || !aligned16(s_w) || !aligned16(y) || !aligned16(workspace)) return W4A8_ERR_ALIGN;
-  const Q8Plan P = q8_plan(M, K, N);
-  if (workspace_bytes < P.total) return W4A8_ERR_WORKSPACE;
+  const Q8Ws w = q8_ws(M, K);
+  if (workspace_bytes < w.total) return W4A8_ERR_WORKSPACE;
   DeviceState* d = nullptr;
   if (w4a8_status st = int8_state(&d); st != W4A8_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
-  int8_t* codes = reinterpret_cast<int8_t*>(ws + P.off_codes);
-  float* s_x = reinterpret_cast<float*>(ws + P.off_s);
+  int8_t* codes = static_cast<int8_t*>(workspace);
+  float* s_x = reinterpret_cast<float*>(codes + w.off_s);
   if (q8_quantize(x, 0, M, K, rotate, codes, s_x, s) != cudaSuccess) return W4A8_ERR_CUDA;
-  return q8_gemm(codes, s_x, M, w_q, s_w, N, K, y, ws, d, s);
+  return q8_gemm(codes, s_x, M, w_q, s_w, N, K, y, d, s);
 }
 
 w4a8_status w4a8_qk_norm_rope(const w4a8_heads* q, const w4a8_heads* k, int64_t T, int32_t D, const float* q_weight,
