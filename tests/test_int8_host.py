@@ -20,6 +20,27 @@ NULL, SHAPE, ALIGN, WORKSPACE = 1, 2, 3, 4
 P = 4096            # an aligned address that nothing reads
 
 
+class Heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("heads", ctypes.c_int32)]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("factor", ctypes.c_float)]
+
+
+class CacheDesc(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("pages", ctypes.c_int64), ("kv_heads", ctypes.c_int32),
+                ("page", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class BatchDesc(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("q_start", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("batch", ctypes.c_int64), ("tokens", ctypes.c_int64)]
+
+
 @pytest.fixture(scope="module")
 def B():
     import __graft_entry__
@@ -57,6 +78,14 @@ def test_header_is_plain_c(B):
     assert subprocess.run([os.path.join(out, "a")]).returncode == 0
 
 
+def test_packed_descriptors_are_the_headers_structs(B):
+    same = lambda fmt, vals, s: fmt.pack(*vals, *([0] if fmt is not B._BATCH else [])) == bytes(s(*vals))
+    assert same(B._HEADS, (4096, 1 << 33, 72, 5), Heads)
+    assert same(B._ROPE, (4096, 64, 1, 1.5), Rope)
+    assert same(B._CACHE, (1 << 40, 2 << 40, 3 << 40, 4 << 40, 77, 8, 16, 128), CacheDesc)
+    assert same(B._BATCH, (1 << 40, 9, 2 << 40, 3 << 40, 4, 5), BatchDesc)
+
+
 def test_int8_layer_refusals(lib):
     ws = lib.w4a8_int8_linear_workspace_bytes(5, 512, 64)
     assert ws >= 5 * 512 + 5 * 4
@@ -89,18 +118,18 @@ def test_int8_layer_refusals(lib):
 
 
 def _heads(B, heads=4, d=128, data=P, token=None, head=None):
-    return B.Heads(data, heads * d if token is None else token, d if head is None else head, heads)
+    return Heads(data, heads * d if token is None else token, d if head is None else head, heads)
 
 
 def _qk(B, lib, q=None, k=None, t=3, d=128, qw=P, kw=P, pos=P, rope=None, qo=None, ko=None):
-    r = rope or B.Rope(P, 64, 0, 1.0)
+    r = rope or Rope(P, 64, 0, 1.0)
     ref = lambda x, y: ctypes.byref(x if x is not None else y)
     return lib.w4a8_qk_norm_rope(ref(q, _heads(B)), ref(k, _heads(B, 2)), t, d, qw, kw, 1e-6, pos, ctypes.byref(r),
                                  ref(qo, _heads(B)), ref(ko, _heads(B, 2)), None)
 
 
 def test_norm_rope_refusals(B, lib):
-    none = B.Heads(None, 0, 0, 0)
+    none = Heads(None, 0, 0, 0)
     assert _qk(B, lib, q=none, k=none) == NULL
     assert _qk(B, lib, qo=none) == NULL
     assert _qk(B, lib, pos=None) == NULL
@@ -113,21 +142,21 @@ def test_norm_rope_refusals(B, lib):
     assert _qk(B, lib, qw=P + 4) == ALIGN
     assert _qk(B, lib, pos=P + 2) == ALIGN
     for rot in (0, 8, 24, 144):
-        assert _qk(B, lib, rope=B.Rope(P, rot, 0, 1.0)) == SHAPE
-    assert _qk(B, lib, rope=B.Rope(P + 4, 64, 0, 1.0)) == ALIGN
+        assert _qk(B, lib, rope=Rope(P, rot, 0, 1.0)) == SHAPE
+    assert _qk(B, lib, rope=Rope(P + 4, 64, 0, 1.0)) == ALIGN
 
 
 def _cache(B, pages=10, heads=2, page=16, d=128, data=P):
-    return B.CacheDesc(data, P, P, P, pages, heads, page, d)
+    return CacheDesc(data, P, P, P, pages, heads, page, d)
 
 
 def _batch(B, batch=2, tokens=3, width=4, table=P):
-    return B.BatchDesc(table, width, P, P, batch, tokens)
+    return BatchDesc(table, width, P, P, batch, tokens)
 
 
 def _update(B, lib, cache=None, batch=None, k=None, v=None, q=None, qo=None, rope=None, pos=None):
-    none = B.Heads(None, 0, 0, 0)
-    r = rope or B.Rope(P, 64, 0, 1.0)
+    none = Heads(None, 0, 0, 0)
+    r = rope or Rope(P, 64, 0, 1.0)
     ref = ctypes.byref
     return lib.w4a8_kv_update(ref(cache or _cache(B)), ref(batch or _batch(B)), ref(k or _heads(B, 2)), ref(v or _heads(B, 2)),
                               ref(q or none), None, P, 1e-6, pos, ref(r), ref(qo or none), None)
@@ -152,7 +181,7 @@ def test_cache_refusals(B, lib, bad):
 
 
 def test_update_and_attention_refusals(B, lib):
-    none = B.Heads(None, 0, 0, 0)
+    none = Heads(None, 0, 0, 0)
     assert _update(B, lib, cache=_cache(B, data=None)) == NULL
     assert _update(B, lib, cache=_cache(B, data=P + 8)) == ALIGN
     assert _update(B, lib, batch=_batch(B, table=None)) == NULL
@@ -164,7 +193,7 @@ def test_update_and_attention_refusals(B, lib):
     assert _update(B, lib, k=_heads(B, 4)) == SHAPE              # the cache has 2 heads
     assert _update(B, lib, q=_heads(B)) == NULL                  # q without q_out
     assert _update(B, lib, q=_heads(B), qo=_heads(B, 3)) == SHAPE
-    assert _update(B, lib, rope=B.Rope(P, 40, 0, 1.0)) == SHAPE
+    assert _update(B, lib, rope=Rope(P, 40, 0, 1.0)) == SHAPE
     assert _update(B, lib, pos=P + 1) == ALIGN
     assert _attend(B, lib, q=none) == NULL
     assert _attend(B, lib, ws=None) == NULL

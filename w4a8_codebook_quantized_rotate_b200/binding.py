@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -42,32 +43,6 @@ class ChainLayer(ctypes.Structure):
     """w4a8_chain_layer: one layer of a chain (device pointers)."""
     _fields_ = [("packed", ctypes.c_void_p), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
                 ("x", ctypes.c_void_p), ("y", ctypes.c_void_p)]
-
-
-class Heads(ctypes.Structure):
-    """w4a8_heads: bf16 rows [token][head][D] (element strides)."""
-    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
-                ("heads", ctypes.c_int32)]
-
-
-class Rope(ctypes.Structure):
-    """w4a8_rope: the position rotation (device fp64 frequencies)."""
-    _fields_ = [("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
-                ("factor", ctypes.c_float)]
-
-
-class CacheDesc(ctypes.Structure):
-    """w4a8_kv_cache: an int8 paged cache (device pointers)."""
-    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
-                ("v_scales", ctypes.c_void_p), ("pages", ctypes.c_int64), ("kv_heads", ctypes.c_int32),
-                ("page", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
-
-
-class BatchDesc(ctypes.Structure):
-    """w4a8_kv_batch: the sequences of a call (device index arrays)."""
-    _fields_ = [("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("q_start", ctypes.c_void_p),
-                ("kv_len", ctypes.c_void_p), ("batch", ctypes.c_int64), ("tokens", ctypes.c_int64)]
-
 
 _lib = None
 
@@ -588,30 +563,48 @@ def nvfp4_linear(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
 
 
 # ---------------------------------------------------------------- 8-bit integer path (include/w4a8_int8.h)
+#
+# These calls are short enough on the GPU for the host's share to count: a
+# tensor's checks are one expression, and the descriptors are packed bytes.
 
-def _here(t: torch.Tensor, dtype: torch.dtype, name: str, shape: tuple | None = None) -> torch.Tensor:
-    """A contiguous CUDA tensor of that type (and shape) on the current device."""
+_HEADS = struct.Struct("=QqqiI")    # w4a8_heads: data, token_stride, head_stride, heads, padding
+_ROPE = struct.Struct("=QiifI")     # w4a8_rope: inv_freq, rot_dim, interleaved, factor, padding
+_CACHE = struct.Struct("=QQQQqiiiI")  # w4a8_kv_cache: codes and scales of K and V, pages, kv_heads, page, head_dim, padding
+_BATCH = struct.Struct("=QqQQqq")   # w4a8_kv_batch: table, table_stride, q_start, kv_len, batch, tokens
+_NO_HEADS = _HEADS.pack(0, 0, 0, 0, 0)
+_NO_ROPE = _ROPE.pack(0, 0, 0, 1.0, 0)
+
+
+def _raw_stream(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _refuse(t, dtype, dev, name, shape):
     _cuda(t, dtype, name)
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{torch.cuda.current_device()}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{dev}")
+    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _at(t: torch.Tensor, dtype: torch.dtype, dev: int, name: str, shape: tuple | None = None) -> int:
+    """The address of a contiguous tensor of that type (and shape) on the current device ``dev``."""
+    if t.get_device() != dev or t.dtype is not dtype or not t.is_contiguous() or (shape is not None and t.shape != shape):
+        _refuse(t, dtype, dev, name, shape)
+    return t.data_ptr()
 
 
 def int8_quantize(x: torch.Tensor, rotate: bool = True, stream=None):
     """x [R, K] (bf16 or fp32) -> (codes int8 [R, K], s fp32 [R]): one scale per
     row (output channels of a weight, tokens of an activation)."""
-    lib = load_library()
     if x.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("x must be bf16 or fp32")
-    _here(x, x.dtype, "x")
+    lib, dev = load_library(), torch.cuda.current_device() if x.is_cuda else 0
+    xp = _at(x, x.dtype, dev, "x")
     r, k = x.shape
     codes = torch.empty((r, k), dtype=torch.int8, device=x.device)
     s = torch.empty(r, dtype=torch.float32, device=x.device)
     _check("w4a8_int8_quantize", lib.w4a8_int8_quantize(
-        x.data_ptr(), int(x.dtype == torch.float32), r, k, int(rotate), codes.data_ptr(), s.data_ptr(),
-        _stream(stream)))
+        xp, x.dtype is torch.float32, r, k, bool(rotate), codes.data_ptr(), s.data_ptr(), _raw_stream(stream, dev)))
     return codes, s
 
 
@@ -626,38 +619,38 @@ def int8_linear_workspace(m: int, k: int, n: int, device) -> torch.Tensor:
 def int8_gemm(x_q: torch.Tensor, s_x: torch.Tensor, w_q: torch.Tensor, s_w: torch.Tensor,
               out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """y [M, N] bf16 = s_x s_w (x_q [M, K] int8 times w_q [N, K]^T int8)."""
-    lib = load_library()
-    m, k = _here(x_q, torch.int8, "x_q").shape
+    lib, dev = load_library(), torch.cuda.current_device()
+    xp = _at(x_q, torch.int8, dev, "x_q")
+    m, k = x_q.shape
     n = w_q.shape[0]
-    _here(w_q, torch.int8, "w_q", (n, k))
-    _here(s_x, torch.float32, "s_x", (m,))
-    _here(s_w, torch.float32, "s_w", (n,))
+    wp, sp = _at(w_q, torch.int8, dev, "w_q", (n, k)), _at(s_w, torch.float32, dev, "s_w", (n,))
+    sx = _at(s_x, torch.float32, dev, "s_x", (m,))
     if out is None:
         out = torch.empty((m, n), dtype=torch.bfloat16, device=x_q.device)
-    _here(out, torch.bfloat16, "out", (m, n))
-    _check("w4a8_int8_gemm", lib.w4a8_int8_gemm(
-        x_q.data_ptr(), s_x.data_ptr(), m, w_q.data_ptr(), s_w.data_ptr(), n, k, out.data_ptr(),
-        _stream(stream)))
+    status = lib.w4a8_int8_gemm(xp, sx, m, wp, sp, n, k, _at(out, torch.bfloat16, dev, "out", (m, n)),
+                                _raw_stream(stream, dev))
+    if status:
+        raise W4A8Error("w4a8_int8_gemm", status)
     return out
 
 
 def int8_linear(x: torch.Tensor, w_q: torch.Tensor, s_w: torch.Tensor, rotate: bool = True,
                 workspace: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The int8 layer on bf16 x [M, K] against weights from int8_quantize(w, rotate)."""
-    lib = load_library()
-    m, k = _here(x, torch.bfloat16, "x").shape
+    lib, dev = load_library(), torch.cuda.current_device()
+    xp = _at(x, torch.bfloat16, dev, "x")
+    m, k = x.shape
     n = w_q.shape[0]
-    _here(w_q, torch.int8, "w_q", (n, k))
-    _here(s_w, torch.float32, "s_w", (n,))
+    wp, sp = _at(w_q, torch.int8, dev, "w_q", (n, k)), _at(s_w, torch.float32, dev, "s_w", (n,))
     if workspace is None:
         workspace = int8_linear_workspace(m, k, n, x.device)
-    _here(workspace, torch.uint8, "workspace")
     if out is None:
-        out = torch.empty((m, n), dtype=torch.bfloat16, device=x.device)
-    _here(out, torch.bfloat16, "out", (m, n))
-    _check("w4a8_int8_linear", lib.w4a8_int8_linear(
-        x.data_ptr(), m, k, int(rotate), w_q.data_ptr(), s_w.data_ptr(), n, out.data_ptr(), workspace.data_ptr(),
-        workspace.numel(), _stream(stream)))
+        out = x.new_empty((m, n))
+    status = lib.w4a8_int8_linear(xp, m, k, bool(rotate), wp, sp, n, _at(out, torch.bfloat16, dev, "out", (m, n)),
+                                  _at(workspace, torch.uint8, dev, "workspace"), workspace.numel(),
+                                  _raw_stream(stream, dev))
+    if status:
+        raise W4A8Error("w4a8_int8_linear", status)
     return out
 
 
@@ -693,35 +686,30 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str | None = 
     return inv.to(device), attention
 
 
-def _heads(t: torch.Tensor | None, name: str, tokens: int | None = None, dim: int | None = None) -> Heads:
+def _heads(t: torch.Tensor, dev: int, name: str, tokens: int, dim: int) -> bytes:
     """bf16 [tokens, heads, D] with contiguous D -> w4a8_heads."""
-    if t is None:
-        return Heads(None, 0, 0, 0)
-    if not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 3:
-        raise ValueError(f"{name} must be a bf16 CUDA tensor [tokens, heads, D]")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{torch.cuda.current_device()}")
-    if t.stride(2) != 1:
+    shape = t.shape
+    if t.get_device() != dev or t.dtype is not torch.bfloat16 or len(shape) != 3:
+        raise ValueError(f"{name} must be a bf16 tensor [tokens, heads, D] on the current CUDA device")
+    if shape[0] != tokens or shape[2] != dim:
+        raise ValueError(f"{name} must be [{tokens}, heads, {dim}], got {tuple(shape)}")
+    token, head, one = t.stride()
+    if one != 1:
         raise ValueError(f"{name}: the values of a head must be contiguous")
-    if (tokens is not None and t.shape[0] != tokens) or (dim is not None and t.shape[2] != dim):
-        raise ValueError(f"{name} must be [{tokens}, heads, {dim}], got {tuple(t.shape)}")
     # a dimension of one row has no stride of its own
-    token = t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
-    head = t.stride(1) if t.shape[1] > 1 else t.shape[2]
-    return Heads(t.data_ptr(), token, head, t.shape[1])
+    if shape[1] == 1:
+        head = dim
+    if tokens == 1:
+        token = shape[1] * dim
+    return _HEADS.pack(t.data_ptr(), token, head, shape[1], 0)
 
 
-def _rope(inv_freq, interleaved, factor) -> Rope:
+def _rope(inv_freq, interleaved, factor, dev) -> bytes:
     if inv_freq is None:
-        return Rope(None, 0, 0, 1.0)
+        return _NO_ROPE
     if inv_freq.dim() != 1:
         raise ValueError("inv_freq must be [rot_dim / 2]")
-    _here(inv_freq, torch.float64, "inv_freq")
-    return Rope(inv_freq.data_ptr(), 2 * inv_freq.numel(), int(interleaved), float(factor))
-
-
-def _ptr(t, dtype, name, shape):
-    return None if t is None else _here(t, dtype, name, shape).data_ptr()
+    return _ROPE.pack(_at(inv_freq, torch.float64, dev, "inv_freq"), 2 * inv_freq.shape[0], bool(interleaved), factor, 0)
 
 
 def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, positions: torch.Tensor | None = None,
@@ -731,24 +719,30 @@ def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, positions: torc
     """RMS norm of every head of q [T, Hq, D] and k [T, Hk, D] (a weight of None
     leaves the norm out) and the rotation by ``positions`` [T] int32 and
     ``inv_freq`` (rope_frequencies; None: no rotation).  Returns (q_out, k_out)."""
-    lib = load_library()
     some = q if q is not None else k
     if some is None:
         raise ValueError("q or k is needed")
-    t, d = some.shape[0], some.shape[2]
-    if q is not None and q_out is None:
-        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    if k is not None and k_out is None:
-        k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=k.device)
-    q_out, k_out = (q_out if q is not None else None), (k_out if k is not None else None)
-    qs, ks = _heads(q, "q", t, d), _heads(k, "k", t, d)
-    qo, ko = _heads(q_out, "q_out", t, d), _heads(k_out, "k_out", t, d)
-    rope = _rope(inv_freq, interleaved, rope_factor)
-    _check("w4a8_qk_norm_rope", lib.w4a8_qk_norm_rope(
-        ctypes.byref(qs), ctypes.byref(ks), t, d, _ptr(q_weight, torch.float32, "q_weight", (d,)),
-        _ptr(k_weight, torch.float32, "k_weight", (d,)), float(eps), _ptr(positions, torch.int32, "positions", (t,)),
-        ctypes.byref(rope), ctypes.byref(qo), ctypes.byref(ko), _stream(stream)))
-    return q_out, k_out
+    if not some.is_cuda:
+        raise ValueError("q and k must be CUDA tensors")
+    lib, dev = load_library(), torch.cuda.current_device()
+    t, _, d = some.shape
+    qs = qo = ks = ko = _NO_HEADS
+    if q is not None:
+        if q_out is None:
+            q_out = q.new_empty(q.shape)
+        qs, qo = _heads(q, dev, "q", t, d), _heads(q_out, dev, "q_out", t, d)
+    if k is not None:
+        if k_out is None:
+            k_out = k.new_empty(k.shape)
+        ks, ko = _heads(k, dev, "k", t, d), _heads(k_out, dev, "k_out", t, d)
+    status = lib.w4a8_qk_norm_rope(
+        qs, ks, t, d, None if q_weight is None else _at(q_weight, torch.float32, dev, "q_weight", (d,)),
+        None if k_weight is None else _at(k_weight, torch.float32, dev, "k_weight", (d,)), eps,
+        None if positions is None else _at(positions, torch.int32, dev, "positions", (t,)),
+        _rope(inv_freq, interleaved, rope_factor, dev), qo, ko, _raw_stream(stream, dev))
+    if status:
+        raise W4A8Error("w4a8_qk_norm_rope", status)
+    return (q_out if q is not None else None), (k_out if k is not None else None)
 
 
 class KvCache:
@@ -757,9 +751,9 @@ class KvCache:
 
     def __init__(self, pages: int, kv_heads: int, page: int, head_dim: int, device="cuda"):
         shape = (pages, kv_heads, page, head_dim)
-        self._set(torch.zeros(shape, dtype=torch.int8, device=device), torch.zeros(shape, dtype=torch.int8, device=device),
-                  torch.zeros(shape[:2], dtype=torch.float32, device=device),
-                  torch.zeros(shape[:2], dtype=torch.float32, device=device))
+        code = lambda: torch.zeros(shape, dtype=torch.int8, device=device)
+        scale = lambda: torch.zeros(shape[:2], dtype=torch.float32, device=device)
+        self._set(code(), code(), scale(), scale())
 
     @classmethod
     def of(cls, k_codes: torch.Tensor, v_codes: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor) -> "KvCache":
@@ -769,25 +763,29 @@ class KvCache:
         return self
 
     def _set(self, k_codes, v_codes, k_scales, v_scales):
-        if k_codes.dim() != 4:
-            raise ValueError("codes must be [pages, kv_heads, page, D]")
-        shape = tuple(k_codes.shape)
-        _here(k_codes, torch.int8, "k_codes")
-        _here(v_codes, torch.int8, "v_codes", shape)
-        _here(k_scales, torch.float32, "k_scales", shape[:2])
-        _here(v_scales, torch.float32, "v_scales", shape[:2])
+        if k_codes.dim() != 4 or not k_codes.is_cuda:
+            raise ValueError("codes must be CUDA tensors [pages, kv_heads, page, D]")
+        shape, dev = tuple(k_codes.shape), k_codes.get_device()
+        at = (_at(k_codes, torch.int8, dev, "k_codes"), _at(v_codes, torch.int8, dev, "v_codes", shape),
+              _at(k_scales, torch.float32, dev, "k_scales", shape[:2]), _at(v_scales, torch.float32, dev, "v_scales", shape[:2]))
         self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
         self.pages, self.kv_heads, self.page, self.head_dim = shape
-        self.desc = CacheDesc(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), *shape)
+        self.device_index, self.desc = dev, _CACHE.pack(*at, *shape, 0)
 
 
-def _batch(block_table: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor, tokens: int) -> BatchDesc:
+def _cache_desc(cache: KvCache, dev: int) -> bytes:
+    if cache.device_index != dev:
+        raise ValueError(f"the cache is on cuda:{cache.device_index}, not on the current device cuda:{dev}")
+    return cache.desc
+
+
+def _batch(block_table, q_start, kv_len, tokens: int, dev: int) -> bytes:
     if block_table.dim() != 2:
         raise ValueError("block_table must be [batch, pages]")
-    b, width = _here(block_table, torch.int32, "block_table").shape
-    _here(q_start, torch.int32, "q_start", (b + 1,))
-    _here(kv_len, torch.int32, "kv_len", (b,))
-    return BatchDesc(block_table.data_ptr(), width, q_start.data_ptr(), kv_len.data_ptr(), b, tokens)
+    table = _at(block_table, torch.int32, dev, "block_table")
+    b, width = block_table.shape
+    return _BATCH.pack(table, width, _at(q_start, torch.int32, dev, "q_start", (b + 1,)),
+                       _at(kv_len, torch.int32, dev, "kv_len", (b,)), b, tokens)
 
 
 def kv_update(cache: KvCache, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor, q_start: torch.Tensor,
@@ -800,31 +798,34 @@ def kv_update(cache: KvCache, k: torch.Tensor, v: torch.Tensor, block_table: tor
     Sequence b's rows are q_start[b] .. q_start[b + 1], the last of its
     kv_len[b] tokens; positions None: the places in the sequences.  Returns
     q_out (None without q)."""
-    lib = load_library()
+    lib, dev = load_library(), torch.cuda.current_device()
     t, d = k.shape[0], cache.head_dim
-    if q is not None and q_out is None:
-        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    q_out = q_out if q is not None else None
-    ks, vs = _heads(k, "k", t, d), _heads(v, "v", t, d)
-    qs, qo = _heads(q, "q", t, d), _heads(q_out, "q_out", t, d)
-    batch = _batch(block_table, q_start, kv_len, t)
-    rope = _rope(inv_freq, interleaved, rope_factor)
-    _check("w4a8_kv_update", lib.w4a8_kv_update(
-        ctypes.byref(cache.desc), ctypes.byref(batch), ctypes.byref(ks), ctypes.byref(vs), ctypes.byref(qs),
-        _ptr(q_weight, torch.float32, "q_weight", (d,)), _ptr(k_weight, torch.float32, "k_weight", (d,)), float(eps),
-        _ptr(positions, torch.int32, "positions", (t,)), ctypes.byref(rope), ctypes.byref(qo), _stream(stream)))
-    return q_out
+    qs = qo = _NO_HEADS
+    if q is not None:
+        if q_out is None:
+            q_out = q.new_empty(q.shape)
+        qs, qo = _heads(q, dev, "q", t, d), _heads(q_out, dev, "q_out", t, d)
+    status = lib.w4a8_kv_update(
+        _cache_desc(cache, dev), _batch(block_table, q_start, kv_len, t, dev), _heads(k, dev, "k", t, d),
+        _heads(v, dev, "v", t, d), qs, None if q_weight is None else _at(q_weight, torch.float32, dev, "q_weight", (d,)),
+        None if k_weight is None else _at(k_weight, torch.float32, dev, "k_weight", (d,)), eps,
+        None if positions is None else _at(positions, torch.int32, dev, "positions", (t,)),
+        _rope(inv_freq, interleaved, rope_factor, dev), qo, _raw_stream(stream, dev))
+    if status:
+        raise W4A8Error("w4a8_kv_update", status)
+    return q_out if q is not None else None
 
 
 def kv_dequant(cache: KvCache, ids: torch.Tensor, stream=None):
     """Pages ``ids`` [n] int32 -> (k, v) bf16 [n, kv_heads, page, D]."""
-    lib = load_library()
-    _here(ids, torch.int32, "ids", (ids.numel(),))
-    shape = (ids.numel(), cache.kv_heads, cache.page, cache.head_dim)
-    k = torch.empty(shape, dtype=torch.bfloat16, device=ids.device)
-    v = torch.empty(shape, dtype=torch.bfloat16, device=ids.device)
-    _check("w4a8_kv_dequant", lib.w4a8_kv_dequant(ctypes.byref(cache.desc), ids.data_ptr(), shape[0], k.data_ptr(),
-                                                  v.data_ptr(), _stream(stream)))
+    lib, dev = load_library(), torch.cuda.current_device()
+    n = ids.shape[0]
+    at = _at(ids, torch.int32, dev, "ids", (n,))
+    out = torch.empty((2, n, cache.kv_heads, cache.page, cache.head_dim), dtype=torch.bfloat16, device=ids.device)
+    k, v = out.unbind(0)
+    status = lib.w4a8_kv_dequant(_cache_desc(cache, dev), at, n, k.data_ptr(), v.data_ptr(), _raw_stream(stream, dev))
+    if status:
+        raise W4A8Error("w4a8_kv_dequant", status)
     return k, v
 
 
@@ -843,17 +844,16 @@ def kv_attention(q: torch.Tensor, cache: KvCache, block_table: torch.Tensor, q_s
     int8 cache that holds the same tokens; ``scale`` defaults to D ** -0.5,
     ``window`` > 0 keeps the last so many positions.  Rows behind the last
     sequence are left as they were."""
-    lib = load_library()
-    t, hq = q.shape[0], q.shape[1]
-    d = cache.head_dim
+    lib, dev = load_library(), torch.cuda.current_device()
+    t, hq, d = q.shape[0], q.shape[1], cache.head_dim
     if workspace is None:
         workspace = kv_attention_workspace(t, hq, cache.kv_heads, d, q.device)
-    _here(workspace, torch.uint8, "workspace")
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    qs, os_ = _heads(q, "q", t, d), _heads(out, "out", t, d)
-    batch = _batch(block_table, q_start, kv_len, t)
-    _check("w4a8_kv_attention", lib.w4a8_kv_attention(
-        ctypes.byref(qs), ctypes.byref(cache.desc), ctypes.byref(batch), float(d ** -0.5 if scale is None else scale),
-        int(window), ctypes.byref(os_), workspace.data_ptr(), workspace.numel(), _stream(stream)))
+        out = q.new_empty(q.shape)
+    status = lib.w4a8_kv_attention(
+        _heads(q, dev, "q", t, d), _cache_desc(cache, dev), _batch(block_table, q_start, kv_len, t, dev),
+        d ** -0.5 if scale is None else scale, window, _heads(out, dev, "out", t, d),
+        _at(workspace, torch.uint8, dev, "workspace"), workspace.numel(), _raw_stream(stream, dev))
+    if status:
+        raise W4A8Error("w4a8_kv_attention", status)
     return out
