@@ -191,7 +191,7 @@ size_t w4a8_kv_attention_workspace_bytes(int64_t tokens, int32_t q_heads, int32_
  * them (w4a8_kv_update):
  *   out_i = sum_j softmax_j(scale q_i . K_j) V_j,  j <= position of i,
  *   and j > position - window when window > 0,
- * K, V = code * scale.  q, out [tokens][q_heads][D], q_heads a multiple of
+ * K, V = code * scale (a V scale below 2^-80 may count as 0).  q, out [tokens][q_heads][D], q_heads a multiple of
  * kv_heads and at most 128 of them to a key head (head h reads key head
  * h / (q_heads / kv_heads)).
  * Errors: NULL, SHAPE, ALIGN, WORKSPACE, ARCH, CUDA.

@@ -17,7 +17,11 @@ Bars:
     of sum |q_d K_d| scale and moves the weights by twice that.  fp16 holds
     p vs with the row's largest at 2^14 or more (2^15 less one step of its
     running maximum), so a subnormal one is off by at most 2^-25, 2^-39 of the
-    largest; times a code (2^7), for every key.
+    largest; times a code (2^7), for every key.  The tensor-memory kernel puts
+    the largest at 2^7 (and keeps the reference until it grows by 2^8), which
+    makes that 2^-32.  V scales below 2^-80 count as 0, and a key without a V
+    scale enters the reference as one of 2^-80, so what is below 2^-80 2^7 is
+    not kept: 2^-73 in absolute terms.
 """
 
 import numpy as np
@@ -206,22 +210,22 @@ def test_dequant(lib):
 
 # ---------------------------------------------------------------- attention
 
-def check_attention(got, ref, absv, top, share):
+def check_attention(got, ref, absv, top, share, least=2.0 ** -39):
     live = ~np.isnan(ref)
     got = got.double().cpu().numpy()
     assert np.isfinite(got[live]).all()
     bar = 2.0 ** -8 * np.abs(ref) + (2.0 ** -11 + 2.0 ** -16 + 2 * 2.0 ** -18 * top[..., None]) * absv
-    bar = bar + 2.0 ** -39 * 2.0 ** 7 * share[..., None]
+    bar = bar + least * 2.0 ** 7 * share[..., None] + 2.0 ** -73
     over = (np.abs(got - ref) - bar)[live]
     assert over.max() <= 0, f"{(over > 0).sum()} outputs off, worst {over.max():.3e}"
 
 
-def attend(lib, b, hq, d, window=0, q_scale=1.0, **more):
+def attend(lib, b, hq, d, window=0, q_scale=1.0, least=2.0 ** -39):
     q, qx = bf16(b.rng, b.t, hq, d, scale=q_scale)
     out = torch.full_like(q, -3.0)
-    lib.kv_attention(q, b.cache(lib), *b.args(), window=window, out=out, **more)
+    lib.kv_attention(q, b.cache(lib), *b.args(), window=window, out=out)
     assert lib.get_device_error() == 0
-    check_attention(out, *R.attention(qx, b.ref, b.table, b.start, b.kv_len, d ** -0.5, window))
+    check_attention(out, *R.attention(qx, b.ref, b.table, b.start, b.kv_len, d ** -0.5, window), least=least)
     assert (out[int(b.start[-1]):] == -3).all()
 
 
@@ -247,6 +251,41 @@ def test_attention_ragged(lib, page, d):
 ])
 def test_attention_shapes(lib, lens, hq, hk, page, d, window):
     attend(lib, Batch(lens, hk, page, d, sum(a * b for a, b in lens) + d), hq, d, window)
+
+
+@pytest.mark.parametrize("lens,hq,hk,page,d,window", [
+    ([(256, 256)], 32, 32, 16, 128, 0),                # the rows of whole tiles, one group
+    ([(200, 200), (150, 333), (1, 77)], 32, 16, 32, 128, 0),
+    ([(129, 700), (3, 50), (260, 260)], 32, 16, 64, 64, 0),
+    ([(150, 150), (0, 9), (135, 512)], 32, 16, 128, 256, 0),
+    ([(70, 129), (128, 1000)], 64, 16, 16, 256, 0),
+    ([(131, 640), (1, 5)], 56, 8, 16, 64, 0),          # seven heads to a key head
+    ([(300, 900), (1, 300)], 16, 16, 16, 128, 100),    # windows, shorter and longer than a key tile
+    ([(300, 900)], 16, 16, 32, 128, 1),
+    ([(200, 700)], 16, 16, 64, 256, 260),
+    ([(64, 2000)], 64, 32, 64, 128, 0),
+])
+def test_attention_many_new_tokens(lib, lens, hq, hk, page, d, window):
+    """Sequences with enough rows for the tensor-memory kernel, alone and beside short ones."""
+    attend(lib, Batch(lens, hk, page, d, sum(a * b for a, b in lens) + d + window, behind=2), hq, d, window,
+           least=2.0 ** -32)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_attention_many_new_tokens_ranges(lib, d):
+    """As the ranges below, on the tensor-memory kernel; a negative scale, which turns the order of the scores."""
+    b = Batch([(130, 400), (140, 150)], 16, 16, d, d + 1)
+    b.ref.scales[1][:] *= 10.0 ** b.rng.integers(-6, 7, b.ref.scales[1].shape)
+    b.ref.scales[1][::3] = 0.0
+    b.ref.scales[0][::4] = 0.0
+    attend(lib, b, 16, d, q_scale=8.0, least=2.0 ** -32)
+    q, _ = bf16(b.rng, b.t, 16, d)
+    size = (10.0 ** b.rng.integers(-30, 3, (b.t, 16, 1))).astype(np.float32)
+    q = (q.float() * dev(size)).to(torch.bfloat16)
+    for scale in (d ** -0.5, -0.1):
+        got = lib.kv_attention(q, b.cache(lib), *b.args(), scale=scale)
+        check_attention(got, *R.attention(q.double().cpu().numpy(), b.ref, b.table, b.start, b.kv_len, scale),
+                        least=2.0 ** -32)
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])

@@ -210,13 +210,25 @@ cudaError_t ka_launch(const KaParams& p, const w4a8_kv_cache* c, int ctas, cudaS
   using C = KaCfg<D>;
   const int box = std::min(C::TK, int(c->page));
   const auto swizzle = D < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
-  const int64_t rows = c->pages * c->kv_heads * c->page;
+  const int64_t slots = c->pages * c->kv_heads * c->page;
   CUtensorMap tk, tv;
-  if (!byte_map(&tk, c->k_codes, D, rows, C::kRowBytes, uint32_t(box), swizzle) ||
-      !byte_map(&tv, c->v_codes, D, rows, C::kRowBytes, uint32_t(box), swizzle))
+  if (!byte_map(&tk, c->k_codes, D, slots, C::kRowBytes, uint32_t(box), swizzle) ||
+      !byte_map(&tv, c->v_codes, D, slots, C::kRowBytes, uint32_t(box), swizzle))
     return cudaErrorUnknown;
   KaParams q = p;
   q.box_shift = page_shift_of(box);
+  // The tensor-memory kernel goes first where the batch may have rows for it (each kernel decides from the
+  // sequences' lengths which of them are its own).
+  const int64_t rows = int64_t(p.batch.tokens) * p.group;
+  const int64_t units = rows / KpCfg<D>::kRows + std::min<int64_t>(p.batch.batch, rows / kKpMinRows);
+  q.both = (rows / 256 + std::min<int64_t>(p.batch.batch, rows / kKpMinRows)) * c->kv_heads >= kKpMinCtas;
+  if (q.both) {
+    if (units * c->kv_heads >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    if (cudaError_t e = launch_pdl(kv_prefill_kernel<D>, dim3(unsigned(units * c->kv_heads)), dim3(KpCfg<D>::kThreads),
+                                   KpCfg<D>::kSmem, st, q);
+        e != cudaSuccess)
+      return e;
+  }
   return launch_pdl(kv_attention_kernel<D>, dim3(ctas), dim3(kKaThreads), C::kSmem, st, tk, tv, q);
 }
 
@@ -238,7 +250,10 @@ bool int8_allow_smem() {
          allow_smem(kv_update_kernel<256>, 128 * 256 * 4) == cudaSuccess &&
          allow_smem(kv_attention_kernel<64>, KaCfg<64>::kSmem) == cudaSuccess &&
          allow_smem(kv_attention_kernel<128>, KaCfg<128>::kSmem) == cudaSuccess &&
-         allow_smem(kv_attention_kernel<256>, KaCfg<256>::kSmem) == cudaSuccess;
+         allow_smem(kv_attention_kernel<256>, KaCfg<256>::kSmem) == cudaSuccess &&
+         allow_smem(kv_prefill_kernel<64>, KpCfg<64>::kSmem) == cudaSuccess &&
+         allow_smem(kv_prefill_kernel<128>, KpCfg<128>::kSmem) == cudaSuccess &&
+         allow_smem(kv_prefill_kernel<256>, KpCfg<256>::kSmem) == cudaSuccess;
 }
 
 // device_state, and the opt-ins above the first time on a device.
@@ -404,6 +419,7 @@ w4a8_status w4a8_kv_attention(const w4a8_heads* q, const w4a8_kv_cache* cache, c
   p.window = window;
   p.group = q->heads / cache->kv_heads;
   p.box_shift = 0;
+  p.both = 0;
   p.counters = static_cast<unsigned*>(workspace);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kKaZeroBytes);
   p.err = d->err;

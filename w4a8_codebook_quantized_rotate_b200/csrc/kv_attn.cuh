@@ -76,6 +76,7 @@ struct KaParams {
   int window;
   int group;         // query heads of a key head
   int box_shift;     // log2 of a TMA box's rows
+  int both;          // the tensor-memory kernel is launched as well
   float* part;       // [CTA][2][kSlotFloats]
   unsigned* counters;  // [CTA]
   unsigned* err;
@@ -91,7 +92,7 @@ struct KaShared {
   float row_factor[kKaRows];
   long long base;   // first item of sequence b0
   long long total;  // items of the batch
-  int b0;
+  int b0, small_only;
   int last;         // this CTA joins the row tile's partial results
   volatile int abort;
 };
@@ -112,14 +113,36 @@ W4A8_HD int ka_item_cta(long long i, long long total, long long ctas) {
   return int(((i + 1) * ctas + total - 1) / total - 1);
 }
 
+// A sequence of at least kKpMinRows rows (new tokens x query heads of a key
+// head) is left to the tensor-memory kernel (kv_prefill.cuh) when the batch
+// has enough such tiles of 256 rows to occupy the SMs, which that kernel
+// does not split along the keys: it then does about 4.5 TFLOP/s a CTA
+// against 140 for this whole kernel.
+constexpr int kKpMinRows = 128;
+constexpr int kKpMinCtas = 32;
+__device__ __forceinline__ bool kp_takes_big(const KaParams& p) {  // whole warp
+  const int lane = threadIdx.x & 31;
+  long long ctas = 0;
+  for (int b0 = 0; b0 < p.batch.batch; b0 += 32) {
+    if (b0 + lane < p.batch.batch) {
+      const long long rows = (long long)kv_load_seq(p.batch, b0 + lane, p.cache.page_shift).q_len * p.group;
+      if (rows >= kKpMinRows) ctas += (rows + 255) / 256 * p.cache.kv_heads;
+    }
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) ctas += __shfl_xor_sync(0xffffffffu, ctas, off);
+  return ctas >= kKpMinCtas;
+}
+
 // Row tiles of a sequence, and items of each (the same for all of them: a
 // tile skips the keys outside its own range).
 template <int D>
-__device__ __forceinline__ void ka_counts(const KvSeq& s, const KaParams& p, int& tiles, int& items) {
+__device__ __forceinline__ void ka_counts(const KvSeq& s, const KaParams& p, bool small_only, int& tiles, int& items) {
   const KvRange r = kv_range(s, 0, s.q_len - 1, p.window);
   const int lo = r.lo & ~(KaCfg<D>::TK - 1);
   tiles = (s.q_len * p.group + kKaRows - 1) / kKaRows;
   items = s.q_len == 0 ? 0 : (s.kv_len - lo + KaCfg<D>::kItem - 1) / KaCfg<D>::kItem;
+  if (small_only && s.q_len * p.group >= kKpMinRows) tiles = items = 0;
 }
 
 // The row tile at the front of a CTA's range.
@@ -136,10 +159,11 @@ template <int D>
 struct KaWalk {
   long long pos, end, base;
   int b, tiles, items;
+  bool small_only;
   KvSeq s;
   __device__ __forceinline__ void load(const KaParams& p) {
     s = kv_load_seq(p.batch, b, p.cache.page_shift);
-    ka_counts<D>(s, p, tiles, items);
+    ka_counts<D>(s, p, small_only, tiles, items);
   }
   __device__ __forceinline__ bool next(const KaParams& p, KaSeg& g) {
     if (pos >= end) return false;
@@ -231,13 +255,14 @@ __global__ void __launch_bounds__(kKaThreads, 1)
   }
   if (warp == 0) {
     // The batch's items, then the sequence that holds this CTA's first one.
+    const bool small_only = p.both && kp_takes_big(p);
     long long total = 0;
     for (int b0 = 0; b0 < p.batch.batch; b0 += 32) {
       int tiles = 0, items = 0;
       if (b0 + lane < p.batch.batch) {
         const KvSeq s = kv_load_seq(p.batch, b0 + lane, p.cache.page_shift);
         if (s.bad) record_error(p.err, kErrInput);
-        ka_counts<D>(s, p, tiles, items);
+        ka_counts<D>(s, p, small_only, tiles, items);
       }
       total += (long long)p.cache.kv_heads * tiles * items;
     }
@@ -250,7 +275,7 @@ __global__ void __launch_bounds__(kKaThreads, 1)
     for (int b0 = 0; b0 < p.batch.batch && at < 0 && i0 < total; b0 += 32) {
       int tiles = 0, items = 0;
       if (b0 + lane < p.batch.batch)
-        ka_counts<D>(kv_load_seq(p.batch, b0 + lane, p.cache.page_shift), p, tiles, items);
+        ka_counts<D>(kv_load_seq(p.batch, b0 + lane, p.cache.page_shift), p, small_only, tiles, items);
       const long long own = (long long)p.cache.kv_heads * tiles * items;
       long long sum = own;
 #pragma unroll
@@ -270,6 +295,7 @@ __global__ void __launch_bounds__(kKaThreads, 1)
       sh->total = total;
       sh->b0 = at;
       sh->base = base;
+      sh->small_only = small_only;
     }
   }
   __syncthreads();
@@ -282,6 +308,7 @@ __global__ void __launch_bounds__(kKaThreads, 1)
   walk.end = ka_first_item(blockIdx.x + 1, total, ctas);
   walk.base = sh->base;
   walk.b = sh->b0;
+  walk.small_only = sh->small_only;
   walk.load(p);
 
   if (warp == kKaWarps) {

@@ -1,0 +1,528 @@
+// Attention of many new tokens over the int8 paged cache, on the 5th
+// generation tensor cores.  Same mathematics as kv_attn.cuh:
+//
+//   o_i = sum_j P'_ij c_j / sum_j (P'_ij / vs_j),
+//   P'_ij = 2^(t_ij - z_i),  t_ij = q_i . k_j ks_j scale log2(e) + log2(vs_j)
+//
+// with integer codes k_j, c_j (exact in fp16) and z_i the running maximum of
+// t_ij less 7, kept until t grows by more than 8 (so P' stays in fp16's range
+// and the accumulator is rescaled a few times a row, not every tile).
+//
+// A CTA takes 256 rows of one key head (the query heads of the group,
+// neighbouring new tokens) as two tiles of 128, TMEM's lanes (heads of 256:
+// one tile), and walks the keys in tiles of 128 (64).  Roles:
+//   * 4 converter warps expand K and V codes to fp16 in 128-byte-swizzled
+//     shared memory, two stages each, with the loads of the next two tiles
+//     in registers.  Expanding once per 256 rows is what makes the expansion
+//     cheap: its shared-memory writes are a third of the MMAs' reads.
+//   * one thread issues the MMAs: S = Q K^T from shared memory, O += P' V with
+//     P' in TMEM (fp16, in S's place) and V as it lies ([key][d], the
+//     operand's MN-major order), O in TMEM.
+//   * a softmax warpgroup per tile, a thread per row: maximum over the row's
+//     scores, then P' back to TMEM 32 keys at a time.
+// While one tile's softmax runs, the other tile's two products do; with heads
+// of 256 the one tile alternates between two score buffers instead.
+// Bounds: per 256 x 128 (rows x keys) and D = 128 the MMAs take 2048 clocks
+// of an SM, its exponentials (16 a clock) 2048 as well, so the softmax keeps
+// to about four other instructions a score: scores are scaled in the exponent's
+// multiply-add, and the sum of p comes from P' per page (sum of P' / vs).
+#pragma once
+
+#include "common.cuh"
+#include "gemm_tc.cuh"
+#include "kv_attn.cuh"
+#include "kv_cache.cuh"
+
+namespace w4a8 {
+
+constexpr int kKpConvWarps = 4;
+constexpr float kKpLeastScale = 0x1p-80f;  // V scales below count as 0
+
+template <int D>
+struct KpCfg {
+  static constexpr int kTiles = D <= 128 ? 2 : 1;        // row tiles of a CTA
+  static constexpr int TK = D <= 128 ? 128 : 64;         // keys of a tile
+  static constexpr int KG = TK / 16;                     // key groups (one page each)
+  static constexpr int kRows = 128 * kTiles;
+  static constexpr int kSoftWarps = 4 * kTiles;
+  static constexpr int kThreads = 32 * (kSoftWarps + kKpConvWarps + 1);  // softmax, converters, MMA warp
+  static constexpr uint32_t kQ = 128 * D * 2;            // a tile of q, fp16
+  static constexpr uint32_t kKV = TK * D * 2;            // a stage of K or V, fp16
+  static constexpr size_t kSmem = 1024 + kTiles * kQ + 4 * kKV + 1024;
+  static constexpr uint32_t kSCols = TK;                 // fp32 scores; P' takes the first half
+  static constexpr uint32_t kOCol = 2 * kSCols;          // two score buffers, then O of each tile
+  static_assert(kOCol + kTiles * D <= 512, "TMEM");
+  // kind::f16: fp16 A and B, fp32 D, M = 128
+  static constexpr uint32_t kIdescQK = (1u << 4) | (uint32_t(TK >> 3) << 17) | (8u << 24);
+  static constexpr uint32_t kIdescPV = (1u << 4) | (1u << 16) | (uint32_t(D >> 3) << 17) | (8u << 24);  // B MN-major
+};
+
+struct KpShared {
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t s_full[2], p_full[2];
+  uint64_t pv_done;
+  uint64_t drain;
+  float ks[4][8], lv[4][8], iv[4][8];  // ks, log2(vs), 1 / vs of a tile's key groups (ring of 4 tiles)
+  uint32_t tmem_base;
+  int found;
+  int b, tile;
+  volatile int abort;
+};
+
+__device__ __forceinline__ bool kp_wait(uint64_t* bar, uint32_t parity, KpShared* sh, unsigned* err) {
+  for (uint32_t i = 0; i < (1u << 20); ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 1023u) == 1023u && sh->abort) return false;
+  }
+  sh->abort = 1;
+  record_error(err, kErrTimeout);
+  return false;
+}
+
+// D[tmem] (+)= A[smem desc] * B[smem desc], kind::f16.
+__device__ __forceinline__ void tc_mma_ss_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// MN-major operand with 128-byte swizzling: rows (k) of 64 values, 8-row
+// groups 1024 bytes apart (SBO), 64-value blocks `lbo` bytes apart.
+__device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t smem_addr, uint32_t lbo) {
+  return uint64_t((smem_addr >> 4) & 0x3FFFu) | (uint64_t(lbo >> 4) << 16) | (uint64_t(1024 >> 4) << 32) |
+         (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+
+// The row tile (of kRows rows) that unit u is; the tiles of a sequence are
+// taken from its last, whose range of keys is longest.  False past the last
+// one, and where the streaming kernel takes the whole batch.
+template <int D>
+__device__ __forceinline__ bool kp_find(const KaParams& p, int u, int& seq, int& tile) {
+  if (!kp_takes_big(p)) return false;
+  const int lane = threadIdx.x & 31;
+  int before = 0;
+  for (int b0 = 0; b0 < p.batch.batch; b0 += 32) {
+    KvSeq s{0, 0, 0, false};
+    if (b0 + lane < p.batch.batch) s = kv_load_seq(p.batch, b0 + lane, p.cache.page_shift);
+    const int rows = s.q_len * p.group;
+    const int own = rows < kKpMinRows ? 0 : (rows + KpCfg<D>::kRows - 1) / KpCfg<D>::kRows;
+    int sum = own;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, sum, off);
+      if (lane >= off) sum += o;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, before + sum > u);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      seq = b0 + l;
+      tile = __shfl_sync(0xffffffffu, before + sum, l) - 1 - u;
+      return true;
+    }
+    before += __shfl_sync(0xffffffffu, sum, 31);
+  }
+  return false;
+}
+
+template <int D>
+__global__ void __launch_bounds__(KpCfg<D>::kThreads, 1) kv_prefill_kernel(const KaParams p) {
+  using C = KpCfg<D>;
+  extern __shared__ __align__(1024) uint8_t kp_smem[];
+  const uint32_t q0 = (smem_u32(kp_smem) + 1023u) & ~1023u;
+  const uint32_t k0 = q0 + C::kTiles * C::kQ, v0 = k0 + 2 * C::kKV;
+  KpShared* sh = reinterpret_cast<KpShared*>(kp_smem + (v0 + 2 * C::kKV - smem_u32(kp_smem)));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh->k_full[i], kKpConvWarps);
+      mbar_init(&sh->v_full[i], kKpConvWarps);
+      mbar_init(&sh->k_empty[i], 1);
+      mbar_init(&sh->v_empty[i], 1);
+      mbar_init(&sh->s_full[i], 1);
+      mbar_init(&sh->p_full[i], 4);
+    }
+    mbar_init(&sh->pv_done, 1);
+    mbar_init(&sh->drain, 1);
+    sh->abort = 0;
+    fence_barrier_init();
+  }
+  const int head = int(blockIdx.x) % p.cache.kv_heads, unit = int(blockIdx.x) / p.cache.kv_heads;
+  if (warp == 1) {
+    int b = 0, tile = 0;
+    const bool found = kp_find<D>(p, unit, b, tile);
+    if (lane == 0) sh->found = found, sh->b = b, sh->tile = tile;
+  }
+  __syncthreads();
+  if (!sh->found) return;
+  if (warp == 0) {
+    tmem_alloc(&sh->tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh->tmem_base;
+  const KvSeq seq = kv_load_seq(p.batch, sh->b, p.cache.page_shift);
+  const int rows = seq.q_len * p.group, row0 = sh->tile * C::kRows;
+  const int last = min(rows, row0 + C::kRows) - 1;
+  const KvRange range = kv_range(seq, row0 / p.group, last / p.group, p.window);
+  const int key0 = range.lo & ~(C::TK - 1);
+  const int n_tiles = (range.hi - key0 + C::TK - 1) / C::TK;
+  constexpr int kMmaWarp = C::kSoftWarps + kKpConvWarps;
+
+  if (warp < C::kSoftWarps) {
+    // ------------------------------------------------ softmax: a thread per row
+    const int t = warp >> 2, q = warp & 3;
+    const int r = 32 * q + lane;                      // row of the tile, TMEM lane
+    const int row = min(row0 + 128 * t + r, rows - 1);  // rows past the last repeat it and are not stored
+    const bool live = row0 + 128 * t + r < rows;
+    const int j = row / p.group, h = head * p.group + row - j * p.group;
+    const uint32_t trow = uint32_t(32 * q) << 16;
+    float f;
+    {
+      // q to fp16 with the row's power of two, [64-value block][row][128 bytes], swizzled
+      const uint16_t* src = p.q.data + (long long)(seq.start + j) * p.q.token + h * p.q.head;
+      float top = 0.f;
+#pragma unroll 4
+      for (int i = 0; i < D; i += 8) {
+        float v[8];
+        bf16x8_to_float(__ldcg(reinterpret_cast<const uint4*>(src + i)), v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[e]));
+      }
+      const int e2 = min(100, max(-100, 127 + 13 - int(__float_as_uint(top) >> 23)));
+      float up = __uint_as_float(uint32_t(127 + e2) << 23);
+      f = __uint_as_float(uint32_t(127 - e2) << 23) * p.scale_log2;
+      if (f < 0.f) {  // a negative scale goes into q, so that larger products stay larger scores
+        f = -f;
+        up = -up;
+      }
+#pragma unroll 4
+      for (int i = 0; i < D; i += 8) {
+        float v[8];
+        bf16x8_to_float(__ldcg(reinterpret_cast<const uint4*>(src + i)), v);
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const __half2 x = __floats2half2_rn(v[2 * e] * up, v[2 * e + 1] * up);
+          w[e] = *reinterpret_cast<const uint32_t*>(&x);
+        }
+        sts128(q0 + uint32_t(t) * C::kQ + uint32_t(i >> 6) * (128 * 128) + uint32_t(r) * 128u +
+                   ((uint32_t((i >> 3) & 7) ^ uint32_t(r & 7)) << 4),
+               w[0], w[1], w[2], w[3]);
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->p_full[t]);  // phase 0: the tile's q is in place
+    }
+    const int lim = seq.kv_len - seq.q_len + j;                      // last key of the row
+    const int low = p.window > 0 ? lim - p.window + 1 : 0;           // first
+    const int lim0 = seq.kv_len - seq.q_len + (row0 + 128 * t) / p.group;   // last key of the tile's first row
+    const int low1 = p.window > 0 ? range.hi - p.window : 0;         // first key of the CTA's last row
+    float z = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int i = 0; i < n_tiles && ok; ++i) {
+      const int slot = C::kTiles == 2 ? t : i & 1;
+      const uint32_t par = C::kTiles == 2 ? uint32_t(i & 1) : uint32_t((i >> 1) & 1);
+      ok = __all_sync(0xffffffffu, kp_wait(&sh->s_full[slot], par, sh, p.err));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t sbuf = tmem + trow + uint32_t(slot) * C::kSCols;
+      const int key = key0 + i * C::TK;
+      const float* ks = sh->ks[i & 3];
+      const float* lv = sh->lv[i & 3];
+      const float* iv = sh->iv[i & 3];
+      const bool edge = key + C::TK - 1 > lim0 || key < low1;
+      // ---- the row's largest score + log2(vs)
+      float x = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < C::TK; c += 32) {
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(sbuf + uint32_t(c), v);
+        tc_wait_ld();
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          float m = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float s = __uint_as_float(v[16 * g + e]);
+            if (edge && (key + c + 16 * g + e > lim || key + c + 16 * g + e < low)) s = -INFINITY;
+            m = fmaxf(m, s);
+          }
+          // (a group without a visible key stays at -inf, whatever its factor)
+          if (m > -INFINITY) x = fmaxf(x, fmaf(m, f * ks[c / 16 + g], lv[c / 16 + g]));
+        }
+      }
+      if (__any_sync(0xffffffffu, x - 7.f > z + 8.f)) {  // (z = -inf: the first visible key)
+        const float nz = fmaxf(z, x - 7.f);
+        const float grow = z == -INFINITY ? 0.f : ex2(z - nz);
+        if (i > 0) {
+          if constexpr (C::kTiles == 1) ok = __all_sync(0xffffffffu, kp_wait(&sh->pv_done, uint32_t((i - 1) & 1), sh, p.err));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t v[32];
+            const uint32_t at = tmem + trow + C::kOCol + uint32_t(t * D + c);
+            tmem_ld_32x32b_x32(at, v);
+            tc_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * grow);
+            tmem_st_32x32b_x32(at, v);
+          }
+          tc_wait_st();
+        }
+        l *= grow;
+        z = nz;
+      }
+      const float ref = z == -INFINITY ? 0.f : z;
+      // ---- P' and the sum of p
+#pragma unroll
+      for (int c = 0; c < C::TK; c += 32) {
+        uint32_t v[32], w[16];
+        tmem_ld_32x32b_x32(sbuf + uint32_t(c), v);
+        tc_wait_ld();
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const float kf = f * ks[c / 16 + g], off = lv[c / 16 + g] - ref;
+          float sum = 0.f;
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            float a = ex2(fmaf(__uint_as_float(v[16 * g + e]), kf, off));
+            float b = ex2(fmaf(__uint_as_float(v[16 * g + e + 1]), kf, off));
+            if (edge) {
+              const int ka = key + c + 16 * g + e;
+              if (ka > lim || ka < low) a = 0.f;
+              if (ka + 1 > lim || ka + 1 < low) b = 0.f;
+            }
+            sum += a + b;
+            const __half2 hh = __floats2half2_rn(a, b);
+            w[8 * g + e / 2] = *reinterpret_cast<const uint32_t*>(&hh);
+          }
+          l = fmaf(sum, iv[c / 16 + g], l);
+        }
+        tmem_st_32x32b_x16(sbuf + uint32_t(c / 2), w);
+      }
+      tc_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->p_full[slot]);
+    }
+    // ---- O / l
+    if (ok) ok = __all_sync(0xffffffffu, kp_wait(&sh->drain, 0, sh, p.err));
+    if (ok) {
+      tc_fence_after();
+      const float norm = l > 0.f ? __fdiv_rn(1.f, l) : 0.f;
+      uint16_t* dst = p.out.data + (long long)(seq.start + j) * p.out.token + h * p.out.head;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(tmem + trow + C::kOCol + uint32_t(t * D + c), v);
+        tc_wait_ld();
+        if (live) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            float o[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[k] = __uint_as_float(v[e + k]) * norm;
+            *reinterpret_cast<uint4*>(dst + c + e) = float_to_bf16x8(o);
+          }
+        }
+      }
+    }
+  } else if (warp < kMmaWarp) {
+    // ------------------------------------------------ converters
+    constexpr int LPR = D / 16;              // lanes of a key (16 codes each)
+    constexpr int RPP = 128 / LPR;           // keys of a pass
+    constexpr int NP = C::TK / RPP;          // passes of a tile
+    const int tid = threadIdx.x - 32 * C::kSoftWarps;
+    const int sub = tid % LPR, r0 = tid / LPR;
+    const int* table = p.batch.table + (long long)sh->b * p.batch.table_stride;
+    const int ps = p.cache.page_shift;
+    // page ids of a tile's groups: lane g holds group g's (-1: nothing there)
+    auto fetch_ids = [&](int i) {
+      const int key = key0 + i * C::TK + 16 * lane;
+      int id = -1;
+      if (i < n_tiles && lane < C::KG && key < range.hi) {
+        id = __ldg(table + (key >> ps));
+        if (id < 0 || id >= p.cache.pages) {
+          record_error(p.err, kErrInput);
+          id = -1;
+        }
+      }
+      return id;
+    };
+    auto load = [&](int kind, int i, int ids, uint4 (&w)[NP]) {
+#pragma unroll
+      for (int n = 0; n < NP; ++n) {
+        const int r = n * RPP + r0;
+        const int id = __shfl_sync(0xffffffffu, ids, r >> 4);
+        w[n] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
+        if (id >= 0) {
+          const long long at = ((((long long)id * p.cache.kv_heads + head) << ps) + ((key0 + i * C::TK + r) & ((1 << ps) - 1))) * D;
+          w[n] = __ldg(reinterpret_cast<const uint4*>(p.cache.codes[kind] + at) + sub);
+          w[n].x ^= 0x80808080u;
+          w[n].y ^= 0x80808080u;
+          w[n].z ^= 0x80808080u;
+          w[n].w ^= 0x80808080u;
+        }
+      }
+    };
+    // live: a bit per key group; a dead group's values are zeros
+    auto store = [&](uint32_t base, const uint4 (&w)[NP], unsigned live) {
+#pragma unroll
+      for (int n = 0; n < NP; ++n) {
+        const int r = n * RPP + r0;
+        const uint32_t row = base + uint32_t(sub >> 2) * uint32_t(C::TK * 128) + uint32_t(r) * 128u;
+        uint32_t x[4] = {w[n].x, w[n].y, w[n].z, w[n].w};
+        if (!((live >> (r >> 4)) & 1u)) x[0] = x[1] = x[2] = x[3] = 0x80808080u;
+        uint32_t o[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          o[2 * e] = ka_codes(x[e], 0x4140u);
+          o[2 * e + 1] = ka_codes(x[e], 0x4342u);
+        }
+        // 16 codes are two 16-byte chunks; lanes 4 apart start with different halves (no bank conflict)
+        const uint32_t ch = uint32_t(sub & 3) * 2u, sw = uint32_t(r & 7);
+        const uint32_t lo = row + ((ch ^ sw) << 4), hi = row + (((ch + 1u) ^ sw) << 4);
+        if (sub & 4) {
+          sts128(hi, o[4], o[5], o[6], o[7]);
+          sts128(lo, o[0], o[1], o[2], o[3]);
+        } else {
+          sts128(lo, o[0], o[1], o[2], o[3]);
+          sts128(hi, o[4], o[5], o[6], o[7]);
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+    };
+    uint4 wk[NP], wv[NP];
+    int ids = fetch_ids(0), next = fetch_ids(1);
+    load(0, 0, ids, wk);
+    bool ok = true;
+    for (int i = 0; i < n_tiles && ok; ++i) {
+      const int st = i & 1;
+      const uint32_t par = uint32_t((i >> 1) & 1) ^ 1u;
+      load(1, i, ids, wv);
+      // the tile's scales (every warp reads them: it needs to know which groups have a V scale)
+      float s_k = 0.f, s_v = 0.f;
+      if (lane < C::KG && ids >= 0) {
+        const long long at = (long long)ids * p.cache.kv_heads + head;
+        s_k = p.cache.scales[0][at];
+        s_v = p.cache.scales[1][at];
+      }
+      const unsigned has = __ballot_sync(0xffffffffu, ids >= 0), live_v = __ballot_sync(0xffffffffu, s_v >= kKpLeastScale);
+      ok = __all_sync(0xffffffffu, kp_wait(&sh->k_empty[st], par, sh, p.err));
+      if (!ok) break;
+      if (tid < C::KG) {
+        // a page without a V scale counts in the sum of p like any other: its values are zeros at a stand-in scale
+        const float v = fmaxf(s_v, kKpLeastScale);
+        sh->ks[i & 3][tid] = s_k;
+        sh->lv[i & 3][tid] = __log2f(v);
+        sh->iv[i & 3][tid] = __fdiv_rn(1.f, v);
+      }
+      store(k0 + uint32_t(st) * C::kKV, wk, has);
+      if (lane == 0) mbar_arrive(&sh->k_full[st]);
+      load(0, i + 1, next, wk);
+      ids = next;
+      next = fetch_ids(i + 2);
+      ok = __all_sync(0xffffffffu, kp_wait(&sh->v_empty[st], par, sh, p.err));
+      if (!ok) break;
+      store(v0 + uint32_t(st) * C::kKV, wv, live_v);
+      if (lane == 0) mbar_arrive(&sh->v_full[st]);
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      bool ok = true;
+      auto qk = [&](int i, int t, int slot) {  // scores of key tile i
+        const uint32_t kb = k0 + uint32_t(i & 1) * C::kKV, qb = q0 + uint32_t(t) * C::kQ;
+#pragma unroll
+        for (int d = 0; d < D; d += 16) {
+          const uint32_t in = uint32_t(d & 63) * 2u;
+          tc_mma_ss_f16(tmem + uint32_t(slot) * C::kSCols, sw128_desc(qb + uint32_t(d >> 6) * (128u * 128u) + in),
+                        sw128_desc(kb + uint32_t(d >> 6) * uint32_t(C::TK * 128) + in), C::kIdescQK, d ? 1u : 0u);
+        }
+        tc_commit(&sh->s_full[slot]);
+      };
+      auto pv = [&](int i, int t, int slot) {
+        const uint32_t vb = v0 + uint32_t(i & 1) * C::kKV;
+#pragma unroll
+        for (int k = 0; k < C::TK; k += 16)
+          tc_mma_ts_f16(tmem + C::kOCol + uint32_t(t * D), tmem + uint32_t(slot) * C::kSCols + uint32_t(k / 2),
+                        sw128_mn_desc(vb + uint32_t(k) * 128u, C::TK * 128), C::kIdescPV, (i | k) ? 1u : 0u);
+      };
+      // p_full: phase 0 is q, phase 1 + n the n-th P' of the slot (with one row tile, slot 1 has no q phase)
+      for (int t = 0; t < C::kTiles && ok; ++t) ok = kp_wait(&sh->p_full[t], 0, sh, p.err);
+      if (ok) ok = kp_wait(&sh->k_full[0], 0, sh, p.err);
+      if (ok) {
+        tc_fence_after();
+        for (int t = 0; t < C::kTiles; ++t) qk(0, t, t);
+        tc_commit(&sh->k_empty[0]);
+      }
+      for (int i = 0; i < n_tiles && ok; ++i) {
+        const uint32_t full = uint32_t((i >> 1) & 1), nfull = uint32_t(((i + 1) >> 1) & 1);
+        if constexpr (C::kTiles == 2) {
+          for (int t = 0; t < 2 && ok; ++t) {
+            ok = kp_wait(&sh->p_full[t], uint32_t((i + 1) & 1), sh, p.err);
+            if (ok && t == 0) ok = kp_wait(&sh->v_full[i & 1], full, sh, p.err);
+            if (!ok) break;
+            tc_fence_after();
+            pv(i, t, t);
+            if (t == 1) tc_commit(&sh->v_empty[i & 1]);
+            if (i + 1 < n_tiles) {
+              if (t == 0) ok = kp_wait(&sh->k_full[(i + 1) & 1], nfull, sh, p.err);
+              if (!ok) break;
+              tc_fence_after();
+              qk(i + 1, t, t);
+              if (t == 1) tc_commit(&sh->k_empty[(i + 1) & 1]);
+            }
+          }
+        } else {
+          if (i + 1 < n_tiles) {
+            ok = kp_wait(&sh->k_full[(i + 1) & 1], nfull, sh, p.err);
+            if (!ok) break;
+            tc_fence_after();
+            qk(i + 1, 0, (i + 1) & 1);
+            tc_commit(&sh->k_empty[(i + 1) & 1]);
+          }
+          // slot 0's barrier had one phase more (q)
+          ok = kp_wait(&sh->p_full[i & 1], uint32_t(((i >> 1) + ((i & 1) ? 0 : 1)) & 1), sh, p.err);
+          if (ok) ok = kp_wait(&sh->v_full[i & 1], full, sh, p.err);
+          if (!ok) break;
+          tc_fence_after();
+          pv(i, 0, i & 1);
+          tc_commit(&sh->v_empty[i & 1]);
+          tc_commit(&sh->pv_done);
+        }
+      }
+      tc_commit(&sh->drain);  // everything issued so far
+      mbar_wait_bounded(&sh->drain, 0, p.err, 1u << 20);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace w4a8

@@ -22,6 +22,7 @@
 #include "int8_quant.cuh"
 #include "kv_attn.cuh"
 #include "kv_cache.cuh"
+#include "kv_prefill.cuh"
 #include "nvfp4.cuh"
 #include "pack.cuh"
 #include "qk_rope.cuh"
