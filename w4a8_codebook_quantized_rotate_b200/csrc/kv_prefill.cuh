@@ -99,6 +99,22 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
@@ -254,22 +270,39 @@ __global__ void __launch_bounds__(KpCfg<D>::kThreads, 1) kv_prefill_kernel(const
       const bool edge = key + C::TK - 1 > lim0 || key < low1;
       // ---- the row's largest score + log2(vs)
       float x = -INFINITY;
+      if (!edge) {
+        uint32_t v[2][32];
 #pragma unroll
-      for (int c = 0; c < C::TK; c += 32) {
-        uint32_t v[32];
-        tmem_ld_32x32b_x32(sbuf + uint32_t(c), v);
-        tc_wait_ld();
+        for (int c = 0; c < C::TK / 32; ++c) {
+          if ((c & 1) == 0) {  // 64 scores at a time
+            tmem_ld_32x32b_x32(sbuf + uint32_t(32 * c), v[0]);
+            tmem_ld_32x32b_x32(sbuf + uint32_t(32 * c + 32), v[1]);
+            tc_wait_ld();
+          }
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
+          for (int g = 0; g < 2; ++g) {
+            float m[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m[e] = __uint_as_float(v[c & 1][16 * g + e]);
+#pragma unroll
+            for (int e = 4; e < 16; ++e) m[e & 3] = fmaxf(m[e & 3], __uint_as_float(v[c & 1][16 * g + e]));
+            const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+            x = fmaxf(x, fmaf(top, f * ks[2 * c + g], lv[2 * c + g]));
+          }
+        }
+      } else {
+#pragma unroll 1
+        for (int g = 0; g < C::KG; ++g) {
+          uint32_t v[16];
+          tmem_ld_32x32b_x16(sbuf + uint32_t(16 * g), v);
+          tc_wait_ld();
+          const int k0g = key + 16 * g;
           float m = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float s = __uint_as_float(v[16 * g + e]);
-            if (edge && (key + c + 16 * g + e > lim || key + c + 16 * g + e < low)) s = -INFINITY;
-            m = fmaxf(m, s);
-          }
+          for (int e = 0; e < 16; ++e)
+            m = fmaxf(m, k0g + e <= lim && k0g + e >= low ? __uint_as_float(v[e]) : -INFINITY);
           // (a group without a visible key stays at -inf, whatever its factor)
-          if (m > -INFINITY) x = fmaxf(x, fmaf(m, f * ks[c / 16 + g], lv[c / 16 + g]));
+          if (m > -INFINITY) x = fmaxf(x, fmaf(m, f * ks[g], lv[g]));
         }
       }
       if (__any_sync(0xffffffffu, x - 7.f > z + 8.f)) {  // (z = -inf: the first visible key)
@@ -296,31 +329,55 @@ __global__ void __launch_bounds__(KpCfg<D>::kThreads, 1) kv_prefill_kernel(const
       }
       const float ref = z == -INFINITY ? 0.f : z;
       // ---- P' and the sum of p
+      if (!edge) {
+        uint32_t v[2][32];
 #pragma unroll
-      for (int c = 0; c < C::TK; c += 32) {
-        uint32_t v[32], w[16];
-        tmem_ld_32x32b_x32(sbuf + uint32_t(c), v);
-        tc_wait_ld();
+        for (int c = 0; c < C::TK / 32; ++c) {
+          if ((c & 1) == 0) {  // 64 scores at a time
+            tmem_ld_32x32b_x32(sbuf + uint32_t(32 * c), v[0]);
+            tmem_ld_32x32b_x32(sbuf + uint32_t(32 * c + 32), v[1]);
+            tc_wait_ld();
+          }
+          uint32_t w[16];
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const float kf = f * ks[c / 16 + g], off = lv[c / 16 + g] - ref;
+          for (int g = 0; g < 2; ++g) {
+            const float kf = f * ks[2 * c + g], off = lv[2 * c + g] - ref;
+            float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const float a = ex2(fmaf(__uint_as_float(v[c & 1][16 * g + e]), kf, off));
+              const float b = ex2(fmaf(__uint_as_float(v[c & 1][16 * g + e + 1]), kf, off));
+              s0 += a;
+              s1 += b;
+              const __half2 hh = __floats2half2_rn(a, b);
+              w[8 * g + e / 2] = *reinterpret_cast<const uint32_t*>(&hh);
+            }
+            l = fmaf(s0 + s1, iv[2 * c + g], l);
+          }
+          // (into the columns of scores that are read already)
+          tmem_st_32x32b_x16(sbuf + uint32_t(16 * c), w);
+        }
+      } else {
+#pragma unroll 1
+        for (int g = 0; g < C::KG; ++g) {
+          uint32_t v[16], w[8];
+          tmem_ld_32x32b_x16(sbuf + uint32_t(16 * g), v);
+          tc_wait_ld();
+          const float kf = f * ks[g], off = lv[g] - ref;
+          const int k0g = key + 16 * g;
           float sum = 0.f;
 #pragma unroll
           for (int e = 0; e < 16; e += 2) {
-            float a = ex2(fmaf(__uint_as_float(v[16 * g + e]), kf, off));
-            float b = ex2(fmaf(__uint_as_float(v[16 * g + e + 1]), kf, off));
-            if (edge) {
-              const int ka = key + c + 16 * g + e;
-              if (ka > lim || ka < low) a = 0.f;
-              if (ka + 1 > lim || ka + 1 < low) b = 0.f;
-            }
+            float a = ex2(fmaf(__uint_as_float(v[e]), kf, off)), b = ex2(fmaf(__uint_as_float(v[e + 1]), kf, off));
+            a = k0g + e <= lim && k0g + e >= low ? a : 0.f;
+            b = k0g + e + 1 <= lim && k0g + e + 1 >= low ? b : 0.f;
             sum += a + b;
             const __half2 hh = __floats2half2_rn(a, b);
-            w[8 * g + e / 2] = *reinterpret_cast<const uint32_t*>(&hh);
+            w[e / 2] = *reinterpret_cast<const uint32_t*>(&hh);
           }
-          l = fmaf(sum, iv[c / 16 + g], l);
+          l = fmaf(sum, iv[g], l);
+          tmem_st_32x32b_x8(sbuf + uint32_t(8 * g), w);
         }
-        tmem_st_32x32b_x16(sbuf + uint32_t(c / 2), w);
       }
       tc_wait_st();
       tc_fence_before();
@@ -371,21 +428,21 @@ __global__ void __launch_bounds__(KpCfg<D>::kThreads, 1) kv_prefill_kernel(const
       }
       return id;
     };
+    // A group without a page reads page 0 instead (its values are zeroed when they are stored), so that the
+    // loads are plain and stay in flight together.
     auto load = [&](int kind, int i, int ids, uint4 (&w)[NP]) {
 #pragma unroll
       for (int n = 0; n < NP; ++n) {
         const int r = n * RPP + r0;
-        const int id = __shfl_sync(0xffffffffu, ids, r >> 4);
-        w[n] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
-        if (id >= 0) {
-          const long long at = ((((long long)id * p.cache.kv_heads + head) << ps) + ((key0 + i * C::TK + r) & ((1 << ps) - 1))) * D;
-          w[n] = __ldg(reinterpret_cast<const uint4*>(p.cache.codes[kind] + at) + sub);
-          w[n].x ^= 0x80808080u;
-          w[n].y ^= 0x80808080u;
-          w[n].z ^= 0x80808080u;
-          w[n].w ^= 0x80808080u;
-        }
+        const int id = max(__shfl_sync(0xffffffffu, ids, r >> 4), 0);
+        const long long at = ((((long long)id * p.cache.kv_heads + head) << ps) + ((key0 + i * C::TK + r) & ((1 << ps) - 1))) * D;
+        w[n] = __ldg(reinterpret_cast<const uint4*>(p.cache.codes[kind] + at) + sub);
       }
+    };
+    auto fetch_scales = [&](int ids) {  // ks, vs of the lane's group
+      const long long at = (long long)max(ids, 0) * p.cache.kv_heads + head;
+      const float2 s = make_float2(__ldg(p.cache.scales[0] + at), __ldg(p.cache.scales[1] + at));
+      return lane < C::KG && ids >= 0 ? s : make_float2(0.f, 0.f);
     };
     // live: a bit per key group; a dead group's values are zeros
     auto store = [&](uint32_t base, const uint4 (&w)[NP], unsigned live) {
@@ -393,7 +450,8 @@ __global__ void __launch_bounds__(KpCfg<D>::kThreads, 1) kv_prefill_kernel(const
       for (int n = 0; n < NP; ++n) {
         const int r = n * RPP + r0;
         const uint32_t row = base + uint32_t(sub >> 2) * uint32_t(C::TK * 128) + uint32_t(r) * 128u;
-        uint32_t x[4] = {w[n].x, w[n].y, w[n].z, w[n].w};
+        // code + 128, or 128 (a zero) in a dead group
+        uint32_t x[4] = {w[n].x ^ 0x80808080u, w[n].y ^ 0x80808080u, w[n].z ^ 0x80808080u, w[n].w ^ 0x80808080u};
         if (!((live >> (r >> 4)) & 1u)) x[0] = x[1] = x[2] = x[3] = 0x80808080u;
         uint32_t o[8];
 #pragma unroll
@@ -418,18 +476,14 @@ __global__ void __launch_bounds__(KpCfg<D>::kThreads, 1) kv_prefill_kernel(const
     uint4 wk[NP], wv[NP];
     int ids = fetch_ids(0), next = fetch_ids(1);
     load(0, 0, ids, wk);
+    float2 sc = fetch_scales(ids), sc_next = fetch_scales(next);
     bool ok = true;
     for (int i = 0; i < n_tiles && ok; ++i) {
       const int st = i & 1;
       const uint32_t par = uint32_t((i >> 1) & 1) ^ 1u;
       load(1, i, ids, wv);
       // the tile's scales (every warp reads them: it needs to know which groups have a V scale)
-      float s_k = 0.f, s_v = 0.f;
-      if (lane < C::KG && ids >= 0) {
-        const long long at = (long long)ids * p.cache.kv_heads + head;
-        s_k = p.cache.scales[0][at];
-        s_v = p.cache.scales[1][at];
-      }
+      const float s_k = sc.x, s_v = sc.y;
       const unsigned has = __ballot_sync(0xffffffffu, ids >= 0), live_v = __ballot_sync(0xffffffffu, s_v >= kKpLeastScale);
       ok = __all_sync(0xffffffffu, kp_wait(&sh->k_empty[st], par, sh, p.err));
       if (!ok) break;
@@ -445,10 +499,12 @@ __global__ void __launch_bounds__(KpCfg<D>::kThreads, 1) kv_prefill_kernel(const
       load(0, i + 1, next, wk);
       ids = next;
       next = fetch_ids(i + 2);
+      sc = sc_next;
       ok = __all_sync(0xffffffffu, kp_wait(&sh->v_empty[st], par, sh, p.err));
       if (!ok) break;
       store(v0 + uint32_t(st) * C::kKV, wv, live_v);
       if (lane == 0) mbar_arrive(&sh->v_full[st]);
+      sc_next = fetch_scales(next);
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------ MMA issuer
