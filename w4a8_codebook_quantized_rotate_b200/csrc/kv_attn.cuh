@@ -509,7 +509,11 @@ __global__ void __launch_bounds__(kKaThreads, 1)
     for (int item = seg.item0; item < seg.item1; ++item) {
       const int key = seg.key0 + (item * kKaWarps + warp) * C::TK;
       if (!(key < seg.range.hi && key + C::TK > seg.range.lo)) continue;
-      if (ok) ok = __all_sync(0xffffffffu, ka_wait(&sh->full[warp][stage], phase, sh, p.err));
+      if (ok) {
+        const int got = lane == 0 ? int(ka_wait(&sh->full[warp][stage], phase, sh, p.err)) : 0;
+        __syncwarp();
+        ok = __shfl_sync(0xffffffffu, got, 0) != 0;
+      }
       if (!ok) continue;
       const uint32_t kt = ring + uint32_t((warp * kKaStages + stage) * 2) * kKaTileBytes, vt = kt + kKaTileBytes;
       // ---- scores

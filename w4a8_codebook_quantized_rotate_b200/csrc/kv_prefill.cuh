@@ -10,22 +10,26 @@
 //
 // A CTA takes 256 rows of one key head (the query heads of the group,
 // neighbouring new tokens) as two tiles of 128, TMEM's lanes (heads of 256:
-// one tile), and walks the keys in tiles of 128 (64).  Roles:
+// one tile), and walks the keys in tiles of 64.  Roles:
 //   * 4 converter warps expand K and V codes to fp16 in 128-byte-swizzled
-//     shared memory, two stages each, with the loads of the next two tiles
+//     shared memory, a ring of stages each, with the loads of the next tile
 //     in registers.  Expanding once per 256 rows is what makes the expansion
 //     cheap: its shared-memory writes are a third of the MMAs' reads.
-//   * one thread issues the MMAs: S = Q K^T from shared memory, O += P' V with
-//     P' in TMEM (fp16, in S's place) and V as it lies ([key][d], the
-//     operand's MN-major order), O in TMEM.
-//   * a softmax warpgroup per tile, a thread per row: maximum over the row's
-//     scores, then P' back to TMEM 32 keys at a time.
-// While one tile's softmax runs, the other tile's two products do; with heads
-// of 256 the one tile alternates between two score buffers instead.
+//   * one thread issues the MMAs of S = Q K^T from shared memory, another those
+//     of O += P' V with P' in TMEM (fp16, in S's place) and V as it lies
+//     ([key][d], the operand's MN-major order), O in TMEM.  (One thread for
+//     both could not issue them fast enough: 2500 clocks per 256 x 64 scores
+//     of heads of 128, against 1300 that the MMAs take.)
+//   * a softmax warpgroup per row tile, a thread per row: maximum over the
+//     row's scores, then P' back to TMEM.
+// Every row tile has two score buffers: the scores of the next key tile are
+// made while the softmax of this one runs, so the softmax warps, which bound
+// the kernel, do not wait for the MMAs.
 // Bounds: per 256 x 128 (rows x keys) and D = 128 the MMAs take 2048 clocks
-// of an SM, its exponentials (16 a clock) 2048 as well, so the softmax keeps
-// to about four other instructions a score: scores are scaled in the exponent's
-// multiply-add, and the sum of p comes from P' per page (sum of P' / vs).
+// of an SM (2560 with the operand reads of 64-key tiles), its exponentials (16
+// a clock) 2048, so the softmax keeps to about four other instructions a
+// score: scores are scaled in the exponent's multiply-add, and the sum of p
+// comes from P' per page (sum of P' / vs).
 #pragma once
 
 #include "common.cuh"
@@ -41,16 +45,17 @@ constexpr float kKpLeastScale = 0x1p-80f;  // V scales below count as 0
 template <int D>
 struct KpCfg {
   static constexpr int kTiles = D <= 128 ? 2 : 1;        // row tiles of a CTA
-  static constexpr int TK = D <= 128 ? 128 : 64;         // keys of a tile
+  static constexpr int TK = 64;                          // keys of a tile
+  static constexpr int kStages = D <= 128 ? 4 : 2;       // of K, and of V
   static constexpr int KG = TK / 16;                     // key groups (one page each)
   static constexpr int kRows = 128 * kTiles;
   static constexpr int kSoftWarps = 4 * kTiles;
-  static constexpr int kThreads = 32 * (kSoftWarps + kKpConvWarps + 1);  // softmax, converters, MMA warp
+  static constexpr int kThreads = 32 * (kSoftWarps + kKpConvWarps + 2);  // softmax, converters, two MMA warps
   static constexpr uint32_t kQ = 128 * D * 2;            // a tile of q, fp16
   static constexpr uint32_t kKV = TK * D * 2;            // a stage of K or V, fp16
-  static constexpr size_t kSmem = 1024 + kTiles * kQ + 4 * kKV + 1024;
+  static constexpr size_t kSmem = 1024 + kTiles * kQ + 2 * kStages * kKV + 1024;
   static constexpr uint32_t kSCols = TK;                 // fp32 scores; P' takes the first half
-  static constexpr uint32_t kOCol = 2 * kSCols;          // two score buffers, then O of each tile
+  static constexpr uint32_t kOCol = 2 * kTiles * kSCols; // two score buffers a tile, then O of each tile
   static_assert(kOCol + kTiles * D <= 512, "TMEM");
   // kind::f16: fp16 A and B, fp32 D, M = 128
   static constexpr uint32_t kIdescQK = (1u << 4) | (uint32_t(TK >> 3) << 17) | (8u << 24);
@@ -58,11 +63,12 @@ struct KpCfg {
 };
 
 struct KpShared {
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t s_full[2], p_full[2];
-  uint64_t pv_done;
+  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+  uint64_t q_full;
+  uint64_t s_full[4], p_full[4];  // [2 tile + buffer]
+  uint64_t pv_done[4];            // [2 tile + buffer]: one each, as the scores may be two products behind
   uint64_t drain;
-  float ks[4][8], lv[4][8], iv[4][8];  // ks, log2(vs), 1 / vs of a tile's key groups (ring of 4 tiles)
+  float ks[8][4], lv[8][4], iv[8][4];  // ks, log2(vs), 1 / vs of a tile's key groups (ring of 8 tiles)
   uint32_t tmem_base;
   int found;
   int b, tile;
@@ -77,6 +83,14 @@ __device__ __forceinline__ bool kp_wait(uint64_t* bar, uint32_t parity, KpShared
   sh->abort = 1;
   record_error(err, kErrTimeout);
   return false;
+}
+
+// A warp's wait: lane 0 polls (32 lanes polling one word take the shared
+// memory's time from the MMAs), the others learn the outcome.
+__device__ __forceinline__ bool kp_wait_warp(uint64_t* bar, uint32_t parity, KpShared* sh, unsigned* err) {
+  const int ok = (threadIdx.x & 31) == 0 ? int(kp_wait(bar, parity, sh, err)) : 0;
+  __syncwarp();
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
 // D[tmem] (+)= A[smem desc] * B[smem desc], kind::f16.
@@ -162,22 +176,23 @@ __global__ void __launch_bounds__(KpCfg<D>::kThreads, 1) kv_prefill_kernel(const
   using C = KpCfg<D>;
   extern __shared__ __align__(1024) uint8_t kp_smem[];
   const uint32_t q0 = (smem_u32(kp_smem) + 1023u) & ~1023u;
-  const uint32_t k0 = q0 + C::kTiles * C::kQ, v0 = k0 + 2 * C::kKV;
-  KpShared* sh = reinterpret_cast<KpShared*>(kp_smem + (v0 + 2 * C::kKV - smem_u32(kp_smem)));
+  const uint32_t k0 = q0 + C::kTiles * C::kQ, v0 = k0 + C::kStages * C::kKV;
+  KpShared* sh = reinterpret_cast<KpShared*>(kp_smem + (v0 + C::kStages * C::kKV - smem_u32(kp_smem)));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&sh->k_full[i], kKpConvWarps);
       mbar_init(&sh->v_full[i], kKpConvWarps);
       mbar_init(&sh->k_empty[i], 1);
       mbar_init(&sh->v_empty[i], 1);
       mbar_init(&sh->s_full[i], 1);
+      mbar_init(&sh->pv_done[i], 1);
       mbar_init(&sh->p_full[i], 4);
     }
-    mbar_init(&sh->pv_done, 1);
-    mbar_init(&sh->drain, 1);
+    mbar_init(&sh->q_full, C::kSoftWarps);
+    mbar_init(&sh->drain, 2);
     sh->abort = 0;
     fence_barrier_init();
   }
@@ -248,7 +263,7 @@ __global__ void __launch_bounds__(KpCfg<D>::kThreads, 1) kv_prefill_kernel(const
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->p_full[t]);  // phase 0: the tile's q is in place
+      if (lane == 0) mbar_arrive(&sh->q_full);
     }
     const int lim = seq.kv_len - seq.q_len + j;                      // last key of the row
     const int low = p.window > 0 ? lim - p.window + 1 : 0;           // first
@@ -257,35 +272,33 @@ __global__ void __launch_bounds__(KpCfg<D>::kThreads, 1) kv_prefill_kernel(const
     float z = -INFINITY, l = 0.f;
     bool ok = true;
     for (int i = 0; i < n_tiles && ok; ++i) {
-      const int slot = C::kTiles == 2 ? t : i & 1;
-      const uint32_t par = C::kTiles == 2 ? uint32_t(i & 1) : uint32_t((i >> 1) & 1);
-      ok = __all_sync(0xffffffffu, kp_wait(&sh->s_full[slot], par, sh, p.err));
+      const int slot = 2 * t + (i & 1);
+      const uint32_t par = uint32_t((i >> 1) & 1);
+      ok = kp_wait_warp(&sh->s_full[slot], par, sh, p.err);
       if (!ok) break;
       tc_fence_after();
       const uint32_t sbuf = tmem + trow + uint32_t(slot) * C::kSCols;
       const int key = key0 + i * C::TK;
-      const float* ks = sh->ks[i & 3];
-      const float* lv = sh->lv[i & 3];
-      const float* iv = sh->iv[i & 3];
+      const float* ks = sh->ks[i & 7];
+      const float* lv = sh->lv[i & 7];
+      const float* iv = sh->iv[i & 7];
       const bool edge = key + C::TK - 1 > lim0 || key < low1;
       // ---- the row's largest score + log2(vs)
       float x = -INFINITY;
+      uint32_t v[C::TK / 32][32];  // 64 scores
       if (!edge) {
-        uint32_t v[2][32];
+#pragma unroll
+        for (int c = 0; c < C::TK / 32; ++c) tmem_ld_32x32b_x32(sbuf + uint32_t(32 * c), v[c]);
+        tc_wait_ld();
 #pragma unroll
         for (int c = 0; c < C::TK / 32; ++c) {
-          if ((c & 1) == 0) {  // 64 scores at a time
-            tmem_ld_32x32b_x32(sbuf + uint32_t(32 * c), v[0]);
-            tmem_ld_32x32b_x32(sbuf + uint32_t(32 * c + 32), v[1]);
-            tc_wait_ld();
-          }
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             float m[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) m[e] = __uint_as_float(v[c & 1][16 * g + e]);
+            for (int e = 0; e < 4; ++e) m[e] = __uint_as_float(v[c][16 * g + e]);
 #pragma unroll
-            for (int e = 4; e < 16; ++e) m[e & 3] = fmaxf(m[e & 3], __uint_as_float(v[c & 1][16 * g + e]));
+            for (int e = 4; e < 16; ++e) m[e & 3] = fmaxf(m[e & 3], __uint_as_float(v[c][16 * g + e]));
             const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
             x = fmaxf(x, fmaf(top, f * ks[2 * c + g], lv[2 * c + g]));
           }
@@ -293,14 +306,14 @@ __global__ void __launch_bounds__(KpCfg<D>::kThreads, 1) kv_prefill_kernel(const
       } else {
 #pragma unroll 1
         for (int g = 0; g < C::KG; ++g) {
-          uint32_t v[16];
-          tmem_ld_32x32b_x16(sbuf + uint32_t(16 * g), v);
+          uint32_t y[16];
+          tmem_ld_32x32b_x16(sbuf + uint32_t(16 * g), y);
           tc_wait_ld();
           const int k0g = key + 16 * g;
           float m = -INFINITY;
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            m = fmaxf(m, k0g + e <= lim && k0g + e >= low ? __uint_as_float(v[e]) : -INFINITY);
+            m = fmaxf(m, k0g + e <= lim && k0g + e >= low ? __uint_as_float(y[e]) : -INFINITY);
           // (a group without a visible key stays at -inf, whatever its factor)
           if (m > -INFINITY) x = fmaxf(x, fmaf(m, f * ks[g], lv[g]));
         }
@@ -309,18 +322,19 @@ __global__ void __launch_bounds__(KpCfg<D>::kThreads, 1) kv_prefill_kernel(const
         const float nz = fmaxf(z, x - 7.f);
         const float grow = z == -INFINITY ? 0.f : ex2(z - nz);
         if (i > 0) {
-          if constexpr (C::kTiles == 1) ok = __all_sync(0xffffffffu, kp_wait(&sh->pv_done, uint32_t((i - 1) & 1), sh, p.err));
+          // O's last product must be done
+          ok = kp_wait_warp(&sh->pv_done[2 * t + ((i - 1) & 1)], uint32_t(((i - 1) >> 1) & 1), sh, p.err);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t v[32];
+          for (int c = 0; c < D; c += 16) {
+            uint32_t y[16];
             const uint32_t at = tmem + trow + C::kOCol + uint32_t(t * D + c);
-            tmem_ld_32x32b_x32(at, v);
+            tmem_ld_32x32b_x16(at, y);
             tc_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * grow);
-            tmem_st_32x32b_x32(at, v);
+            for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * grow);
+            tmem_st_32x32b_x16(at, y);
           }
           tc_wait_st();
         }
@@ -330,14 +344,8 @@ __global__ void __launch_bounds__(KpCfg<D>::kThreads, 1) kv_prefill_kernel(const
       const float ref = z == -INFINITY ? 0.f : z;
       // ---- P' and the sum of p
       if (!edge) {
-        uint32_t v[2][32];
 #pragma unroll
         for (int c = 0; c < C::TK / 32; ++c) {
-          if ((c & 1) == 0) {  // 64 scores at a time
-            tmem_ld_32x32b_x32(sbuf + uint32_t(32 * c), v[0]);
-            tmem_ld_32x32b_x32(sbuf + uint32_t(32 * c + 32), v[1]);
-            tc_wait_ld();
-          }
           uint32_t w[16];
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
@@ -345,8 +353,8 @@ __global__ void __launch_bounds__(KpCfg<D>::kThreads, 1) kv_prefill_kernel(const
             float s0 = 0.f, s1 = 0.f;
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
-              const float a = ex2(fmaf(__uint_as_float(v[c & 1][16 * g + e]), kf, off));
-              const float b = ex2(fmaf(__uint_as_float(v[c & 1][16 * g + e + 1]), kf, off));
+              const float a = ex2(fmaf(__uint_as_float(v[c][16 * g + e]), kf, off));
+              const float b = ex2(fmaf(__uint_as_float(v[c][16 * g + e + 1]), kf, off));
               s0 += a;
               s1 += b;
               const __half2 hh = __floats2half2_rn(a, b);
@@ -360,15 +368,15 @@ __global__ void __launch_bounds__(KpCfg<D>::kThreads, 1) kv_prefill_kernel(const
       } else {
 #pragma unroll 1
         for (int g = 0; g < C::KG; ++g) {
-          uint32_t v[16], w[8];
-          tmem_ld_32x32b_x16(sbuf + uint32_t(16 * g), v);
+          uint32_t y[16], w[8];
+          tmem_ld_32x32b_x16(sbuf + uint32_t(16 * g), y);
           tc_wait_ld();
           const float kf = f * ks[g], off = lv[g] - ref;
           const int k0g = key + 16 * g;
           float sum = 0.f;
 #pragma unroll
           for (int e = 0; e < 16; e += 2) {
-            float a = ex2(fmaf(__uint_as_float(v[e]), kf, off)), b = ex2(fmaf(__uint_as_float(v[e + 1]), kf, off));
+            float a = ex2(fmaf(__uint_as_float(y[e]), kf, off)), b = ex2(fmaf(__uint_as_float(y[e + 1]), kf, off));
             a = k0g + e <= lim && k0g + e >= low ? a : 0.f;
             b = k0g + e + 1 <= lim && k0g + e + 1 >= low ? b : 0.f;
             sum += a + b;
@@ -385,7 +393,7 @@ __global__ void __launch_bounds__(KpCfg<D>::kThreads, 1) kv_prefill_kernel(const
       if (lane == 0) mbar_arrive(&sh->p_full[slot]);
     }
     // ---- O / l
-    if (ok) ok = __all_sync(0xffffffffu, kp_wait(&sh->drain, 0, sh, p.err));
+    if (ok) ok = kp_wait_warp(&sh->drain, 0, sh, p.err);
     if (ok) {
       tc_fence_after();
       const float norm = l > 0.f ? __fdiv_rn(1.f, l) : 0.f;
@@ -415,16 +423,16 @@ __global__ void __launch_bounds__(KpCfg<D>::kThreads, 1) kv_prefill_kernel(const
     const int sub = tid % LPR, r0 = tid / LPR;
     const int* table = p.batch.table + (long long)sh->b * p.batch.table_stride;
     const int ps = p.cache.page_shift;
-    // page ids of a tile's groups: lane g holds group g's (-1: nothing there)
+    // Page ids of a tile's groups: lane g holds group g's (-1: nothing there).  What is fetched is looked at an
+    // iteration later, so that no load is waited for.
     auto fetch_ids = [&](int i) {
       const int key = key0 + i * C::TK + 16 * lane;
-      int id = -1;
-      if (i < n_tiles && lane < C::KG && key < range.hi) {
-        id = __ldg(table + (key >> ps));
-        if (id < 0 || id >= p.cache.pages) {
-          record_error(p.err, kErrInput);
-          id = -1;
-        }
+      return i < n_tiles && lane < C::KG && key < range.hi ? __ldg(table + (key >> ps)) : -1;
+    };
+    auto checked = [&](int id, int i) {
+      if (id >= p.cache.pages || (id < 0 && i < n_tiles && lane < C::KG && key0 + i * C::TK + 16 * lane < range.hi)) {
+        record_error(p.err, kErrInput);
+        id = -1;
       }
       return id;
     };
@@ -441,139 +449,147 @@ __global__ void __launch_bounds__(KpCfg<D>::kThreads, 1) kv_prefill_kernel(const
     };
     auto fetch_scales = [&](int ids) {  // ks, vs of the lane's group
       const long long at = (long long)max(ids, 0) * p.cache.kv_heads + head;
-      const float2 s = make_float2(__ldg(p.cache.scales[0] + at), __ldg(p.cache.scales[1] + at));
-      return lane < C::KG && ids >= 0 ? s : make_float2(0.f, 0.f);
+      return make_float2(__ldg(p.cache.scales[0] + at), __ldg(p.cache.scales[1] + at));
     };
-    // live: a bit per key group; a dead group's values are zeros
+    // live: a bit per key group; a dead group's values are zeros.  16 codes are two 16-byte chunks of a row; lanes
+    // 4 apart start with different halves (no bank conflict).  RPP is a multiple of 8, so a thread's chunks keep
+    // their swizzle from pass to pass.
+    static_assert(RPP % 8 == 0, "passes keep the swizzle");
+    const uint32_t at_row = uint32_t(sub >> 2) * uint32_t(C::TK * 128) + uint32_t(r0) * 128u;
+    const uint32_t ch = uint32_t(sub & 3) * 2u, sw = uint32_t(r0 & 7);
+    const uint32_t at_a = at_row + (((ch + ((sub & 4) ? 1u : 0u)) ^ sw) << 4);
+    const uint32_t at_b = at_row + (((ch + ((sub & 4) ? 0u : 1u)) ^ sw) << 4);
     auto store = [&](uint32_t base, const uint4 (&w)[NP], unsigned live) {
 #pragma unroll
       for (int n = 0; n < NP; ++n) {
-        const int r = n * RPP + r0;
-        const uint32_t row = base + uint32_t(sub >> 2) * uint32_t(C::TK * 128) + uint32_t(r) * 128u;
         // code + 128, or 128 (a zero) in a dead group
         uint32_t x[4] = {w[n].x ^ 0x80808080u, w[n].y ^ 0x80808080u, w[n].z ^ 0x80808080u, w[n].w ^ 0x80808080u};
-        if (!((live >> (r >> 4)) & 1u)) x[0] = x[1] = x[2] = x[3] = 0x80808080u;
+        if (live != (1u << C::KG) - 1u && !((live >> ((n * RPP + r0) >> 4)) & 1u)) x[0] = x[1] = x[2] = x[3] = 0x80808080u;
+        if (sub & 4) {
+          const uint32_t y0 = x[0], y1 = x[1];
+          x[0] = x[2], x[1] = x[3], x[2] = y0, x[3] = y1;
+        }
         uint32_t o[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           o[2 * e] = ka_codes(x[e], 0x4140u);
           o[2 * e + 1] = ka_codes(x[e], 0x4342u);
         }
-        // 16 codes are two 16-byte chunks; lanes 4 apart start with different halves (no bank conflict)
-        const uint32_t ch = uint32_t(sub & 3) * 2u, sw = uint32_t(r & 7);
-        const uint32_t lo = row + ((ch ^ sw) << 4), hi = row + (((ch + 1u) ^ sw) << 4);
-        if (sub & 4) {
-          sts128(hi, o[4], o[5], o[6], o[7]);
-          sts128(lo, o[0], o[1], o[2], o[3]);
-        } else {
-          sts128(lo, o[0], o[1], o[2], o[3]);
-          sts128(hi, o[4], o[5], o[6], o[7]);
-        }
+        sts128(base + at_a + uint32_t(n * RPP * 128), o[0], o[1], o[2], o[3]);
+        sts128(base + at_b + uint32_t(n * RPP * 128), o[4], o[5], o[6], o[7]);
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
     };
     uint4 wk[NP], wv[NP];
-    int ids = fetch_ids(0), next = fetch_ids(1);
+    int ids = checked(fetch_ids(0), 0), raw = fetch_ids(1);
     load(0, 0, ids, wk);
-    float2 sc = fetch_scales(ids), sc_next = fetch_scales(next);
-    bool ok = true;
+    load(1, 0, ids, wv);
+    float2 sc = fetch_scales(ids);
+    bool ok = true, k_free = true, v_free = true;
+    int st = 0;
+    uint32_t phase = 1;
     for (int i = 0; i < n_tiles && ok; ++i) {
-      const int st = i & 1;
-      const uint32_t par = uint32_t((i >> 1) & 1) ^ 1u;
-      load(1, i, ids, wv);
-      // the tile's scales (every warp reads them: it needs to know which groups have a V scale)
-      const float s_k = sc.x, s_v = sc.y;
-      const unsigned has = __ballot_sync(0xffffffffu, ids >= 0), live_v = __ballot_sync(0xffffffffu, s_v >= kKpLeastScale);
-      ok = __all_sync(0xffffffffu, kp_wait(&sh->k_empty[st], par, sh, p.err));
+      const bool here = lane < C::KG && ids >= 0;
+      const float s_k = here ? sc.x : 0.f, s_v = here ? sc.y : 0.f;
+      const unsigned has = __ballot_sync(0xffffffffu, here), live_v = __ballot_sync(0xffffffffu, s_v >= kKpLeastScale);
+      if (!k_free) ok = kp_wait_warp(&sh->k_empty[st], phase, sh, p.err);
       if (!ok) break;
       if (tid < C::KG) {
         // a page without a V scale counts in the sum of p like any other: its values are zeros at a stand-in scale
         const float v = fmaxf(s_v, kKpLeastScale);
-        sh->ks[i & 3][tid] = s_k;
-        sh->lv[i & 3][tid] = __log2f(v);
-        sh->iv[i & 3][tid] = __fdiv_rn(1.f, v);
+        sh->ks[i & 7][tid] = s_k;
+        sh->lv[i & 7][tid] = __log2f(v);
+        sh->iv[i & 7][tid] = __fdiv_rn(1.f, v);
       }
       store(k0 + uint32_t(st) * C::kKV, wk, has);
       if (lane == 0) mbar_arrive(&sh->k_full[st]);
-      load(0, i + 1, next, wk);
-      ids = next;
-      next = fetch_ids(i + 2);
-      sc = sc_next;
-      ok = __all_sync(0xffffffffu, kp_wait(&sh->v_empty[st], par, sh, p.err));
+      ids = checked(raw, i + 1);
+      load(0, i + 1, ids, wk);
+      sc = fetch_scales(ids);
+      raw = fetch_ids(i + 2);
+      if (!v_free) ok = kp_wait_warp(&sh->v_empty[st], phase, sh, p.err);
       if (!ok) break;
       store(v0 + uint32_t(st) * C::kKV, wv, live_v);
       if (lane == 0) mbar_arrive(&sh->v_full[st]);
-      sc_next = fetch_scales(next);
+      load(1, i + 1, ids, wv);
+      if (++st == C::kStages) { st = 0; phase ^= 1u; }
+      // (a look at a barrier costs a warp about 150 clocks if it waits for the answer)
+      k_free = mbar_test_wait(&sh->k_empty[st], phase);
+      v_free = mbar_test_wait(&sh->v_empty[st], phase);
+      k_free = __all_sync(0xffffffffu, k_free);
+      v_free = __all_sync(0xffffffffu, v_free);
     }
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      bool ok = true;
-      auto qk = [&](int i, int t, int slot) {  // scores of key tile i
-        const uint32_t kb = k0 + uint32_t(i & 1) * C::kKV, qb = q0 + uint32_t(t) * C::kQ;
-#pragma unroll
-        for (int d = 0; d < D; d += 16) {
-          const uint32_t in = uint32_t(d & 63) * 2u;
-          tc_mma_ss_f16(tmem + uint32_t(slot) * C::kSCols, sw128_desc(qb + uint32_t(d >> 6) * (128u * 128u) + in),
-                        sw128_desc(kb + uint32_t(d >> 6) * uint32_t(C::TK * 128) + in), C::kIdescQK, d ? 1u : 0u);
-        }
-        tc_commit(&sh->s_full[slot]);
-      };
-      auto pv = [&](int i, int t, int slot) {
-        const uint32_t vb = v0 + uint32_t(i & 1) * C::kKV;
-#pragma unroll
-        for (int k = 0; k < C::TK; k += 16)
-          tc_mma_ts_f16(tmem + C::kOCol + uint32_t(t * D), tmem + uint32_t(slot) * C::kSCols + uint32_t(k / 2),
-                        sw128_mn_desc(vb + uint32_t(k) * 128u, C::TK * 128), C::kIdescPV, (i | k) ? 1u : 0u);
-      };
-      // p_full: phase 0 is q, phase 1 + n the n-th P' of the slot (with one row tile, slot 1 has no q phase)
-      for (int t = 0; t < C::kTiles && ok; ++t) ok = kp_wait(&sh->p_full[t], 0, sh, p.err);
-      if (ok) ok = kp_wait(&sh->k_full[0], 0, sh, p.err);
-      if (ok) {
-        tc_fence_after();
-        for (int t = 0; t < C::kTiles; ++t) qk(0, t, t);
-        tc_commit(&sh->k_empty[0]);
-      }
+  } else if (lane == 0) {
+    // ------------------------------------------------ MMA issuers
+    // The issuing thread's own instructions must stay few: descriptors are bases with constants added to their low
+    // word (the address field; shared memory ends below 256 KiB, so nothing carries out of it), and as a wait costs
+    // about 150 clocks even on a barrier that is complete (measured), each barrier is probed ahead of the MMAs that
+    // come before it and waited for only where the probe found it incomplete.
+    auto plus = [](uint64_t d, uint32_t bytes) {
+      return (d & 0xFFFFFFFF00000000ull) | uint64_t(uint32_t(d) + (bytes >> 4));
+    };
+    bool ok = true;
+    int st = 0;          // stage of tile i
+    uint32_t phase = 0;  // and its phase
+    if (warp == kMmaWarp) {
+      // ---- scores: tile i into buffer i & 1, whose P' the product of tile i - 2 must have read
+      const uint64_t qd0 = sw128_desc(q0), kd0 = sw128_desc(k0);
+      ok = kp_wait(&sh->q_full, 0, sh, p.err);
+      bool k_in = false, f_in = false;
       for (int i = 0; i < n_tiles && ok; ++i) {
-        const uint32_t full = uint32_t((i >> 1) & 1), nfull = uint32_t(((i + 1) >> 1) & 1);
-        if constexpr (C::kTiles == 2) {
-          for (int t = 0; t < 2 && ok; ++t) {
-            ok = kp_wait(&sh->p_full[t], uint32_t((i + 1) & 1), sh, p.err);
-            if (ok && t == 0) ok = kp_wait(&sh->v_full[i & 1], full, sh, p.err);
-            if (!ok) break;
-            tc_fence_after();
-            pv(i, t, t);
-            if (t == 1) tc_commit(&sh->v_empty[i & 1]);
-            if (i + 1 < n_tiles) {
-              if (t == 0) ok = kp_wait(&sh->k_full[(i + 1) & 1], nfull, sh, p.err);
-              if (!ok) break;
-              tc_fence_after();
-              qk(i + 1, t, t);
-              if (t == 1) tc_commit(&sh->k_empty[(i + 1) & 1]);
-            }
-          }
-        } else {
-          if (i + 1 < n_tiles) {
-            ok = kp_wait(&sh->k_full[(i + 1) & 1], nfull, sh, p.err);
-            if (!ok) break;
-            tc_fence_after();
-            qk(i + 1, 0, (i + 1) & 1);
-            tc_commit(&sh->k_empty[(i + 1) & 1]);
-          }
-          // slot 0's barrier had one phase more (q)
-          ok = kp_wait(&sh->p_full[i & 1], uint32_t(((i >> 1) + ((i & 1) ? 0 : 1)) & 1), sh, p.err);
-          if (ok) ok = kp_wait(&sh->v_full[i & 1], full, sh, p.err);
+        if (!k_in) ok = kp_wait(&sh->k_full[st], phase, sh, p.err);
+        if (!ok) break;
+        const uint64_t kd = plus(kd0, uint32_t(st) * C::kKV);
+        for (int t = 0; t < C::kTiles; ++t) {
+          if (i >= 2 && !f_in) ok = kp_wait(&sh->pv_done[2 * t + (i & 1)], uint32_t(((i - 2) >> 1) & 1), sh, p.err);
           if (!ok) break;
           tc_fence_after();
-          pv(i, 0, i & 1);
-          tc_commit(&sh->v_empty[i & 1]);
-          tc_commit(&sh->pv_done);
+          f_in = t + 1 < C::kTiles ? i >= 2 && mbar_test_wait(&sh->pv_done[2 + (i & 1)], uint32_t(((i - 2) >> 1) & 1)) : false;
+          const uint64_t qd = plus(qd0, uint32_t(t) * C::kQ);
+          const int slot = 2 * t + (i & 1);
+          const uint32_t at = tmem + uint32_t(slot) * C::kSCols;
+#pragma unroll
+          for (int d = 0; d < D; d += 16)
+            tc_mma_ss_f16(at, plus(qd, uint32_t(d >> 6) * (128u * 128u) + uint32_t(d & 63) * 2u),
+                          plus(kd, uint32_t(d >> 6) * uint32_t(C::TK * 128) + uint32_t(d & 63) * 2u), C::kIdescQK,
+                          d ? 1u : 0u);
+          tc_commit(&sh->s_full[slot]);
         }
+        if (!ok) break;
+        tc_commit(&sh->k_empty[st]);
+        if (++st == C::kStages) { st = 0; phase ^= 1u; }
+        k_in = i + 1 < n_tiles && mbar_test_wait(&sh->k_full[st], phase);
+        f_in = i >= 1 && mbar_test_wait(&sh->pv_done[(i + 1) & 1], uint32_t(((i - 1) >> 1) & 1));
       }
-      tc_commit(&sh->drain);  // everything issued so far
-      mbar_wait_bounded(&sh->drain, 0, p.err, 1u << 20);
+    } else {
+      // ---- O += P' V
+      const uint64_t vd0 = sw128_mn_desc(v0, C::TK * 128);
+      bool v_in = false, p_in = false;
+      for (int i = 0; i < n_tiles && ok; ++i) {
+        const uint32_t pp = uint32_t((i >> 1) & 1);
+        if (!v_in) ok = kp_wait(&sh->v_full[st], phase, sh, p.err);
+        const uint64_t vd = plus(vd0, uint32_t(st) * C::kKV);
+        for (int t = 0; t < C::kTiles && ok; ++t) {
+          if (!p_in) ok = kp_wait(&sh->p_full[2 * t + (i & 1)], pp, sh, p.err);
+          if (!ok) break;
+          tc_fence_after();
+          p_in = t + 1 < C::kTiles ? mbar_test_wait(&sh->p_full[2 + (i & 1)], pp) : false;
+          const uint32_t at = tmem + C::kOCol + uint32_t(t * D), ap = tmem + uint32_t(2 * t + (i & 1)) * C::kSCols;
+#pragma unroll
+          for (int k = 0; k < C::TK; k += 16)
+            tc_mma_ts_f16(at, ap + uint32_t(k / 2), plus(vd, uint32_t(k) * 128u), C::kIdescPV, (i | k) ? 1u : 0u);
+          tc_commit(&sh->pv_done[2 * t + (i & 1)]);
+        }
+        if (!ok) break;
+        tc_commit(&sh->v_empty[st]);
+        if (++st == C::kStages) { st = 0; phase ^= 1u; }
+        v_in = i + 1 < n_tiles && mbar_test_wait(&sh->v_full[st], phase);
+        p_in = i + 1 < n_tiles && mbar_test_wait(&sh->p_full[(i + 1) & 1], uint32_t(((i + 1) >> 1) & 1));
+      }
     }
+    tc_commit(&sh->drain);  // everything that this thread issued
+    mbar_wait_bounded(&sh->drain, 0, p.err, 1u << 20);
   }
   tc_fence_before();
   __syncthreads();
