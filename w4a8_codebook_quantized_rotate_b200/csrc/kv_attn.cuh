@@ -27,13 +27,19 @@
 // last of them to arrive adds in CTA order (the result does not depend on
 // the order of arrival).
 //
-// A producer warp keeps a ring of TMA tiles per consumer warp full (8 lanes,
-// one per consumer), with the block table and the page scales of the next
-// tiles fetched ahead.  K fragments are 16-byte reads of a token's codes in
-// the order d = 64 c + 16 t + 4 s + e (q's fragments use the same order); V
-// fragments come from ldmatrix.trans on code pairs, whose even and odd codes
-// make two output tiles.  Tokens of an 8-token group are taken in the order
-// tau, which keeps the swizzled K reads free of bank conflicts.
+// Each warp feeds itself: a ring of TMA tiles, refilled by its own lanes as
+// soon as it has used a tile, with the page ids and scales of its next tiles
+// held one to a lane and fetched a batch ahead.  (A producer warp with a lane
+// per consumer ran those lanes' divergent steps one after the other, about
+// 1000 clocks a tile: 123 us for 131072 keys of 24/4 heads of 256, against
+// the 41 us that the bytes take.)  The next row tile's first loads go out
+// before this one is joined.
+//
+// K fragments are 16-byte reads of a token's codes in the order d = 64 c +
+// 16 t + 4 s + e (q's fragments use the same order); V fragments come from
+// ldmatrix.trans on code pairs, whose even and odd codes make two output
+// tiles.  Tokens of an 8-token group are taken in the order tau, which keeps
+// the swizzled K reads free of bank conflicts.
 #pragma once
 
 #include <cuda.h>
@@ -45,8 +51,8 @@
 
 namespace w4a8 {
 
-constexpr int kKaWarps = 8;                      // consumer warps
-constexpr int kKaThreads = (kKaWarps + 1) * 32;  // and a producer warp
+constexpr int kKaWarps = 8;
+constexpr int kKaThreads = kKaWarps * 32;
 constexpr int kKaStages = 3;
 constexpr int kKaRows = 16;
 constexpr int kKaTileBytes = 4096;               // one warp's K (or V) tile
@@ -59,6 +65,7 @@ struct KaCfg {
   static constexpr int kItem = kKaWarps * TK;  // keys of an item
   static constexpr int kSteps = D / 16;
   static constexpr bool kQRegs = D <= 128;     // q fragments in registers
+  static constexpr int kBatch = 32 / KG;       // tiles whose page ids a warp holds
   static constexpr uint32_t kRowBytes = D < 128 ? D : 128;  // bytes of a row in a TMA box
   static constexpr int kColBlocks = D / int(kRowBytes);
   static constexpr uint32_t kRing = kKaWarps * kKaStages * 2 * kKaTileBytes;
@@ -84,7 +91,6 @@ struct KaParams {
 
 struct KaShared {
   uint64_t full[kKaWarps][kKaStages];
-  uint64_t empty[kKaWarps][kKaStages];
   float scales[kKaWarps][kKaStages][3][4];  // ks, vs, log2(vs) of each group of 16 keys
   float warp_m[kKaWarps][kKaRows];
   float warp_l[kKaWarps][kKaRows];
@@ -248,7 +254,6 @@ __global__ void __launch_bounds__(kKaThreads, 1)
     for (int w = 0; w < kKaWarps; ++w)
       for (int s = 0; s < kKaStages; ++s) {
         mbar_init(&sh->full[w][s], 1);
-        mbar_init(&sh->empty[w][s], 1);
       }
     sh->abort = 0;
     fence_barrier_init();
@@ -311,137 +316,88 @@ __global__ void __launch_bounds__(kKaThreads, 1)
   walk.small_only = sh->small_only;
   walk.load(p);
 
-  if (warp == kKaWarps) {
-    // ------------------------------------------------ producer: lane w fills consumer w's ring
-    if (lane < kKaWarps) {
-      if (lane == 0) {
-        tma_prefetch_desc(&tmap_k);
-        tma_prefetch_desc(&tmap_v);
-      }
-      const int w = lane;
-      const int boxes = C::TK >> p.box_shift, per = 1 << (p.box_shift - 4);  // boxes of a tile, key groups of a box
-      struct Tile {
-        int b, head, key;  // key < 0: none
-        int end;           // keys of the sequence
-        int id[C::KG];
-        float ks[C::KG], vs[C::KG];
-      };
-      KaSeg g;
-      int item = 0, stop = 0;
-      bool more = true;
-      auto advance = [&](Tile& t) {  // the next tile of this lane, without its page ids
-        t.key = -1;
-        while (more) {
-          if (item >= stop) {
-            more = walk.next(p, g);
-            if (!more) return;
-            item = g.item0;
-            stop = g.item1;
-          }
-          const int key = g.key0 + (item * kKaWarps + w) * C::TK;
-          ++item;
-          if (key < g.range.hi && key + C::TK > g.range.lo) {
-            t.b = g.b;
-            t.head = g.head;
-            t.key = key;
-            t.end = g.s.kv_len;
-            return;
-          }
-        }
-      };
-      auto fetch_ids = [&](Tile& t) {
+  // -------------------------------------------------- the warp's feed
+  // Tiles of a row tile that this warp takes: items [fi, fend) with a key in range.  Lane l holds the page id and
+  // scales of key group l % KG of tile fbase + l / KG; the batch after it is on its way.
+  const int per = 1 << (p.box_shift - 4);  // key groups of a TMA box
+  const int fgroup = lane % C::KG, ftile = lane / C::KG;
+  int fi = 0, fend = 0, fbase = 0, fstage = 0, fid = -1, nraw = -1;
+  float fks = 0.f, fvs = 0.f;
+  bool fload = false;  // fks, fvs are of this batch
+  KaSeg fseg;
+  auto group_key = [&](int item) { return fseg.key0 + (item * kKaWarps + warp) * C::TK + 16 * fgroup; };
+  auto fetch_raw = [&](int base) {
+    const int item = base + ftile;
+    return item < fend && group_key(item) < fseg.range.hi
+               ? __ldg(p.batch.table + (long long)fseg.b * p.batch.table_stride + (group_key(item) >> p.cache.page_shift))
+               : -1;
+  };
+  auto take_batch = [&](int base) {  // nraw, fetched for `base`, becomes the batch at hand
+    fid = nraw;
+    if (fid >= p.cache.pages || (fid < 0 && base + ftile < fend && group_key(base + ftile) < fseg.range.hi)) {
+      record_error(p.err, kErrInput);
+      fid = -1;
+    }
+    fbase = base;
+    const long long at = (long long)max(fid, 0) * p.cache.kv_heads + fseg.head;
+    fks = __ldg(p.cache.scales[0] + at);
+    fvs = __ldg(p.cache.scales[1] + at);
+    nraw = fetch_raw(base + C::kBatch);
+  };
+  // Loads of tile fi into the next stage (its scales beside it).
+  auto issue = [&]() {
+    if (fi == fbase + C::kBatch) take_batch(fi);
+    const bool mine = fi == fbase + ftile;
+    const bool box = mine && fid >= 0 && fgroup % per == 0;
+    const unsigned boxes = __popc(__ballot_sync(0xffffffffu, box));
+    uint64_t* bar = &sh->full[warp][fstage];
+    if (lane == 0) mbar_arrive_expect_tx(bar, boxes * 2u * (uint32_t(D) << p.box_shift));
+    __syncwarp();
+    if (box) {
+      const uint32_t kt = ring + uint32_t((warp * kKaStages + fstage) * 2) * kKaTileBytes + uint32_t(16 * fgroup) * C::kRowBytes;
+      const int row = int((((long long)fid * p.cache.kv_heads + fseg.head) << p.cache.page_shift) +
+                          (group_key(fi) & ((1 << p.cache.page_shift) - 1)));
 #pragma unroll
-        for (int i = 0; i < C::KG; ++i) {
-          t.id[i] = -1;
-          if (t.key >= 0 && i < boxes && t.key + (i << p.box_shift) < t.end)
-            t.id[i] = __ldg(p.batch.table + (long long)t.b * p.batch.table_stride +
-                            ((t.key + (i << p.box_shift)) >> p.cache.page_shift));
-        }
-      };
-      auto fetch_scales = [&](Tile& t) {
-#pragma unroll
-        for (int i = 0; i < C::KG; ++i) {
-          t.ks[i] = t.vs[i] = 0.f;
-          if (t.key >= 0 && i < boxes && t.key + (i << p.box_shift) < t.end) {
-            if (t.id[i] >= 0 && t.id[i] < p.cache.pages) {
-              const long long at = (long long)t.id[i] * p.cache.kv_heads + t.head;
-              t.ks[i] = p.cache.scales[0][at];
-              t.vs[i] = p.cache.scales[1][at];
-            } else {
-              record_error(p.err, kErrInput);
-              t.id[i] = -1;
-            }
-          }
-        }
-      };
-      Tile t0, t1, t2;
-      advance(t0);
-      fetch_ids(t0);
-      advance(t1);
-      fetch_ids(t1);
-      fetch_scales(t0);
-      int stage = 0;
-      uint32_t phase = 0;
-      while (t0.key >= 0) {
-        advance(t2);
-        fetch_ids(t2);
-        fetch_scales(t1);
-        if (!ka_wait(&sh->empty[w][stage], phase ^ 1u, sh, p.err)) break;
-        uint32_t bytes = 0;
-#pragma unroll
-        for (int i = 0; i < C::KG; ++i)
-          if (i < boxes && t0.id[i] >= 0) bytes += 2u * (uint32_t(D) << p.box_shift);
-#pragma unroll
-        for (int i = 0; i < C::KG; ++i) {
-          const int box = i / per;
-          float ks = 0.f, vs = 0.f;
-#pragma unroll
-          for (int j = 0; j < C::KG; ++j)
-            if (j == box) ks = t0.ks[j], vs = t0.vs[j];
-          sh->scales[w][stage][0][i] = ks;
-          sh->scales[w][stage][1][i] = vs;
-          sh->scales[w][stage][2][i] = __log2f(vs);
-        }
-        mbar_arrive_expect_tx(&sh->full[w][stage], bytes);
-        const uint32_t kt = ring + uint32_t((w * kKaStages + stage) * 2) * kKaTileBytes, vt = kt + kKaTileBytes;
-#pragma unroll
-        for (int i = 0; i < C::KG; ++i) {
-          if (i < boxes && t0.id[i] >= 0) {
-            const int key = t0.key + (i << p.box_shift);
-            const int row = int((((long long)t0.id[i] * p.cache.kv_heads + t0.head) << p.cache.page_shift) +
-                                (key & ((1 << p.cache.page_shift) - 1)));
-            const uint32_t off = (uint32_t(i) << p.box_shift) * C::kRowBytes;
-#pragma unroll
-            for (int cb = 0; cb < C::kColBlocks; ++cb) {
-              tma_load_2d(kt + off + uint32_t(cb) * C::TK * 128u, &tmap_k, &sh->full[w][stage], cb * 128, row);
-              tma_load_2d(vt + off + uint32_t(cb) * C::TK * 128u, &tmap_v, &sh->full[w][stage], cb * 128, row);
-            }
-          }
-        }
-        if (++stage == kKaStages) { stage = 0; phase ^= 1u; }
-        t0 = t1;
-        t1 = t2;
-      }
-      if (sh->abort) {
-        // let the copies in flight land before the CTA exits (bounded: 50 us)
-        unsigned long long ta, tb;
-        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(ta));
-        do {
-          asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(tb));
-        } while (tb - ta < 50000ull);
+      for (int cb = 0; cb < C::kColBlocks; ++cb) {
+        tma_load_2d(kt + uint32_t(cb) * C::TK * 128u, &tmap_k, bar, cb * 128, row);
+        tma_load_2d(kt + kKaTileBytes + uint32_t(cb) * C::TK * 128u, &tmap_v, bar, cb * 128, row);
       }
     }
-    return;
-  }
+    if (mine) {
+      const float vs = fid >= 0 ? fvs : 0.f;
+      sh->scales[warp][fstage][0][fgroup] = fid >= 0 ? fks : 0.f;
+      sh->scales[warp][fstage][1][fgroup] = vs;
+      sh->scales[warp][fstage][2][fgroup] = __log2f(vs);
+    }
+    __syncwarp();
+    ++fi;
+    if (++fstage == kKaStages) fstage = 0;
+  };
+  // The first loads of a row tile; its tiles are [nfirst, fend).
+  int nfirst = 0;
+  auto start = [&](const KaSeg& s) {
+    fseg = s;
+    // items with key < hi, and key + TK > lo (key0 is at most TK - 1 below the lowest lo of the sequence)
+    const int first = s.range.lo - s.key0 - warp * C::TK;
+    fi = max(s.item0, first > 0 ? first / C::kItem + (first % C::kItem >= C::TK ? 1 : 0) : 0);
+    fend = min(s.item1, (s.range.hi - s.key0 - warp * C::TK + C::kItem - 1) / C::kItem);
+    nfirst = fi;
+    nraw = fetch_raw(fi);
+    if (fi < fend) take_batch(fi);
+    for (int n = 0; n < kKaStages && fi < fend; ++n) issue();
+  };
 
-  // -------------------------------------------------- consumers
+  // -------------------------------------------------- row tiles
   const int g = lane >> 2, t = lane & 3;
   const int tid = threadIdx.x;
   bool ok = true;  // every warp goes through every barrier below, even after a wait that gave up
   int stage = 0;
   uint32_t phase = 0;
-  KaSeg seg;
-  while (walk.next(p, seg)) {
+  KaSeg seg, nxt;
+  bool have = walk.next(p, seg);
+  if (have) start(seg);
+  while (have) {
+    const int c_first_item = nfirst, c_end_item = fend;
     // ---- q rows of the tile into fragments: half a warp per row
     const int rows = seg.s.q_len * p.group;
     {
@@ -506,15 +462,10 @@ __global__ void __launch_bounds__(kKaThreads, 1)
     // running maxima of the scores (m) and of score + log2(vs), less 15 (v); both as log2
     float m0 = -INFINITY, m1 = -INFINITY, v0 = -INFINITY, v1 = -INFINITY, l0 = 0.f, l1 = 0.f;
 
-    for (int item = seg.item0; item < seg.item1; ++item) {
+    for (int item = c_first_item; item < c_end_item; ++item) {
       const int key = seg.key0 + (item * kKaWarps + warp) * C::TK;
-      if (!(key < seg.range.hi && key + C::TK > seg.range.lo)) continue;
-      if (ok) {
-        const int got = lane == 0 ? int(ka_wait(&sh->full[warp][stage], phase, sh, p.err)) : 0;
-        __syncwarp();
-        ok = __shfl_sync(0xffffffffu, got, 0) != 0;
-      }
-      if (!ok) continue;
+      if (ok) ok = __all_sync(0xffffffffu, ka_wait(&sh->full[warp][stage], phase, sh, p.err));
+      if (!ok) break;
       const uint32_t kt = ring + uint32_t((warp * kKaStages + stage) * 2) * kKaTileBytes, vt = kt + kKaTileBytes;
       // ---- scores
       float s[C::TK / 8][4];
@@ -633,12 +584,14 @@ __global__ void __launch_bounds__(kKaThreads, 1)
           ka_mma(o[4 * c2 + 3], a, ka_codes(r[2], 0x4341u), ka_codes(r[3], 0x4341u));
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->empty[warp][stage]);
+      __syncwarp();  // every lane has used the tile: its stage takes the next one
+      if (fi < fend) issue();
       if (++stage == kKaStages) { stage = 0; phase ^= 1u; }
     }
 
-    // ---- join the warps
+    // ---- the next row tile's loads go out, then join the warps
+    const bool more = walk.next(p, nxt);
+    if (more && ok) start(nxt);
 #pragma unroll
     for (int off = 1; off < 4; off <<= 1) {
       l0 += __shfl_xor_sync(0xffffffffu, l0, off);
@@ -759,6 +712,16 @@ __global__ void __launch_bounds__(kKaThreads, 1)
       }
     }
     ka_sync();  // q fragments, warp_m and the join buffer are free again
+    seg = nxt;
+    have = more;
+  }
+  if (sh->abort) {
+    // let the copies in flight land before the CTA exits (bounded: 50 us)
+    unsigned long long ta, tb;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(ta));
+    do {
+      asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(tb));
+    } while (tb - ta < 50000ull);
   }
 }
 
