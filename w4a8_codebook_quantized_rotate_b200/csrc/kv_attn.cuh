@@ -69,7 +69,8 @@ struct KaCfg {
   static constexpr uint32_t kRowBytes = D < 128 ? D : 128;  // bytes of a row in a TMA box
   static constexpr int kColBlocks = D / int(kRowBytes);
   static constexpr uint32_t kRing = kKaWarps * kKaStages * 2 * kKaTileBytes;
-  static constexpr uint32_t kJoin = kKaWarps * kKaRows * 32 * 4;  // 32 columns of every warp
+  static constexpr uint32_t kJoin = kKaWarps * kKaRows * 32 * 4;  // 32 columns of every warp; the CTAs' weights
+  static_assert(kKaRows * kKaMaxCtas * 4 <= kJoin, "weights of a row tile's CTAs");
   static constexpr uint32_t kQ = kKaRows * D * 2;
   static constexpr size_t kSmem = 1024 + kRing + kJoin + kQ + 4096;
   static constexpr int kSlotFloats = kKaRows * D + 3 * kKaRows;
@@ -673,39 +674,67 @@ __global__ void __launch_bounds__(kKaThreads, 1)
       ka_sync();
       if (sh->last) {
         __threadfence();
+        // Slot of CTA c: its first row tile's, but for the CTA in which the tile starts behind another one.  A row's
+        // 16 threads take the CTAs' maxima and sums 16 at a time, and leave the CTAs' weights in shared memory; the
+        // accumulators then come in eight at a time (one at a time waits a round trip to L2 for each).
+        const int n_cta = c_last - c_first + 1;
+        const float* slot0 = p.part + (size_t)(c_first * 2 + (ka_first_item(c_first, total, ctas) >= seg.start ? 0 : 1)) * C::kSlotFloats;
         auto slot_of = [&](int c) {
-          return p.part + (size_t)(c * 2 + (ka_first_item(c, total, ctas) >= seg.start ? 0 : 1)) * C::kSlotFloats;
+          return c == 0 ? slot0 : p.part + (size_t)((c_first + c) * 2) * C::kSlotFloats;
         };
+        float* weight = join + jr * kKaMaxCtas;
         float top = -INFINITY, vtop = -INFINITY, sum = 0.f;
-        for (int c = c_first; c <= c_last; ++c) {
-          top = fmaxf(top, __ldcg(slot_of(c) + kKaRows * D + jr));
-          vtop = fmaxf(vtop, __ldcg(slot_of(c) + kKaRows * D + 2 * kKaRows + jr));
+        for (int c = jc; c < n_cta; c += 16) {
+          const float* m = slot_of(c) + kKaRows * D + jr;
+          const float cm = __ldcg(m), cl = __ldcg(m + kKaRows), cv = __ldcg(m + 2 * kKaRows);
+          const float nt = fmaxf(top, cm);
+          if (nt > -INFINITY) sum = sum * ex2(top - nt) + (cm > -INFINITY ? cl * ex2(cm - nt) : 0.f);
+          top = nt;
+          vtop = fmaxf(vtop, cv);
+          weight[c] = cv;
         }
+#pragma unroll
+        for (int off = 1; off < 16; off <<= 1) {
+          const float ot = __shfl_xor_sync(0xffffffffu, top, off), os = __shfl_xor_sync(0xffffffffu, sum, off);
+          const float nt = fmaxf(top, ot);
+          if (nt > -INFINITY) sum = sum * ex2(top - nt) + os * ex2(ot - nt);
+          top = nt;
+          vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, off));
+        }
+        for (int c = jc; c < n_cta; c += 16) weight[c] = weight[c] == -INFINITY ? 0.f : ex2(weight[c] - vtop);
+        __syncwarp();
         float acc[D / 16];
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) acc[i] = 0.f;
-        for (int c = c_first; c <= c_last; ++c) {
-          const float* src = slot_of(c);
-          const float cm = __ldcg(src + kKaRows * D + jr), cv = __ldcg(src + kKaRows * D + 2 * kKaRows + jr);
-          const float f = cv == -INFINITY ? 0.f : ex2(cv - vtop);
-          if (cm != -INFINITY) sum += ex2(cm - top) * __ldcg(src + kKaRows * D + kKaRows + jr);
+        constexpr int kAhead = D <= 128 ? 8 : 4;
+        for (int c0 = 0; c0 < n_cta; c0 += kAhead) {
+          float4 v[kAhead][D / 64];
 #pragma unroll
-          for (int i = 0; i < D / 16; i += 4) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(src + jr * D + jc * 4 + i * 16));
-            acc[i] += f * v.x;
-            acc[i + 1] += f * v.y;
-            acc[i + 2] += f * v.z;
-            acc[i + 3] += f * v.w;
+          for (int u = 0; u < kAhead; ++u) {
+            const float* src = slot_of(min(c0 + u, n_cta - 1)) + jr * D + jc * 4;
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) v[u][i] = __ldcg(reinterpret_cast<const float4*>(src + i * 64));
+          }
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u) {
+            const float f = c0 + u < n_cta ? weight[c0 + u] : 0.f;
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) {
+              acc[4 * i] += f * v[u][i].x;
+              acc[4 * i + 1] += f * v[u][i].y;
+              acc[4 * i + 2] += f * v[u][i].z;
+              acc[4 * i + 3] += f * v[u][i].w;
+            }
           }
         }
         const float n = vtop > -INFINITY ? __fdiv_rn(ex2(vtop - top), sum) : 0.f;
         if (row < rows) {
 #pragma unroll
-          for (int i = 0; i < D / 16; i += 4) {
-            const __nv_bfloat162 a = __floats2bfloat162_rn(acc[i] * n, acc[i + 1] * n);
-            const __nv_bfloat162 b = __floats2bfloat162_rn(acc[i + 2] * n, acc[i + 3] * n);
-            *reinterpret_cast<uint2*>(dst + jc * 4 + i * 16) =
-                make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+          for (int i = 0; i < D / 64; ++i) {
+            const __nv_bfloat162 x = __floats2bfloat162_rn(acc[4 * i] * n, acc[4 * i + 1] * n);
+            const __nv_bfloat162 y = __floats2bfloat162_rn(acc[4 * i + 2] * n, acc[4 * i + 3] * n);
+            *reinterpret_cast<uint2*>(dst + jc * 4 + i * 64) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
           }
         }
         if (tid == 0) p.counters[c_first] = 0u;  // ready for the next launch on this workspace
