@@ -229,7 +229,7 @@ cudaError_t ka_launch(const KaParams& p, const w4a8_kv_cache* c, int ctas, cudaS
         e != cudaSuccess)
       return e;
   }
-  return launch_pdl(kv_attention_kernel<D>, dim3(ctas), dim3(kKaThreads), C::kSmem, st, tk, tv, q);
+  return launch_pdl(kv_attention_kernel<D>, dim3(ctas), dim3(C::kThreads), C::kSmem, st, tk, tv, q);
 }
 
 // Shared-memory opt-ins of this file's kernels, once per device.
@@ -392,7 +392,7 @@ w4a8_status w4a8_kv_dequant(const w4a8_kv_cache* cache, const int32_t* ids, int6
 
 size_t w4a8_kv_attention_workspace_bytes(int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
   if (!ka_shape_ok(tokens, q_heads, kv_heads, head_dim)) return 0;
-  return kKaZeroBytes + size_t(kKaMaxCtas) * 2 * (size_t(kKaRows) * head_dim + 3 * kKaRows) * 4;
+  return kKaZeroBytes + size_t(kKaMaxCtas) * 2 * (size_t(kKaRows) * head_dim + 2 * kKaRows) * 4;
 }
 
 w4a8_status w4a8_kv_attention(const w4a8_heads* q, const w4a8_kv_cache* cache, const w4a8_kv_batch* batch, float scale,

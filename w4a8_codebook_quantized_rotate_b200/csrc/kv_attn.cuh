@@ -1,24 +1,27 @@
 // Attention of new tokens over the int8 paged cache, streaming kernel.
 //
-//   o_i = sum_j softmax_j(scale * ks[page j] * (q_i . k_j)) * vs[page j] * v_j
+//   o_i = sum_j P'_ij c_j / sum_j (P'_ij / vs_j),
+//   P'_ij = 2^(t_ij - z_i),  t_ij = (q_i . k_j) ks_j scale log2(e) + log2(vs_j)
 //
-// over the positions j <= i of the sequence (and j > i - window), k_j and v_j
-// the int8 codes.  The codes are exact in fp16, so both products run on
-// fp16 operands with fp32 accumulation, and the page scales stay outside:
-// ks multiplies the scores, vs the probabilities.
+// over the positions j <= i of the sequence (and j > i - window), which is
+// softmax(scale q_i . K_j) V_j with K_j = ks_j k_j, V_j = vs_j c_j: k_j, c_j are
+// the int8 codes, ks_j, vs_j their pages' scales.  The codes are exact in
+// fp16, so both products run on fp16 operands with fp32 accumulation.
 //   * q is taken to fp16 with a power of two per row (exact: bf16 has fewer
 //     significant bits, the power keeps its range).
-//   * p vs is taken to fp16 relative to the row's largest p vs so far, at
-//     2^15, with a running maximum of its own (page scales of one head may
-//     be far apart, and the largest p need not carry the largest share of
-//     the result), so what fp16 drops is below 2^-40 of the largest share.
-//     p itself is summed in fp32 under the usual running maximum.
+//   * P' is taken to fp16.  z_i is the running maximum of t_ij less 15: page
+//     scales of one head may be far apart, and the largest p need not carry
+//     the largest share of the result, so the reference is the share; what
+//     fp16 drops is below 2^-39 of the largest one.
+//   * the sum of p comes from P' before its rounding, in fp32, a page's worth
+//     at a time (times 1 / vs).
 //
 // The cache is read once, so at decode sizes its bytes bound the kernel
 // (6.5 TB/s: 23 bytes a clock and SM, against which the fp16 expansion of
 // the codes costs about one instruction per byte and 32 lanes).  A row tile
 // is 16 rows, the query heads of one key head (and neighbouring new tokens,
-// if the group is smaller); work is a list of items of 8 warps x TK keys,
+// if the group is smaller); work is a list of items of a TK-key tile per
+// warp,
 // [sequence][key head][row tile][item], of which every CTA takes an equal
 // contiguous share (one CTA per SM), so ragged batches and single long
 // contexts fill the GPU alike.  Each warp keeps its own running maximum, sum
@@ -51,9 +54,7 @@
 
 namespace w4a8 {
 
-constexpr int kKaWarps = 8;
-constexpr int kKaThreads = kKaWarps * 32;
-constexpr int kKaStages = 3;
+constexpr float kKvLeastScale = 0x1p-80f;  // V scales below count as 0 (in the sum of p, as this)
 constexpr int kKaRows = 16;
 constexpr int kKaTileBytes = 4096;               // one warp's K (or V) tile
 constexpr int kKaMaxCtas = 160;
@@ -62,18 +63,23 @@ template <int D>
 struct KaCfg {
   static constexpr int TK = kKaTileBytes / D;  // keys of a warp's tile: 64, 32, 16
   static constexpr int KG = TK / 16;           // groups of 16 keys
-  static constexpr int kItem = kKaWarps * TK;  // keys of an item
+  // 12 warps with 168 registers hide latencies better than 8 with 250 (the kernel is bound by its dependent
+  // instructions, not by memory); heads of 256 need the registers for their accumulator.
+  static constexpr int kWarps = 8;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kStages = 3;
+  static constexpr int kItem = kWarps * TK;  // keys of an item
   static constexpr int kSteps = D / 16;
   static constexpr bool kQRegs = D <= 128;     // q fragments in registers
   static constexpr int kBatch = 32 / KG;       // tiles whose page ids a warp holds
   static constexpr uint32_t kRowBytes = D < 128 ? D : 128;  // bytes of a row in a TMA box
   static constexpr int kColBlocks = D / int(kRowBytes);
-  static constexpr uint32_t kRing = kKaWarps * kKaStages * 2 * kKaTileBytes;
-  static constexpr uint32_t kJoin = kKaWarps * kKaRows * 32 * 4;  // 32 columns of every warp; the CTAs' weights
+  static constexpr uint32_t kRing = kWarps * kStages * 2 * kKaTileBytes;
+  static constexpr uint32_t kJoin = kWarps * kKaRows * 32 * 4;  // 32 columns of every warp; the CTAs' weights
   static_assert(kKaRows * kKaMaxCtas * 4 <= kJoin, "weights of a row tile's CTAs");
   static constexpr uint32_t kQ = kKaRows * D * 2;
   static constexpr size_t kSmem = 1024 + kRing + kJoin + kQ + 4096;
-  static constexpr int kSlotFloats = kKaRows * D + 3 * kKaRows;
+  static constexpr int kSlotFloats = kKaRows * D + 2 * kKaRows;
 };
 
 struct KaParams {
@@ -90,12 +96,12 @@ struct KaParams {
   unsigned* err;
 };
 
+constexpr int kKaMaxWarps = 12, kKaMaxStages = 3;
 struct KaShared {
-  uint64_t full[kKaWarps][kKaStages];
-  float scales[kKaWarps][kKaStages][3][4];  // ks, vs, log2(vs) of each group of 16 keys
-  float warp_m[kKaWarps][kKaRows];
-  float warp_l[kKaWarps][kKaRows];
-  float warp_v[kKaWarps][kKaRows];
+  uint64_t full[kKaMaxWarps][kKaMaxStages];
+  float scales[kKaMaxWarps][kKaMaxStages][3][4];  // ks, log2(vs), 1 / vs of each group of 16 keys
+  float warp_z[kKaMaxWarps][kKaRows];
+  float warp_l[kKaMaxWarps][kKaRows];
   float row_factor[kKaRows];
   long long base;   // first item of sequence b0
   long long total;  // items of the batch
@@ -216,8 +222,6 @@ __device__ __forceinline__ uint32_t ka_codes(uint32_t biased, uint32_t sel) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-__device__ __forceinline__ void ka_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kKaWarps * 32) : "memory"); }
-
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -236,7 +240,7 @@ __device__ __forceinline__ uint32_t ka_at(uint32_t r, uint32_t c) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kKaThreads, 1)
+__global__ void __launch_bounds__(KaCfg<D>::kThreads, 1)
     kv_attention_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                         const KaParams p) {
   using C = KaCfg<D>;
@@ -252,8 +256,8 @@ __global__ void __launch_bounds__(kKaThreads, 1)
   pdl_wait();
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
-    for (int w = 0; w < kKaWarps; ++w)
-      for (int s = 0; s < kKaStages; ++s) {
+    for (int w = 0; w < C::kWarps; ++w)
+      for (int s = 0; s < C::kStages; ++s) {
         mbar_init(&sh->full[w][s], 1);
       }
     sh->abort = 0;
@@ -326,7 +330,7 @@ __global__ void __launch_bounds__(kKaThreads, 1)
   float fks = 0.f, fvs = 0.f;
   bool fload = false;  // fks, fvs are of this batch
   KaSeg fseg;
-  auto group_key = [&](int item) { return fseg.key0 + (item * kKaWarps + warp) * C::TK + 16 * fgroup; };
+  auto group_key = [&](int item) { return fseg.key0 + (item * C::kWarps + warp) * C::TK + 16 * fgroup; };
   auto fetch_raw = [&](int base) {
     const int item = base + ftile;
     return item < fend && group_key(item) < fseg.range.hi
@@ -355,7 +359,7 @@ __global__ void __launch_bounds__(kKaThreads, 1)
     if (lane == 0) mbar_arrive_expect_tx(bar, boxes * 2u * (uint32_t(D) << p.box_shift));
     __syncwarp();
     if (box) {
-      const uint32_t kt = ring + uint32_t((warp * kKaStages + fstage) * 2) * kKaTileBytes + uint32_t(16 * fgroup) * C::kRowBytes;
+      const uint32_t kt = ring + uint32_t((warp * C::kStages + fstage) * 2) * kKaTileBytes + uint32_t(16 * fgroup) * C::kRowBytes;
       const int row = int((((long long)fid * p.cache.kv_heads + fseg.head) << p.cache.page_shift) +
                           (group_key(fi) & ((1 << p.cache.page_shift) - 1)));
 #pragma unroll
@@ -365,14 +369,14 @@ __global__ void __launch_bounds__(kKaThreads, 1)
       }
     }
     if (mine) {
-      const float vs = fid >= 0 ? fvs : 0.f;
+      const float vs = fid >= 0 ? fmaxf(fvs, kKvLeastScale) : kKvLeastScale;
       sh->scales[warp][fstage][0][fgroup] = fid >= 0 ? fks : 0.f;
-      sh->scales[warp][fstage][1][fgroup] = vs;
-      sh->scales[warp][fstage][2][fgroup] = __log2f(vs);
+      sh->scales[warp][fstage][1][fgroup] = __log2f(vs);
+      sh->scales[warp][fstage][2][fgroup] = __fdividef(1.f, vs);
     }
     __syncwarp();
     ++fi;
-    if (++fstage == kKaStages) fstage = 0;
+    if (++fstage == C::kStages) fstage = 0;
   };
   // The first loads of a row tile; its tiles are [nfirst, fend).
   int nfirst = 0;
@@ -385,7 +389,7 @@ __global__ void __launch_bounds__(kKaThreads, 1)
     nfirst = fi;
     nraw = fetch_raw(fi);
     if (fi < fend) take_batch(fi);
-    for (int n = 0; n < kKaStages && fi < fend; ++n) issue();
+    for (int n = 0; n < C::kStages && fi < fend; ++n) issue();
   };
 
   // -------------------------------------------------- row tiles
@@ -401,7 +405,7 @@ __global__ void __launch_bounds__(kKaThreads, 1)
     const int c_first_item = nfirst, c_end_item = fend;
     // ---- q rows of the tile into fragments: half a warp per row
     const int rows = seg.s.q_len * p.group;
-    {
+    if (warp < kKaRows / 2) {
       const int r = 2 * warp + (lane >> 4), l16 = lane & 15;
       const int row = seg.tile * kKaRows + r;
       float v[D / 16];
@@ -426,8 +430,9 @@ __global__ void __launch_bounds__(kKaThreads, 1)
       for (int off = 8; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
       // the row's power of two: its largest value lands in [2^13, 2^14)
       const int e = min(100, max(-100, 127 + 13 - int(__float_as_uint(top) >> 23)));
-      const float up = __uint_as_float(uint32_t(127 + e) << 23);
-      if (l16 == 0) sh->row_factor[r] = __uint_as_float(uint32_t(127 - e) << 23) * p.scale_log2;
+      // (a negative scale goes into q, so that larger products stay larger scores)
+      const float up = copysignf(__uint_as_float(uint32_t(127 + e) << 23), p.scale_log2);
+      if (l16 == 0) sh->row_factor[r] = __uint_as_float(uint32_t(127 - e) << 23) * fabsf(p.scale_log2);
 #pragma unroll
       for (int i = 0; i < D / 16; i += 2) {
         const int d = l16 * (D / 16) + i;
@@ -437,7 +442,7 @@ __global__ void __launch_bounds__(kKaThreads, 1)
         qf[(step * 32 + ln) * 4 + reg] = *reinterpret_cast<const uint32_t*>(&h);
       }
     }
-    ka_sync();
+    __syncthreads();
     uint32_t qr[C::kQRegs ? C::kSteps : 1][4];
     if constexpr (C::kQRegs) {
 #pragma unroll
@@ -460,14 +465,13 @@ __global__ void __launch_bounds__(kKaThreads, 1)
     float o[D / 8][4];
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    // running maxima of the scores (m) and of score + log2(vs), less 15 (v); both as log2
-    float m0 = -INFINITY, m1 = -INFINITY, v0 = -INFINITY, v1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    float z0 = -INFINITY, z1 = -INFINITY, l0 = 0.f, l1 = 0.f;
 
     for (int item = c_first_item; item < c_end_item; ++item) {
-      const int key = seg.key0 + (item * kKaWarps + warp) * C::TK;
+      const int key = seg.key0 + (item * C::kWarps + warp) * C::TK;
       if (ok) ok = __all_sync(0xffffffffu, ka_wait(&sh->full[warp][stage], phase, sh, p.err));
       if (!ok) break;
-      const uint32_t kt = ring + uint32_t((warp * kKaStages + stage) * 2) * kKaTileBytes, vt = kt + kKaTileBytes;
+      const uint32_t kt = ring + uint32_t((warp * C::kStages + stage) * 2) * kKaTileBytes, vt = kt + kKaTileBytes;
       // ---- scores
       float s[C::TK / 8][4];
 #pragma unroll
@@ -498,48 +502,41 @@ __global__ void __launch_bounds__(kKaThreads, 1)
           }
         }
       }
-      // ---- running maxima and sum
-      float t0 = -INFINITY, t1 = -INFINITY, x0 = -INFINITY, x1 = -INFINITY;
+      // ---- the rows' references
+      const float* ks = sh->scales[warp][stage][0];
+      const float* lv = sh->scales[warp][stage][1];
+      const float* iv = sh->scales[warp][stage][2];
       const bool edge = key + C::TK - 1 > lim_min || key < low_max;
+      if (edge) {
+#pragma unroll
+        for (int j = 0; j < C::TK / 8; ++j) {
+          const int ka = key + 8 * j + int(ka_tau<D>(2 * t)), kc = key + 8 * j + int(ka_tau<D>(2 * t + 1));
+          if (ka > lim[0] || ka < low[0]) s[j][0] = -INFINITY;
+          if (kc > lim[0] || kc < low[0]) s[j][1] = -INFINITY;
+          if (ka > lim[1] || ka < low[1]) s[j][2] = -INFINITY;
+          if (kc > lim[1] || kc < low[1]) s[j][3] = -INFINITY;
+        }
+      }
+      float x0 = -INFINITY, x1 = -INFINITY;
 #pragma unroll
       for (int kb = 0; kb < C::KG; ++kb) {
-        const float ks = sh->scales[warp][stage][0][kb], lv = sh->scales[warp][stage][2][kb] - 15.f;
-        float g0 = -INFINITY, g1 = -INFINITY;
-#pragma unroll
-        for (int j = 2 * kb; j < 2 * kb + 2; ++j) {
-          s[j][0] *= f0 * ks;
-          s[j][1] *= f0 * ks;
-          s[j][2] *= f1 * ks;
-          s[j][3] *= f1 * ks;
-          if (edge) {
-            const int ka = key + 8 * j + int(ka_tau<D>(2 * t)), kc = key + 8 * j + int(ka_tau<D>(2 * t + 1));
-            if (ka > lim[0] || ka < low[0]) s[j][0] = -INFINITY;
-            if (kc > lim[0] || kc < low[0]) s[j][1] = -INFINITY;
-            if (ka > lim[1] || ka < low[1]) s[j][2] = -INFINITY;
-            if (kc > lim[1] || kc < low[1]) s[j][3] = -INFINITY;
-          }
-          g0 = fmaxf(g0, fmaxf(s[j][0], s[j][1]));
-          g1 = fmaxf(g1, fmaxf(s[j][2], s[j][3]));
-        }
-        t0 = fmaxf(t0, g0);
-        t1 = fmaxf(t1, g1);
-        x0 = fmaxf(x0, g0 + lv);
-        x1 = fmaxf(x1, g1 + lv);
+        const float g0 = fmaxf(fmaxf(s[2 * kb][0], s[2 * kb][1]), fmaxf(s[2 * kb + 1][0], s[2 * kb + 1][1]));
+        const float g1 = fmaxf(fmaxf(s[2 * kb][2], s[2 * kb][3]), fmaxf(s[2 * kb + 1][2], s[2 * kb + 1][3]));
+        const float k = ks[kb], off = lv[kb] - 15.f;
+        // (fmaxf drops the NaN of a wholly masked group under a K scale of 0)
+        x0 = fmaxf(x0, fmaf(g0, f0 * k, off));
+        x1 = fmaxf(x1, fmaf(g1, f1 * k, off));
       }
 #pragma unroll
       for (int off = 1; off < 4; off <<= 1) {
-        t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, off));
-        t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, off));
         x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, off));
         x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, off));
       }
-      const float n0 = fmaxf(m0, t0), n1 = fmaxf(m1, t1), y0 = fmaxf(v0, x0), y1 = fmaxf(v1, x1);
-      const float u0 = n0 == -INFINITY ? 0.f : n0, u1 = n1 == -INFINITY ? 0.f : n1;
-      const float z0 = y0 == -INFINITY ? 0.f : y0, z1 = y1 == -INFINITY ? 0.f : y1;
-      l0 *= ex2(m0 - u0);
-      l1 *= ex2(m1 - u1);
-      const float r0 = ex2(v0 - z0), r1 = ex2(v1 - z1);
-      if (__any_sync(0xffffffffu, r0 != 1.f || r1 != 1.f)) {
+      if (__any_sync(0xffffffffu, x0 > z0 || x1 > z1)) {
+        const float n0 = fmaxf(z0, x0), n1 = fmaxf(z1, x1);
+        const float r0 = z0 == -INFINITY ? 0.f : ex2(z0 - n0), r1 = z1 == -INFINITY ? 0.f : ex2(z1 - n1);
+        l0 *= r0;
+        l1 *= r1;
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) {
           o[i][0] *= r0;
@@ -547,29 +544,36 @@ __global__ void __launch_bounds__(kKaThreads, 1)
           o[i][2] *= r1;
           o[i][3] *= r1;
         }
+        z0 = n0;
+        z1 = n1;
       }
-      m0 = n0;
-      m1 = n1;
-      v0 = y0;
-      v1 = y1;
-      // what takes p to the scale of v (times vs); where it is out of range, p is 0
-      const float c0 = fminf(ex2(u0 - z0), 0x1p100f), c1 = fminf(ex2(u1 - z1), 0x1p100f);
-      // ---- probabilities, and their product with V
+      const float u0 = z0 == -INFINITY ? 0.f : z0, u1 = z1 == -INFINITY ? 0.f : z1;
+      // ---- P', the sum of p, and the product with V
 #pragma unroll
       for (int kb = 0; kb < C::KG; ++kb) {
-        const float vs = sh->scales[warp][stage][1][kb];
-        const float vs0 = fminf(vs * c0, 0x1p100f), vs1 = fminf(vs * c1, 0x1p100f);
+        const float k0 = f0 * ks[kb], k1 = f1 * ks[kb], o0 = lv[kb] - u0, o1 = lv[kb] - u1, w = iv[kb];
         uint32_t a[4];
+        float s0 = 0.f, s1 = 0.f;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float* x = s[2 * kb + i];
-          const float p0 = ex2(x[0] - u0), p1 = ex2(x[1] - u0), p2 = ex2(x[2] - u1), p3 = ex2(x[3] - u1);
-          l0 += p0 + p1;
-          l1 += p2 + p3;
-          const __half2 h0 = __floats2half2_rn(p0 * vs0, p1 * vs0), h1 = __floats2half2_rn(p2 * vs1, p3 * vs1);
+          const float* x = s[2 * kb + i];
+          float p0 = ex2(fmaf(x[0], k0, o0)), p1 = ex2(fmaf(x[1], k0, o0));
+          float p2 = ex2(fmaf(x[2], k1, o1)), p3 = ex2(fmaf(x[3], k1, o1));
+          if (edge) {  // (a masked score times a K scale of 0 is no zero)
+            p0 = x[0] == -INFINITY ? 0.f : p0;
+            p1 = x[1] == -INFINITY ? 0.f : p1;
+            p2 = x[2] == -INFINITY ? 0.f : p2;
+            p3 = x[3] == -INFINITY ? 0.f : p3;
+          }
+          s0 += p0 + p1;
+          s1 += p2 + p3;
+          const __half2 h0 = __floats2half2_rn(p0, p1), h1 = __floats2half2_rn(p2, p3);
           a[2 * i] = *reinterpret_cast<const uint32_t*>(&h0);
           a[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&h1);
         }
+        l0 = fmaf(s0, w, l0);
+        l1 = fmaf(s1, w, l1);
+        if (w >= 1.f / kKvLeastScale) a[0] = a[1] = a[2] = a[3] = 0u;  // a page without a V scale: its values are zeros
         const uint32_t vrow = uint32_t(16 * kb + ((lane >> 3) & 1) * 8) + ka_tau<D>(lane & 7);
 #pragma unroll
         for (int c2 = 0; c2 < D / 32; ++c2) {
@@ -587,7 +591,7 @@ __global__ void __launch_bounds__(kKaThreads, 1)
       }
       __syncwarp();  // every lane has used the tile: its stage takes the next one
       if (fi < fend) issue();
-      if (++stage == kKaStages) { stage = 0; phase ^= 1u; }
+      if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
     }
 
     // ---- the next row tile's loads go out, then join the warps
@@ -599,40 +603,35 @@ __global__ void __launch_bounds__(kKaThreads, 1)
       l1 += __shfl_xor_sync(0xffffffffu, l1, off);
     }
     if (t == 0) {
-      sh->warp_m[warp][g] = m0;
-      sh->warp_m[warp][g + 8] = m1;
+      sh->warp_z[warp][g] = z0;
+      sh->warp_z[warp][g + 8] = z1;
       sh->warp_l[warp][g] = l0;
       sh->warp_l[warp][g + 8] = l1;
-      sh->warp_v[warp][g] = v0;
-      sh->warp_v[warp][g + 8] = v1;
     }
-    ka_sync();
+    __syncthreads();
     float top0 = -INFINITY, top1 = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kKaWarps; ++w) {
-      top0 = fmaxf(top0, sh->warp_v[w][g]);
-      top1 = fmaxf(top1, sh->warp_v[w][g + 8]);
+    for (int w = 0; w < C::kWarps; ++w) {
+      top0 = fmaxf(top0, sh->warp_z[w][g]);
+      top1 = fmaxf(top1, sh->warp_z[w][g + 8]);
     }
-    const float w0 = v0 == -INFINITY ? 0.f : ex2(v0 - top0), w1 = v1 == -INFINITY ? 0.f : ex2(v1 - top1);
-    // this thread's place in the joined tile: row jr, columns 2 jc, 2 jc + 1 of each 32
-    const int jr = tid >> 4, jc = tid & 15;
-    float jm = -INFINITY, jv = -INFINITY, jl = 0.f;
+    const float w0 = z0 == -INFINITY ? 0.f : ex2(z0 - top0), w1 = z1 == -INFINITY ? 0.f : ex2(z1 - top1);
+    // this thread's place in the joined tile: row jr, columns 2 jc, 2 jc + 1 of each 32 (threads past 256 have none)
+    const int jr = (tid >> 4) & 15, jc = tid & 15;
+    const bool joins = tid < 256;
+    float jz = -INFINITY, jl = 0.f;
 #pragma unroll
-    for (int w = 0; w < kKaWarps; ++w) {
-      jm = fmaxf(jm, sh->warp_m[w][jr]);
-      jv = fmaxf(jv, sh->warp_v[w][jr]);
-    }
+    for (int w = 0; w < C::kWarps; ++w) jz = fmaxf(jz, sh->warp_z[w][jr]);
 #pragma unroll
-    for (int w = 0; w < kKaWarps; ++w)
-      if (sh->warp_m[w][jr] != -INFINITY) jl += sh->warp_l[w][jr] * ex2(sh->warp_m[w][jr] - jm);
+    for (int w = 0; w < C::kWarps; ++w)
+      if (sh->warp_z[w][jr] != -INFINITY) jl += sh->warp_l[w][jr] * ex2(sh->warp_z[w][jr] - jz);
     const bool whole = seg.item0 == 0 && seg.item1 == seg.items;
     const int slot = int(blockIdx.x) * 2 + (i0 >= seg.start ? 0 : 1);
     float* part = p.part + (size_t)slot * C::kSlotFloats;
     const int row = seg.tile * kKaRows + jr;
     const int oj = row / p.group, oh = seg.head * p.group + row - oj * p.group;
     uint16_t* dst = p.out.data + (long long)(seg.s.start + oj) * p.out.token + oh * p.out.head;
-    // (sum of p vs v at 2^-jv) 2^(jv - jm) / (sum of p at 2^-jm); jv is -inf where every vs is 0
-    const float norm = jv > -INFINITY ? __fdiv_rn(ex2(jv - jm), jl) : 0.f;
+    const float norm = jl > 0.f ? __fdiv_rn(1.f, jl) : 0.f;
 #pragma unroll
     for (int c2 = 0; c2 < D / 32; ++c2) {
       float* mine = join + warp * (kKaRows * 32);
@@ -645,34 +644,34 @@ __global__ void __launch_bounds__(kKaThreads, 1)
         *reinterpret_cast<float4*>(mine + (g + 8) * 32 + 16 * hf + 4 * t) =
             make_float4(e[2] * w1, d[2] * w1, e[3] * w1, d[3] * w1);
       }
-      ka_sync();
+      __syncthreads();
       float x = 0.f, y = 0.f;
 #pragma unroll
-      for (int w = 0; w < kKaWarps; ++w) {
+      for (int w = 0; w < C::kWarps; ++w) {
         const float2 v = *reinterpret_cast<const float2*>(join + w * (kKaRows * 32) + jr * 32 + 2 * jc);
         x += v.x;
         y += v.y;
       }
-      if (!whole) {
+      if (!joins) {
+      } else if (!whole) {
         *reinterpret_cast<float2*>(part + jr * D + 32 * c2 + 2 * jc) = make_float2(x, y);
       } else if (row < rows && ok) {
         const __nv_bfloat162 b = __floats2bfloat162_rn(x * norm, y * norm);
         *reinterpret_cast<__nv_bfloat162*>(dst + 32 * c2 + 2 * jc) = b;
       }
-      ka_sync();
+      __syncthreads();
     }
     if (!whole) {
-      if (jc == 0) {
-        part[kKaRows * D + jr] = jm;
+      if (joins && jc == 0) {
+        part[kKaRows * D + jr] = jz;
         part[kKaRows * D + kKaRows + jr] = jl;
-        part[kKaRows * D + 2 * kKaRows + jr] = jv;
       }
       const int c_first = ka_item_cta(seg.start, total, ctas), c_last = ka_item_cta(seg.start + seg.items - 1, total, ctas);
       __threadfence();
-      ka_sync();
+      __syncthreads();
       if (tid == 0) sh->last = atomicAdd(p.counters + c_first, 1u) == unsigned(c_last - c_first);
-      ka_sync();
-      if (sh->last) {
+      __syncthreads();
+      if (sh->last && joins) {
         __threadfence();
         // Slot of CTA c: its first row tile's, but for the CTA in which the tile starts behind another one.  A row's
         // 16 threads take the CTAs' maxima and sums 16 at a time, and leave the CTAs' weights in shared memory; the
@@ -683,15 +682,14 @@ __global__ void __launch_bounds__(kKaThreads, 1)
           return c == 0 ? slot0 : p.part + (size_t)((c_first + c) * 2) * C::kSlotFloats;
         };
         float* weight = join + jr * kKaMaxCtas;
-        float top = -INFINITY, vtop = -INFINITY, sum = 0.f;
+        float top = -INFINITY, sum = 0.f;
         for (int c = jc; c < n_cta; c += 16) {
           const float* m = slot_of(c) + kKaRows * D + jr;
-          const float cm = __ldcg(m), cl = __ldcg(m + kKaRows), cv = __ldcg(m + 2 * kKaRows);
-          const float nt = fmaxf(top, cm);
-          if (nt > -INFINITY) sum = sum * ex2(top - nt) + (cm > -INFINITY ? cl * ex2(cm - nt) : 0.f);
+          const float cz = __ldcg(m), cl = __ldcg(m + kKaRows);
+          const float nt = fmaxf(top, cz);
+          if (nt > -INFINITY) sum = sum * ex2(top - nt) + (cz > -INFINITY ? cl * ex2(cz - nt) : 0.f);
           top = nt;
-          vtop = fmaxf(vtop, cv);
-          weight[c] = cv;
+          weight[c] = cz;
         }
 #pragma unroll
         for (int off = 1; off < 16; off <<= 1) {
@@ -699,9 +697,8 @@ __global__ void __launch_bounds__(kKaThreads, 1)
           const float nt = fmaxf(top, ot);
           if (nt > -INFINITY) sum = sum * ex2(top - nt) + os * ex2(ot - nt);
           top = nt;
-          vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, off));
         }
-        for (int c = jc; c < n_cta; c += 16) weight[c] = weight[c] == -INFINITY ? 0.f : ex2(weight[c] - vtop);
+        for (int c = jc; c < n_cta; c += 16) weight[c] = weight[c] == -INFINITY ? 0.f : ex2(weight[c] - top);
         __syncwarp();
         float acc[D / 16];
 #pragma unroll
@@ -727,7 +724,7 @@ __global__ void __launch_bounds__(kKaThreads, 1)
             }
           }
         }
-        const float n = vtop > -INFINITY ? __fdiv_rn(ex2(vtop - top), sum) : 0.f;
+        const float n = sum > 0.f ? __fdiv_rn(1.f, sum) : 0.f;
         if (row < rows) {
 #pragma unroll
           for (int i = 0; i < D / 64; ++i) {
@@ -740,7 +737,7 @@ __global__ void __launch_bounds__(kKaThreads, 1)
         if (tid == 0) p.counters[c_first] = 0u;  // ready for the next launch on this workspace
       }
     }
-    ka_sync();  // q fragments, warp_m and the join buffer are free again
+    __syncthreads();  // q fragments, warp_m and the join buffer are free again
     seg = nxt;
     have = more;
   }

@@ -40,7 +40,6 @@
 namespace w4a8 {
 
 constexpr int kKpConvWarps = 4;
-constexpr float kKpLeastScale = 0x1p-80f;  // V scales below count as 0
 
 template <int D>
 struct KpCfg {
@@ -492,12 +491,12 @@ __global__ void __launch_bounds__(KpCfg<D>::kThreads, 1) kv_prefill_kernel(const
     for (int i = 0; i < n_tiles && ok; ++i) {
       const bool here = lane < C::KG && ids >= 0;
       const float s_k = here ? sc.x : 0.f, s_v = here ? sc.y : 0.f;
-      const unsigned has = __ballot_sync(0xffffffffu, here), live_v = __ballot_sync(0xffffffffu, s_v >= kKpLeastScale);
+      const unsigned has = __ballot_sync(0xffffffffu, here), live_v = __ballot_sync(0xffffffffu, s_v >= kKvLeastScale);
       if (!k_free) ok = kp_wait_warp(&sh->k_empty[st], phase, sh, p.err);
       if (!ok) break;
       if (tid < C::KG) {
         // a page without a V scale counts in the sum of p like any other: its values are zeros at a stand-in scale
-        const float v = fmaxf(s_v, kKpLeastScale);
+        const float v = fmaxf(s_v, kKvLeastScale);
         sh->ks[i & 7][tid] = s_k;
         sh->lv[i & 7][tid] = __log2f(v);
         sh->iv[i & 7][tid] = __fdiv_rn(1.f, v);
