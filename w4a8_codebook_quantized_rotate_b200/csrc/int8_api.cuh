@@ -333,10 +333,11 @@ w4a8_status w4a8_qk_norm_rope(const w4a8_heads* q, const w4a8_heads* k, int64_t 
   QkParams p{head_rows(q), head_rows(k), head_rows(q_out), head_rows(k_out), q_weight, k_weight, eps,
              rope_params(rope), positions, int(T)};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const dim3 grid{unsigned(T)}, block{kQkThreads};
-  return status_of(D == 64    ? launch_pdl(qk_norm_rope_kernel<64>, grid, block, 0, s, p)
-                   : D == 128 ? launch_pdl(qk_norm_rope_kernel<128>, grid, block, 0, s, p)
-                              : launch_pdl(qk_norm_rope_kernel<256>, grid, block, 0, s, p));
+  const int parts = qk_parts(T, (has_q ? q->heads : 0) + (has_k ? k->heads : 0), D);
+  const dim3 grid{unsigned((T * parts * 32 + kQkThreads - 1) / kQkThreads)}, block{kQkThreads};
+  return status_of(D == 64    ? launch_pdl(qk_norm_rope_kernel<64>, grid, block, 0, s, p, parts)
+                   : D == 128 ? launch_pdl(qk_norm_rope_kernel<128>, grid, block, 0, s, p, parts)
+                              : launch_pdl(qk_norm_rope_kernel<256>, grid, block, 0, s, p, parts));
 }
 
 w4a8_status w4a8_kv_update(const w4a8_kv_cache* cache, const w4a8_kv_batch* batch, const w4a8_heads* k,
@@ -368,7 +369,9 @@ w4a8_status w4a8_kv_update(const w4a8_kv_cache* cache, const w4a8_kv_batch* batc
   p.page_ctas = int(page_ctas);
   p.err = d->err;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const dim3 grid{unsigned(page_ctas + (has_q ? batch->tokens : 0))}, block{kKvThreads};
+  p.q_parts = has_q ? qk_parts(batch->tokens, q->heads, D) : 1;
+  const int64_t q_ctas = has_q ? (batch->tokens * p.q_parts * 32 + kKvThreads - 1) / kKvThreads : 0;
+  const dim3 grid{unsigned(page_ctas + q_ctas)}, block{kKvThreads};
   const size_t smem = size_t(cache->page) * D * 4;
   return status_of(D == 64    ? launch_pdl(kv_update_kernel<64>, grid, block, smem, s, p)
                    : D == 128 ? launch_pdl(kv_update_kernel<128>, grid, block, smem, s, p)
@@ -379,15 +382,15 @@ w4a8_status w4a8_kv_dequant(const w4a8_kv_cache* cache, const int32_t* ids, int6
                             void* stream) {
   if (!ids || !k_out || !v_out) return W4A8_ERR_NULL;
   if (w4a8_status st = cache_ok(cache); st != W4A8_OK) return st;
-  if (n < 1 || n > (int64_t(1) << 31)) return W4A8_ERR_SHAPE;
-  const int64_t chunks = n * (int64_t(cache->kv_heads) * cache->page * (cache->head_dim / 16));
-  if (chunks >= (int64_t(1) << 37)) return W4A8_ERR_SHAPE;
+  if (n < 1 || n >= (int64_t(1) << 31)) return W4A8_ERR_SHAPE;
+  const int slab = cache->page * cache->head_dim, parts = (slab + 16 * kDqThreads - 1) / (16 * kDqThreads);
+  const int64_t ctas = 2 * n * cache->kv_heads * parts;
+  if (ctas >= (int64_t(1) << 31)) return W4A8_ERR_SHAPE;
   if (!aligned4(ids) || !aligned16(k_out) || !aligned16(v_out)) return W4A8_ERR_ALIGN;
   DeviceState* d = nullptr;
   if (w4a8_status st = int8_state(&d); st != W4A8_OK) return st;
-  return status_of(launch_pdl(kv_dequant_kernel, dim3(unsigned((2 * chunks + 255) / 256)), dim3(256), 0,
-                              static_cast<cudaStream_t>(stream), cache_params(cache), ids, (long long)chunks, k_out, v_out,
-                              d->err));
+  return status_of(launch_pdl(kv_dequant_kernel, dim3(unsigned(ctas)), dim3(kDqThreads), 0,
+                              static_cast<cudaStream_t>(stream), cache_params(cache), ids, int(n), k_out, v_out, d->err));
 }
 
 size_t w4a8_kv_attention_workspace_bytes(int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t head_dim) {

@@ -96,7 +96,8 @@ struct KvUpdateParams {
   HeadRows v;
   KvCacheParams cache;
   KvBatchParams batch;
-  int page_ctas;        // units * kv_heads * 2; the CTAs after them take a token of q each
+  int page_ctas;        // units * kv_heads * 2; the CTAs after them take q
+  int q_parts;          // warps that share a token's heads
   unsigned* err;
 };
 
@@ -138,26 +139,23 @@ __device__ __forceinline__ uint32_t recode4(uint32_t w, float ratio) {
 template <int D>
 __global__ void __launch_bounds__(kKvThreads) kv_update_kernel(const KvUpdateParams p) {
   extern __shared__ __align__(16) float kv_rows[];  // [page][D]: the page's new rows, fp32
-  __shared__ float2 cs[kQkMaxPairs];
-  __shared__ float warp_max[kKvThreads / 32];
   constexpr int LPH = D / 8, RPP = kKvThreads / LPH;  // rows per pass
+  constexpr int kAhead = 4;                           // passes in flight
+  __shared__ float warp_max[kKvThreads / 32];
   pdl_wait();
   pdl_launch_dependents();
   const int g = threadIdx.x / LPH, sub = threadIdx.x & (LPH - 1);
   const int ps = p.cache.page_shift;
   if (int(blockIdx.x) >= p.page_ctas) {
-    // ------------------------------------------------ a token of q
-    const int token = int(blockIdx.x) - p.page_ctas;
+    // ------------------------------------------------ q: a warp per share of a token's heads
+    const long long unit = ((long long)(int(blockIdx.x) - p.page_ctas) * kKvThreads + threadIdx.x) >> 5;
+    const int token = int(unit / p.q_parts), part = int(unit - (long long)token * p.q_parts);
+    if (token >= p.batch.tokens) return;
     const int at = kv_find_position(p.batch, ps, token);
     if (at < 0) return;
-    const QkParams& qk = p.qk;
-    if (qk.rope.inv_freq) {
-      const int pos = qk.positions ? qk.positions[token] : at;
-      for (int i = threadIdx.x; i < qk.rope.rot_dim / 2; i += kKvThreads) cs[i] = rope_cs(qk.rope, pos, i);
-      __syncthreads();
-    }
-    for (int h0 = 0; h0 < qk.q.heads; h0 += RPP)
-      qk_head<D>(qk.q, qk.q_out, qk.q_weight, qk.eps, qk.rope, cs, token, h0 + g, h0 + g < qk.q.heads);
+    QkParams qk = p.qk;
+    qk.k.data = nullptr;
+    qk_token<D>(qk, token, qk.positions ? __ldg(qk.positions + token) : at, part, p.q_parts);
     return;
   }
   // -------------------------------------------------- a page of a head, K or V
@@ -181,29 +179,43 @@ __global__ void __launch_bounds__(kKvThreads) kv_update_kernel(const KvUpdatePar
   float w[8];
   const float* weight = kind ? nullptr : p.qk.k_weight;
   head_weight<LPH>(weight, sub, w);
+  float* scale = p.cache.scales[kind] + (long long)id * p.cache.kv_heads + head;
+  const float old = first == 0 ? 0.f : __ldcg(scale);
+  const bool turn = kind == 0 && p.qk.rope.inv_freq;
   float amax = 0.f;
-  for (int r0 = 0; r0 < n; r0 += RPP) {  // every warp takes every pass: the norm and the rotation shuffle
-    const int r = r0 + g;
-    const bool live = r < n;
-    const int token = s.start + j0 + r;
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (live) bf16x8_to_float(__ldcg(reinterpret_cast<const uint4*>(src.data + token * src.token + head * src.head) + sub), v);
-    if (weight) head_norm<LPH>(v, w, p.qk.eps);
-    if (kind == 0 && p.qk.rope.inv_freq) {
-      const int pos = !live ? 0 : p.qk.positions ? p.qk.positions[token] : s.kv_len - s.q_len + j0 + r;
-      head_rope<LPH>(v, p.qk.rope, sub, [&](int i) { return rope_cs(p.qk.rope, pos, i); });
-    }
-    if (live) {
+  for (int r0 = 0; r0 < n; r0 += kAhead * RPP) {  // rows go out kAhead passes at a time
+    uint4 raw[kAhead];
+    int pos[kAhead];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
-      float4* dst = reinterpret_cast<float4*>(kv_rows + r * D + 8 * sub);
-      dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-      dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+    for (int a = 0; a < kAhead; ++a) {
+      const int r = r0 + a * RPP + g;
+      const long long token = s.start + j0 + r;
+      raw[a] = r < n ? __ldcg(reinterpret_cast<const uint4*>(src.data + token * src.token + head * src.head) + sub)
+                     : make_uint4(0u, 0u, 0u, 0u);
+      pos[a] = turn && p.qk.positions && r < n ? __ldg(p.qk.positions + token) : s.kv_len - s.q_len + j0 + r;
+    }
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      if (r0 + a * RPP >= n) break;  // (the same for all lanes: the norm and the rotation shuffle)
+      const int r = r0 + a * RPP + g;
+      float v[8];
+      bf16x8_to_float(raw[a], v);
+      if (weight) head_norm<LPH>(v, w, p.qk.eps);
+      if (turn) {
+        float2 cs[8];
+        lane_angles(p.qk.rope, sub, pos[a], cs);
+        head_rope(v, p.qk.rope, sub, cs);
+      }
+      if (r < n) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+        float4* dst = reinterpret_cast<float4*>(kv_rows + r * D + 8 * sub);
+        dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+        dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+      }
     }
   }
   const float need = quant_scale(block_max_256(amax, warp_max));
-  float* scale = p.cache.scales[kind] + (long long)id * p.cache.kv_heads + head;
-  const float old = first == 0 ? 0.f : *scale;
   const float now = fmaxf(old, need);
   int8_t* codes = p.cache.codes[kind] + (((long long)id * p.cache.kv_heads + head) << ps) * D;
   if (first > 0 && now > old) {
@@ -229,30 +241,33 @@ __global__ void __launch_bounds__(kKvThreads) kv_update_kernel(const KvUpdatePar
 }
 
 // Pages back to bf16: values code * scale of both kinds, [n][kv_heads][page][D].
-__global__ void __launch_bounds__(256) kv_dequant_kernel(KvCacheParams c, const int* __restrict__ ids, long long chunks,
-                                                         uint16_t* __restrict__ k_out, uint16_t* __restrict__ v_out,
-                                                         unsigned* err) {
+// A CTA takes 4096 codes of one (page, head) of one kind (or the whole of a
+// smaller one), 16 to a thread.
+constexpr int kDqThreads = 256;
+__global__ void __launch_bounds__(kDqThreads) kv_dequant_kernel(KvCacheParams c, const int* __restrict__ ids, int n,
+                                                                uint16_t* __restrict__ k_out,
+                                                                uint16_t* __restrict__ v_out, unsigned* err) {
   pdl_wait();
   pdl_launch_dependents();
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;  // 16 codes of one kind
-  if (i >= 2 * chunks) return;
-  const int kind = i >= chunks;
-  const long long at = (kind ? i - chunks : i) * 16;
-  const long long slab = at / ((long long)c.D << c.page_shift);  // (n, head)
-  const long long inside = at - slab * ((long long)c.D << c.page_shift);
-  const long long nth = slab / c.kv_heads;
-  const int head = int(slab - nth * c.kv_heads);
+  const int slab = c.D << c.page_shift;  // codes of a (page, head), a multiple of 1024
+  const int parts = (slab + 16 * kDqThreads - 1) / (16 * kDqThreads);
+  const long long unit = blockIdx.x / parts;  // (kind, nth, head)
+  const int inside = (int(blockIdx.x) - int(unit) * parts) * 16 * kDqThreads + threadIdx.x * 16;
+  if (inside >= slab) return;
+  const long long row = unit / c.kv_heads;
+  const int head = int(unit - row * c.kv_heads), kind = row >= n;
+  const long long nth = kind ? row - n : row;
   const int id = __ldg(ids + nth);
   uint4 w = make_uint4(0u, 0u, 0u, 0u);
   float s = 0.f;
   if (id >= 0 && id < c.pages) {
     const long long at_head = (long long)id * c.kv_heads + head;
-    w = *reinterpret_cast<const uint4*>(c.codes[kind] + (at_head << c.page_shift) * c.D + inside);
-    s = c.scales[kind][at_head];
+    w = __ldcg(reinterpret_cast<const uint4*>(c.codes[kind] + at_head * slab + inside));
+    s = __ldcg(c.scales[kind] + at_head);
   } else {
     record_error(err, kErrInput);
   }
-  uint16_t* out = (kind ? v_out : k_out) + at;
+  uint16_t* out = (kind ? v_out : k_out) + (nth * c.kv_heads + head) * slab + inside;
   const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int h = 0; h < 2; ++h) {

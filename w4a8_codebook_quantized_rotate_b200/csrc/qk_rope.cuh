@@ -9,11 +9,17 @@
 // Sums and products are fp32 and the result is rounded once.  The angle is
 // formed in fp64 as a number of turns, position * (inv_freq / 2 pi), and its
 // whole turns are dropped there: in fp32 the angle of a position of 10^6
-// would be off by 0.03 rad.  What is left (|t| <= 1/2 turn) goes to fp32.
+// would be off by 0.03 rad.  What is left (|t| <= 1/2 turn) goes to fp32 and
+// to the hardware's sine and cosine (2^-21 off at most, against the 2^-9 of
+// the bf16 result or the 2^-8 of an int8 code).
 //
 // A head is held by D / 8 neighbouring lanes, 8 values (16 bytes) each, so
 // a row's loads are whole 16-byte words, the norm is a few shuffles, and as
-// rot_dim is a multiple of 16 a half-layout partner is a whole lane away.
+// rot_dim is a multiple of 16 a half-layout partner is a whole lane away.  A
+// lane's angles and weights are the same for every head of a token and stay
+// in registers; a warp walks a token's heads with nothing shared and no
+// barrier.  The kernel's instructions (about 75 a lane and head) and its
+// bytes then take about the same time.
 #pragma once
 
 #include "common.cuh"
@@ -39,10 +45,8 @@ constexpr double kInvTwoPi = 0.15915494309189533577;
 // cos and sin (times the factor) of pair i at a position.
 __device__ __forceinline__ float2 rope_cs(const RopeParams& r, int pos, int i) {
   const double turns = double(pos) * (__ldg(r.inv_freq + i) * kInvTwoPi);
-  const float t = float(turns - rint(turns));
-  float s, c;
-  sincospif(2.0f * t, &s, &c);
-  return make_float2(c * r.factor, s * r.factor);
+  const float t = float(turns - rint(turns)) * 6.28318530717958647692f;
+  return make_float2(__cosf(t) * r.factor, __sinf(t) * r.factor);
 }
 
 __device__ __forceinline__ void bf16x8_to_float(const uint4 raw, float (&v)[8]) {
@@ -89,34 +93,42 @@ __device__ __forceinline__ void head_norm(float (&v)[8], const float (&w)[8], fl
   for (int i = 0; i < 8; ++i) v[i] = v[i] * r * w[i];
 }
 
-// The lane's cos/sin values: interleaved, pair 4 sub + i / 2 for value i;
-// half layout, pair (8 sub + i) % (rot_dim / 2).  `cs(pair)` gives them.
-template <int LPH, typename Cs>
-__device__ __forceinline__ void head_rope(float (&v)[8], const RopeParams& r, int sub, Cs cs) {
+// The lane's cosines and sines at a position: interleaved, pair 4 sub + i / 2
+// for value i (the first four); half layout, pair (8 sub + i) % (rot_dim / 2).
+__device__ __forceinline__ void lane_angles(const RopeParams& r, int sub, int pos, float2 (&cs)[8]) {
+  const int span = r.rot_dim >> 3, half = span >> 1;
+  if (sub < span) {
+    if (r.interleaved) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) cs[i] = rope_cs(r, pos, 4 * sub + i);
+    } else {
+      const int p0 = 8 * (sub < half ? sub : sub - half);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) cs[i] = rope_cs(r, pos, p0 + i);
+    }
+  }
+}
+
+// Rotation of a head's values; the whole warp takes part.
+__device__ __forceinline__ void head_rope(float (&v)[8], const RopeParams& r, int sub, const float2 (&cs)[8]) {
   const int span = r.rot_dim >> 3;  // lanes that hold rotated values
   if (r.interleaved) {
     if (sub < span) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 t = cs(4 * sub + i);
         const float a = v[2 * i], b = v[2 * i + 1];
-        v[2 * i] = a * t.x - b * t.y;
-        v[2 * i + 1] = b * t.x + a * t.y;
+        v[2 * i] = a * cs[i].x - b * cs[i].y;
+        v[2 * i + 1] = b * cs[i].x + a * cs[i].y;
       }
     }
   } else {
-    const int half = span >> 1;
+    const int half = span >> 1, lane = threadIdx.x & 31;
     const bool low = sub < half;
-    const int lane = threadIdx.x & 31;
     const int src = sub < span ? (low ? lane + half : lane - half) : lane;
-    const int p0 = low ? 8 * sub : 8 * (sub - half);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float o = __shfl_sync(0xffffffffu, v[i], src);
-      if (sub < span) {
-        const float2 t = cs(p0 + i);
-        v[i] = low ? v[i] * t.x - o * t.y : v[i] * t.x + o * t.y;
-      }
+      if (sub < span) v[i] = v[i] * cs[i].x + (low ? -o : o) * cs[i].y;
     }
   }
 }
@@ -133,46 +145,61 @@ struct QkParams {
 };
 
 constexpr int kQkThreads = 256;
-constexpr int kQkMaxPairs = 128;  // rot_dim / 2 at most (heads of 256)
 
-// One head row of the warp's current group: load, norm, rotate, store.
+// Heads [h0, h1) of one token's rows, by a warp.
 template <int D>
-__device__ __forceinline__ void qk_head(const HeadRows& in, const HeadRows& out, const float* weight, float eps,
-                                        const RopeParams& rope, const float2* cs, int token, int head, bool live) {
-  constexpr int LPH = D / 8;
-  const int sub = threadIdx.x & (LPH - 1);
-  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (live)
-    bf16x8_to_float(__ldcg(reinterpret_cast<const uint4*>(in.data + token * in.token + head * in.head) + sub), v);
-  if (weight) {
-    float w[8];
-    head_weight<LPH>(weight, sub, w);
-    head_norm<LPH>(v, w, eps);
+__device__ __forceinline__ void qk_rows(const HeadRows& in, const HeadRows& out, const float* weight, float eps,
+                                        const RopeParams& rope, const float2 (&cs)[8], int token, int h0, int h1) {
+  constexpr int LPH = D / 8, HPW = 32 / LPH;  // heads of a warp at a time
+  const int lane = threadIdx.x & 31, sub = lane & (LPH - 1), g = lane / LPH;
+  float w[8];
+  head_weight<LPH>(weight, sub, w);
+  const uint16_t* src = in.data + token * in.token + 8 * sub;
+  uint16_t* dst = out.data + token * out.token + 8 * sub;
+  auto load = [&](int h) {
+    return h + g < h1 ? __ldcg(reinterpret_cast<const uint4*>(src + (h + g) * in.head)) : make_uint4(0u, 0u, 0u, 0u);
+  };
+  uint4 raw = load(h0), next = load(h0 + HPW);
+  for (int h = h0; h < h1; h += HPW) {
+    float v[8];
+    bf16x8_to_float(raw, v);
+    raw = next;
+    next = load(h + 2 * HPW);
+    if (weight) head_norm<LPH>(v, w, eps);
+    if (rope.inv_freq) head_rope(v, rope, sub, cs);
+    if (h + g < h1) *reinterpret_cast<uint4*>(dst + (h + g) * out.head) = float_to_bf16x8(v);
   }
-  if (rope.inv_freq) head_rope<LPH>(v, rope, sub, [&](int i) { return cs[i]; });
-  if (live)
-    reinterpret_cast<uint4*>(out.data + token * out.token + head * out.head)[sub] = float_to_bf16x8(v);
 }
 
-// A CTA per token: its angles once, then every head of q and k.
+// How many warps share a token's heads: enough to fill the SMs where tokens
+// are few, one where there are many (its angles are then formed once).
+__host__ __device__ inline int qk_parts(int64_t tokens, int heads, int D) {
+  const int64_t most = (heads + 256 / D - 1) / (256 / D), fill = (148 * 16 + tokens - 1) / tokens;
+  return int(fill < most ? fill : most);
+}
+
+// Part `part` of `parts` of a token's heads, q's then k's, in steps of a warp's heads.
 template <int D>
-__global__ void __launch_bounds__(kQkThreads) qk_norm_rope_kernel(const QkParams p) {
-  __shared__ float2 cs[kQkMaxPairs];
-  constexpr int LPH = D / 8, HPC = kQkThreads / LPH;  // heads per pass
+__device__ __forceinline__ void qk_token(const QkParams& p, int token, int pos, int part, int parts) {
+  constexpr int HPW = 256 / D;
+  float2 cs[8];
+  if (p.rope.inv_freq) lane_angles(p.rope, threadIdx.x & (D / 8 - 1), pos, cs);
+  const int sq = p.q.data ? (p.q.heads + HPW - 1) / HPW : 0, sk = p.k.data ? (p.k.heads + HPW - 1) / HPW : 0;
+  const int s0 = (sq + sk) * part / parts, s1 = (sq + sk) * (part + 1) / parts;
+  if (s0 < sq)
+    qk_rows<D>(p.q, p.q_out, p.q_weight, p.eps, p.rope, cs, token, s0 * HPW, min(p.q.heads, min(s1, sq) * HPW));
+  if (s1 > sq)
+    qk_rows<D>(p.k, p.k_out, p.k_weight, p.eps, p.rope, cs, token, max(s0 - sq, 0) * HPW, min(p.k.heads, (s1 - sq) * HPW));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kQkThreads) qk_norm_rope_kernel(const QkParams p, int parts) {
   pdl_wait();
   pdl_launch_dependents();
-  const int token = blockIdx.x;
-  if (p.rope.inv_freq) {
-    const int pos = p.positions[token];
-    for (int i = threadIdx.x; i < p.rope.rot_dim / 2; i += kQkThreads) cs[i] = rope_cs(p.rope, pos, i);
-    __syncthreads();
-  }
-  const int hq = p.q.data ? p.q.heads : 0, hk = p.k.data ? p.k.heads : 0;
-  const int g = threadIdx.x / LPH;
-  for (int h0 = 0; h0 < hq; h0 += HPC)
-    qk_head<D>(p.q, p.q_out, p.q_weight, p.eps, p.rope, cs, token, h0 + g, h0 + g < hq);
-  for (int h0 = 0; h0 < hk; h0 += HPC)
-    qk_head<D>(p.k, p.k_out, p.k_weight, p.eps, p.rope, cs, token, h0 + g, h0 + g < hk);
+  const long long unit = ((long long)blockIdx.x * kQkThreads + threadIdx.x) >> 5;
+  const int token = int(unit / parts), part = int(unit - (long long)token * parts);
+  if (token >= p.tokens) return;
+  qk_token<D>(p, token, p.rope.inv_freq ? __ldg(p.positions + token) : 0, part, parts);
 }
 
 }  // namespace w4a8
