@@ -245,9 +245,6 @@ bool int8_allow_smem() {
          allow_smem(int8_gemm_kernel<128, 2>, Q8Cfg<128, 2>::kSmem) == cudaSuccess &&
          allow_smem(int8_gemm_kernel<128, 1>, Q8Cfg<128, 1>::kSmem) == cudaSuccess &&
          allow_smem(int8_gemm_kernel<256, 1>, Q8Cfg<256, 1>::kSmem) == cudaSuccess &&
-         allow_smem(kv_update_kernel<64>, 128 * 64 * 4) == cudaSuccess &&
-         allow_smem(kv_update_kernel<128>, 128 * 128 * 4) == cudaSuccess &&
-         allow_smem(kv_update_kernel<256>, 128 * 256 * 4) == cudaSuccess &&
          allow_smem(kv_attention_kernel<64>, KaCfg<64>::kSmem) == cudaSuccess &&
          allow_smem(kv_attention_kernel<128>, KaCfg<128>::kSmem) == cudaSuccess &&
          allow_smem(kv_attention_kernel<256>, KaCfg<256>::kSmem) == cudaSuccess &&
@@ -370,12 +367,19 @@ w4a8_status w4a8_kv_update(const w4a8_kv_cache* cache, const w4a8_kv_batch* batc
   p.err = d->err;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   p.q_parts = has_q ? qk_parts(batch->tokens, q->heads, D) : 1;
-  const int64_t q_ctas = has_q ? (batch->tokens * p.q_parts * 32 + kKvThreads - 1) / kKvThreads : 0;
-  const dim3 grid{unsigned(page_ctas + q_ctas)}, block{kKvThreads};
-  const size_t smem = size_t(cache->page) * D * 4;
-  return status_of(D == 64    ? launch_pdl(kv_update_kernel<64>, grid, block, smem, s, p)
-                   : D == 128 ? launch_pdl(kv_update_kernel<128>, grid, block, smem, s, p)
-                              : launch_pdl(kv_update_kernel<256>, grid, block, smem, s, p));
+  // Few new tokens a sequence: small CTAs.
+  const bool small = batch->tokens <= 4 * batch->batch;
+  const int threads = small ? 64 : 256;
+  const int64_t q_ctas = has_q ? (batch->tokens * p.q_parts * 32 + threads - 1) / threads : 0;
+  const dim3 grid{unsigned(page_ctas + q_ctas)}, block{unsigned(threads)};
+  switch (D + small) {
+    case 64: return status_of(launch_pdl(kv_update_kernel<64, 256>, grid, block, 0, s, p));
+    case 65: return status_of(launch_pdl(kv_update_kernel<64, 64>, grid, block, 0, s, p));
+    case 128: return status_of(launch_pdl(kv_update_kernel<128, 256>, grid, block, 0, s, p));
+    case 129: return status_of(launch_pdl(kv_update_kernel<128, 64>, grid, block, 0, s, p));
+    case 256: return status_of(launch_pdl(kv_update_kernel<256, 256>, grid, block, 0, s, p));
+    default: return status_of(launch_pdl(kv_update_kernel<256, 64>, grid, block, 0, s, p));
+  }
 }
 
 w4a8_status w4a8_kv_dequant(const w4a8_kv_cache* cache, const int32_t* ids, int64_t n, uint16_t* k_out, uint16_t* v_out,

@@ -101,16 +101,15 @@ struct KvUpdateParams {
   unsigned* err;
 };
 
-constexpr int kKvThreads = 256;
-
-__device__ __forceinline__ float block_max_256(float v, float* warp_max) {
+template <int THREADS>
+__device__ __forceinline__ float block_max(float v, float* warp_max) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
   if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = v;
   __syncthreads();
   v = warp_max[0];
 #pragma unroll
-  for (int i = 1; i < kKvThreads / 32; ++i) v = fmaxf(v, warp_max[i]);
+  for (int i = 1; i < THREADS / 32; ++i) v = fmaxf(v, warp_max[i]);
   return v;
 }
 
@@ -136,19 +135,20 @@ __device__ __forceinline__ uint32_t recode4(uint32_t w, float ratio) {
   return out;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kKvThreads) kv_update_kernel(const KvUpdateParams p) {
-  extern __shared__ __align__(16) float kv_rows[];  // [page][D]: the page's new rows, fp32
-  constexpr int LPH = D / 8, RPP = kKvThreads / LPH;  // rows per pass
-  constexpr int kAhead = 4;                           // passes in flight
-  __shared__ float warp_max[kKvThreads / 32];
+// THREADS: 256, or 64 where a page gets a token or two (a decode step: the
+// CTAs of 64 sequences x 8 heads are then all resident at once).
+template <int D, int THREADS>
+__global__ void __launch_bounds__(THREADS, 768 / THREADS) kv_update_kernel(const KvUpdateParams p) {
+  constexpr int LPH = D / 8, RPP = THREADS / LPH;  // rows per pass
+  constexpr int kAhead = 4;                        // passes of a chunk
+  __shared__ float warp_max[THREADS / 32];
   pdl_wait();
   pdl_launch_dependents();
   const int g = threadIdx.x / LPH, sub = threadIdx.x & (LPH - 1);
   const int ps = p.cache.page_shift;
   if (int(blockIdx.x) >= p.page_ctas) {
     // ------------------------------------------------ q: a warp per share of a token's heads
-    const long long unit = ((long long)(int(blockIdx.x) - p.page_ctas) * kKvThreads + threadIdx.x) >> 5;
+    const long long unit = ((long long)(int(blockIdx.x) - p.page_ctas) * THREADS + threadIdx.x) >> 5;
     const int token = int(unit / p.q_parts), part = int(unit - (long long)token * p.q_parts);
     if (token >= p.batch.tokens) return;
     const int at = kv_find_position(p.batch, ps, token);
@@ -176,14 +176,15 @@ __global__ void __launch_bounds__(kKvThreads) kv_update_kernel(const KvUpdatePar
     return;
   }
   const HeadRows& src = kind ? p.v : p.qk.k;
-  float w[8];
   const float* weight = kind ? nullptr : p.qk.k_weight;
-  head_weight<LPH>(weight, sub, w);
+  const Head8 w = head_weight(weight, sub);
   float* scale = p.cache.scales[kind] + (long long)id * p.cache.kv_heads + head;
   const float old = first == 0 ? 0.f : __ldcg(scale);
   const bool turn = kind == 0 && p.qk.rope.inv_freq;
-  float amax = 0.f;
-  for (int r0 = 0; r0 < n; r0 += kAhead * RPP) {  // rows go out kAhead passes at a time
+  // A chunk of rows, kAhead passes: their loads go out together, then norm and rotation.  The values stay in
+  // registers; where the rows are more than one chunk, the chunks are made again once the scale is known.
+  Head8 v[kAhead];
+  auto chunk = [&](int r0) {
     uint4 raw[kAhead];
     int pos[kAhead];
 #pragma unroll
@@ -197,30 +198,30 @@ __global__ void __launch_bounds__(kKvThreads) kv_update_kernel(const KvUpdatePar
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
       if (r0 + a * RPP >= n) break;  // (the same for all lanes: the norm and the rotation shuffle)
-      const int r = r0 + a * RPP + g;
-      float v[8];
-      bf16x8_to_float(raw[a], v);
-      if (weight) head_norm<LPH>(v, w, p.qk.eps);
-      if (turn) {
-        float2 cs[8];
-        lane_angles(p.qk.rope, sub, pos[a], cs);
-        head_rope(v, p.qk.rope, sub, cs);
-      }
-      if (r < n) {
+      v[a] = head_unpack(raw[a]);
+      if (weight) head_norm<LPH>(v[a], w, p.qk.eps);
+      if (turn) head_rope(v[a], p.qk.rope.interleaved, head_turn(p.qk.rope, sub, pos[a]));
+    }
+  };
+  float amax = 0.f;
+  for (int r0 = 0; r0 < n; r0 += kAhead * RPP) {
+    chunk(r0);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
-        float4* dst = reinterpret_cast<float4*>(kv_rows + r * D + 8 * sub);
-        dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-        dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+    for (int a = 0; a < kAhead; ++a) {
+      if (r0 + a * RPP + g < n) {
+        float x[8];
+        head_values(v[a], x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
       }
     }
   }
-  const float need = quant_scale(block_max_256(amax, warp_max));
+  const float need = quant_scale(block_max<THREADS>(amax, warp_max));
   const float now = fmaxf(old, need);
   int8_t* codes = p.cache.codes[kind] + (((long long)id * p.cache.kv_heads + head) << ps) * D;
   if (first > 0 && now > old) {
     const float ratio = __fdiv_rn(old, now);
-    for (int i = threadIdx.x * 16; i < first * D; i += kKvThreads * 16) {
+    for (int i = threadIdx.x * 16; i < first * D; i += THREADS * 16) {
       uint4 c = *reinterpret_cast<uint4*>(codes + i);
       c.x = recode4(c.x, ratio);
       c.y = recode4(c.y, ratio);
@@ -230,14 +231,19 @@ __global__ void __launch_bounds__(kKvThreads) kv_update_kernel(const KvUpdatePar
     }
   }
   const QuantScale qs = quant_prepare(now);
-  for (int r = g; r < n; r += RPP) {  // the rows this thread staged
-    const float4 a = *reinterpret_cast<const float4*>(kv_rows + r * D + 8 * sub);
-    const float4 b = *reinterpret_cast<const float4*>(kv_rows + r * D + 8 * sub + 4);
-    const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    *reinterpret_cast<uint2*>(codes + (first + r) * D + 8 * sub) = quant8(v, qs);
+  for (int r0 = 0; r0 < n; r0 += kAhead * RPP) {
+    if (n > kAhead * RPP) chunk(r0);
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      const int r = r0 + a * RPP + g;
+      if (r < n) {
+        float x[8];
+        head_values(v[a], x);
+        *reinterpret_cast<uint2*>(codes + (first + r) * D + 8 * sub) = quant8(x, qs);
+      }
+    }
   }
-  __syncthreads();  // every thread has read the old scale
-  if (threadIdx.x == 0) *scale = now;
+  if (threadIdx.x == 0) *scale = now;  // (every thread read the old one before block_max's barrier)
 }
 
 // Pages back to bf16: values code * scale of both kinds, [n][kv_heads][page][D].

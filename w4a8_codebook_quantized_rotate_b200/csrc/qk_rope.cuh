@@ -67,69 +67,128 @@ __device__ __forceinline__ uint4 float_to_bf16x8(const float (&v)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The lane's 8 weights (ones without a weight).
-template <int LPH>
-__device__ __forceinline__ void head_weight(const float* weight, int sub, float (&w)[8]) {
+// Two fp32 values as one operand of the packed fp32 instructions (each half
+// rounded like the scalar one; half the issue slots, which bound these kernels).
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t d) {
+  float2 v;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(d));
+  return v;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+struct Head8 {  // a lane's 8 values of a head, neighbouring values paired
+  uint64_t p[4];
+};
+__device__ __forceinline__ Head8 head_unpack(const uint4 raw) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  Head8 h;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = 1.f;
+  for (int i = 0; i < 4; ++i) h.p[i] = pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+  return h;
+}
+__device__ __forceinline__ uint4 head_pack(const Head8& h) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = unpack2(h.p[i]);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
+    w[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void head_values(const Head8& h, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = unpack2(h.p[i]);
+    v[2 * i] = x.x;
+    v[2 * i + 1] = x.y;
+  }
+}
+
+// The lane's 8 weights (ones without a weight).
+__device__ __forceinline__ Head8 head_weight(const float* weight, int sub) {
+  Head8 w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w.p[i] = pack2(1.f, 1.f);
   if (weight) {
     const float4 a = __ldg(reinterpret_cast<const float4*>(weight) + 2 * sub);
     const float4 b = __ldg(reinterpret_cast<const float4*>(weight) + 2 * sub + 1);
-    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+    w.p[0] = pack2(a.x, a.y), w.p[1] = pack2(a.z, a.w), w.p[2] = pack2(b.x, b.y), w.p[3] = pack2(b.z, b.w);
   }
+  return w;
 }
 
 // Norm of a head held by LPH neighbouring lanes (8 values each); the whole
 // warp takes part.
 template <int LPH>
-__device__ __forceinline__ void head_norm(float (&v)[8], const float (&w)[8], float eps) {
-  float ss = 0.f;
+__device__ __forceinline__ void head_norm(Head8& h, const Head8& w, float eps) {
+  uint64_t sq = mul2(h.p[0], h.p[0]);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
+  for (int i = 1; i < 4; ++i) sq = fma2(h.p[i], h.p[i], sq);
+  const float2 s2 = unpack2(sq);
+  float ss = s2.x + s2.y;
 #pragma unroll
   for (int off = LPH / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
   const float r = rsqrtf(ss * (1.0f / float(8 * LPH)) + eps);
+  const uint64_t r2 = pack2(r, r);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = v[i] * r * w[i];
+  for (int i = 0; i < 4; ++i) h.p[i] = mul2(mul2(h.p[i], r2), w.p[i]);
 }
 
-// The lane's cosines and sines at a position: interleaved, pair 4 sub + i / 2
-// for value i (the first four); half layout, pair (8 sub + i) % (rot_dim / 2).
-__device__ __forceinline__ void lane_angles(const RopeParams& r, int sub, int pos, float2 (&cs)[8]) {
-  const int span = r.rot_dim >> 3, half = span >> 1;
-  if (sub < span) {
-    if (r.interleaved) {
+// The lane's cosines and (signed) sines at a position, so that a value turns
+// to v * c + (its partner) * s: half layout, pair (8 sub + i) % (rot_dim / 2)
+// for value i, the sine negative in the first half; interleaved, pair 4 sub +
+// i / 2, negative for the even value.  Lanes past the rotated part hold 1, 0.
+struct Turn8 {
+  uint64_t c[4], s[4];
+  int src;  // half layout: the lane that holds the partners
+};
+__device__ __forceinline__ Turn8 head_turn(const RopeParams& r, int sub, int pos) {
+  const int span = r.rot_dim >> 3, half = span >> 1, lane = threadIdx.x & 31;
+  const bool low = sub < half, in = sub < span;
+  Turn8 t;
+  t.src = in && !r.interleaved ? (low ? lane + half : lane - half) : lane;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) cs[i] = rope_cs(r, pos, 4 * sub + i);
-    } else {
-      const int p0 = 8 * (sub < half ? sub : sub - half);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) cs[i] = rope_cs(r, pos, p0 + i);
+  for (int i = 0; i < 4; ++i) {
+    float2 a = make_float2(1.f, 0.f), b = a;
+    if (in && r.interleaved) {
+      a = rope_cs(r, pos, 4 * sub + i);
+      b = a;
+      a.y = -a.y;
+    } else if (in) {
+      const int p0 = 8 * (low ? sub : sub - half) + 2 * i;
+      a = rope_cs(r, pos, p0);
+      b = rope_cs(r, pos, p0 + 1);
+      if (low) a.y = -a.y, b.y = -b.y;
     }
+    t.c[i] = pack2(a.x, b.x);
+    t.s[i] = pack2(a.y, b.y);
   }
+  return t;
 }
 
 // Rotation of a head's values; the whole warp takes part.
-__device__ __forceinline__ void head_rope(float (&v)[8], const RopeParams& r, int sub, const float2 (&cs)[8]) {
-  const int span = r.rot_dim >> 3;  // lanes that hold rotated values
-  if (r.interleaved) {
-    if (sub < span) {
+__device__ __forceinline__ void head_rope(Head8& h, int interleaved, const Turn8& t) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float a = v[2 * i], b = v[2 * i + 1];
-        v[2 * i] = a * cs[i].x - b * cs[i].y;
-        v[2 * i + 1] = b * cs[i].x + a * cs[i].y;
-      }
-    }
-  } else {
-    const int half = span >> 1, lane = threadIdx.x & 31;
-    const bool low = sub < half;
-    const int src = sub < span ? (low ? lane + half : lane - half) : lane;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float o = __shfl_sync(0xffffffffu, v[i], src);
-      if (sub < span) v[i] = v[i] * cs[i].x + (low ? -o : o) * cs[i].y;
-    }
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = unpack2(h.p[i]);
+    const uint64_t o = interleaved ? pack2(v.y, v.x)
+                                   : pack2(__shfl_sync(0xffffffffu, v.x, t.src), __shfl_sync(0xffffffffu, v.y, t.src));
+    h.p[i] = fma2(o, t.s[i], mul2(h.p[i], t.c[i]));
   }
 }
 
@@ -145,29 +204,34 @@ struct QkParams {
 };
 
 constexpr int kQkThreads = 256;
+constexpr int kQkAhead = 4;  // head rows of a lane group in flight
 
 // Heads [h0, h1) of one token's rows, by a warp.
 template <int D>
 __device__ __forceinline__ void qk_rows(const HeadRows& in, const HeadRows& out, const float* weight, float eps,
-                                        const RopeParams& rope, const float2 (&cs)[8], int token, int h0, int h1) {
+                                        const RopeParams& rope, const Turn8& turn, int token, int h0, int h1) {
   constexpr int LPH = D / 8, HPW = 32 / LPH;  // heads of a warp at a time
   const int lane = threadIdx.x & 31, sub = lane & (LPH - 1), g = lane / LPH;
-  float w[8];
-  head_weight<LPH>(weight, sub, w);
-  const uint16_t* src = in.data + token * in.token + 8 * sub;
-  uint16_t* dst = out.data + token * out.token + 8 * sub;
-  auto load = [&](int h) {
-    return h + g < h1 ? __ldcg(reinterpret_cast<const uint4*>(src + (h + g) * in.head)) : make_uint4(0u, 0u, 0u, 0u);
-  };
-  uint4 raw = load(h0), next = load(h0 + HPW);
-  for (int h = h0; h < h1; h += HPW) {
-    float v[8];
-    bf16x8_to_float(raw, v);
-    raw = next;
-    next = load(h + 2 * HPW);
-    if (weight) head_norm<LPH>(v, w, eps);
-    if (rope.inv_freq) head_rope(v, rope, sub, cs);
-    if (h + g < h1) *reinterpret_cast<uint4*>(dst + (h + g) * out.head) = float_to_bf16x8(v);
+  const Head8 w = head_weight(weight, sub);
+  const uint16_t* src = in.data + token * in.token + (h0 + g) * in.head + 8 * sub;
+  uint16_t* dst = out.data + token * out.token + (h0 + g) * out.head + 8 * sub;
+  const long long step_in = HPW * in.head, step_out = HPW * out.head;
+  int left = h1 - h0 - g;  // heads of this lane group, HPW apart
+  for (; left + g > 0; left -= kQkAhead * HPW) {  // (left + g is the same for all lanes: the shuffles below)
+    uint4 raw[kQkAhead];
+#pragma unroll
+    for (int a = 0; a < kQkAhead; ++a)
+      raw[a] = left > a * HPW ? __ldcg(reinterpret_cast<const uint4*>(src + a * step_in)) : make_uint4(0u, 0u, 0u, 0u);
+    src += kQkAhead * step_in;
+#pragma unroll
+    for (int a = 0; a < kQkAhead; ++a) {
+      if (left + g <= a * HPW) break;
+      Head8 v = head_unpack(raw[a]);
+      if (weight) head_norm<LPH>(v, w, eps);
+      if (rope.inv_freq) head_rope(v, rope.interleaved, turn);
+      if (left > a * HPW) *reinterpret_cast<uint4*>(dst) = head_pack(v);
+      dst += step_out;
+    }
   }
 }
 
@@ -182,18 +246,18 @@ __host__ __device__ inline int qk_parts(int64_t tokens, int heads, int D) {
 template <int D>
 __device__ __forceinline__ void qk_token(const QkParams& p, int token, int pos, int part, int parts) {
   constexpr int HPW = 256 / D;
-  float2 cs[8];
-  if (p.rope.inv_freq) lane_angles(p.rope, threadIdx.x & (D / 8 - 1), pos, cs);
+  Turn8 turn{};
+  if (p.rope.inv_freq) turn = head_turn(p.rope, threadIdx.x & (D / 8 - 1), pos);
   const int sq = p.q.data ? (p.q.heads + HPW - 1) / HPW : 0, sk = p.k.data ? (p.k.heads + HPW - 1) / HPW : 0;
   const int s0 = (sq + sk) * part / parts, s1 = (sq + sk) * (part + 1) / parts;
   if (s0 < sq)
-    qk_rows<D>(p.q, p.q_out, p.q_weight, p.eps, p.rope, cs, token, s0 * HPW, min(p.q.heads, min(s1, sq) * HPW));
+    qk_rows<D>(p.q, p.q_out, p.q_weight, p.eps, p.rope, turn, token, s0 * HPW, min(p.q.heads, min(s1, sq) * HPW));
   if (s1 > sq)
-    qk_rows<D>(p.k, p.k_out, p.k_weight, p.eps, p.rope, cs, token, max(s0 - sq, 0) * HPW, min(p.k.heads, (s1 - sq) * HPW));
+    qk_rows<D>(p.k, p.k_out, p.k_weight, p.eps, p.rope, turn, token, max(s0 - sq, 0) * HPW, min(p.k.heads, (s1 - sq) * HPW));
 }
 
 template <int D>
-__global__ void __launch_bounds__(kQkThreads) qk_norm_rope_kernel(const QkParams p, int parts) {
+__global__ void __launch_bounds__(kQkThreads, 4) qk_norm_rope_kernel(const QkParams p, int parts) {
   pdl_wait();
   pdl_launch_dependents();
   const long long unit = ((long long)blockIdx.x * kQkThreads + threadIdx.x) >> 5;
