@@ -704,6 +704,15 @@ def _heads(t: torch.Tensor, dev: int, name: str, tokens: int, dim: int) -> bytes
     return _HEADS.pack(t.data_ptr(), token, head, shape[1], 0)
 
 
+def _out_heads(like: torch.Tensor, out: torch.Tensor | None, dev: int, name: str, tokens: int, dim: int):
+    """The output of rows shaped like ``like`` (a new tensor where none is given) and its w4a8_heads."""
+    if out is None:
+        out = like.new_empty(like.shape)
+        heads = like.shape[1]
+        return out, _HEADS.pack(out.data_ptr(), heads * dim, dim, heads, 0)
+    return out, _heads(out, dev, name, tokens, dim)
+
+
 def _rope(inv_freq, interleaved, factor, dev) -> bytes:
     if inv_freq is None:
         return _NO_ROPE
@@ -728,13 +737,11 @@ def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, positions: torc
     t, _, d = some.shape
     qs = qo = ks = ko = _NO_HEADS
     if q is not None:
-        if q_out is None:
-            q_out = q.new_empty(q.shape)
-        qs, qo = _heads(q, dev, "q", t, d), _heads(q_out, dev, "q_out", t, d)
+        qs = _heads(q, dev, "q", t, d)
+        q_out, qo = _out_heads(q, q_out, dev, "q_out", t, d)
     if k is not None:
-        if k_out is None:
-            k_out = k.new_empty(k.shape)
-        ks, ko = _heads(k, dev, "k", t, d), _heads(k_out, dev, "k_out", t, d)
+        ks = _heads(k, dev, "k", t, d)
+        k_out, ko = _out_heads(k, k_out, dev, "k_out", t, d)
     status = lib.w4a8_qk_norm_rope(
         qs, ks, t, d, None if q_weight is None else _at(q_weight, torch.float32, dev, "q_weight", (d,)),
         None if k_weight is None else _at(k_weight, torch.float32, dev, "k_weight", (d,)), eps,
@@ -802,9 +809,8 @@ def kv_update(cache: KvCache, k: torch.Tensor, v: torch.Tensor, block_table: tor
     t, d = k.shape[0], cache.head_dim
     qs = qo = _NO_HEADS
     if q is not None:
-        if q_out is None:
-            q_out = q.new_empty(q.shape)
-        qs, qo = _heads(q, dev, "q", t, d), _heads(q_out, dev, "q_out", t, d)
+        qs = _heads(q, dev, "q", t, d)
+        q_out, qo = _out_heads(q, q_out, dev, "q_out", t, d)
     status = lib.w4a8_kv_update(
         _cache_desc(cache, dev), _batch(block_table, q_start, kv_len, t, dev), _heads(k, dev, "k", t, d),
         _heads(v, dev, "v", t, d), qs, None if q_weight is None else _at(q_weight, torch.float32, dev, "q_weight", (d,)),
@@ -848,11 +854,11 @@ def kv_attention(q: torch.Tensor, cache: KvCache, block_table: torch.Tensor, q_s
     t, hq, d = q.shape[0], q.shape[1], cache.head_dim
     if workspace is None:
         workspace = kv_attention_workspace(t, hq, cache.kv_heads, d, q.device)
-    if out is None:
-        out = q.new_empty(q.shape)
+    qs = _heads(q, dev, "q", t, d)
+    out, outs = _out_heads(q, out, dev, "out", t, d)
     status = lib.w4a8_kv_attention(
-        _heads(q, dev, "q", t, d), _cache_desc(cache, dev), _batch(block_table, q_start, kv_len, t, dev),
-        d ** -0.5 if scale is None else scale, window, _heads(out, dev, "out", t, d),
+        qs, _cache_desc(cache, dev), _batch(block_table, q_start, kv_len, t, dev),
+        d ** -0.5 if scale is None else scale, window, outs,
         _at(workspace, torch.uint8, dev, "workspace"), workspace.numel(), _raw_stream(stream, dev))
     if status:
         raise W4A8Error("w4a8_kv_attention", status)

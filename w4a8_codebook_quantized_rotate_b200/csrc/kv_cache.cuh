@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) kv_update_kernel(const
       if (r0 + a * RPP >= n) break;  // (the same for all lanes: the norm and the rotation shuffle)
       v[a] = head_unpack(raw[a]);
       if (weight) head_norm<LPH>(v[a], w, p.qk.eps);
-      if (turn) head_rope(v[a], p.qk.rope.interleaved, head_turn(p.qk.rope, sub, pos[a]));
+      if (turn) head_rope(v[a], p.qk.rope.interleaved, head_turn<LPH>(p.qk.rope, sub, pos[a]));
     }
   };
   float amax = 0.f;

@@ -153,32 +153,48 @@ __device__ __forceinline__ void head_norm(Head8& h, const Head8& w, float eps) {
 // to v * c + (its partner) * s: half layout, pair (8 sub + i) % (rot_dim / 2)
 // for value i, the sine negative in the first half; interleaved, pair 4 sub +
 // i / 2, negative for the even value.  Lanes past the rotated part hold 1, 0.
+// The lanes of a head form M angles each and hand them round (where a quarter
+// of a head turns, its few lanes would form eight each while the others wait).
 struct Turn8 {
   uint64_t c[4], s[4];
   int src;  // half layout: the lane that holds the partners
 };
-__device__ __forceinline__ Turn8 head_turn(const RopeParams& r, int sub, int pos) {
-  const int span = r.rot_dim >> 3, half = span >> 1, lane = threadIdx.x & 31;
+template <int LPH, int M>
+__device__ __forceinline__ Turn8 head_turn_by(const RopeParams& r, int sub, int pos) {
+  const int span = r.rot_dim >> 3, half = span >> 1, lane = threadIdx.x & 31, group = lane & ~(LPH - 1);
   const bool low = sub < half, in = sub < span;
+  float2 mine[M];
+#pragma unroll
+  for (int i = 0; i < M; ++i)
+    mine[i] = 2 * (sub * M + i) < r.rot_dim ? rope_cs(r, pos, sub * M + i) : make_float2(1.f, 0.f);
+  const int p0 = !in ? 0 : r.interleaved ? 4 * sub : 8 * (low ? sub : sub - half);  // the lane's first pair
+  auto pair = [&](int i) {  // p0 is a multiple of 4, so pair p0 + i is number i % M of its lane
+    const int from = group + (p0 + i) / M;
+    return make_float2(__shfl_sync(0xffffffffu, mine[i % M].x, from), __shfl_sync(0xffffffffu, mine[i % M].y, from));
+  };
   Turn8 t;
   t.src = in && !r.interleaved ? (low ? lane + half : lane - half) : lane;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float2 a = make_float2(1.f, 0.f), b = a;
-    if (in && r.interleaved) {
-      a = rope_cs(r, pos, 4 * sub + i);
-      b = a;
+    float2 a, b;
+    if (r.interleaved) {
+      a = b = pair(i);
       a.y = -a.y;
-    } else if (in) {
-      const int p0 = 8 * (low ? sub : sub - half) + 2 * i;
-      a = rope_cs(r, pos, p0);
-      b = rope_cs(r, pos, p0 + 1);
+    } else {
+      a = pair(2 * i);
+      b = pair(2 * i + 1);
       if (low) a.y = -a.y, b.y = -b.y;
     }
-    t.c[i] = pack2(a.x, b.x);
-    t.s[i] = pack2(a.y, b.y);
+    t.c[i] = in ? pack2(a.x, b.x) : pack2(1.f, 1.f);
+    t.s[i] = in ? pack2(a.y, b.y) : pack2(0.f, 0.f);
   }
   return t;
+}
+template <int LPH>
+__device__ __forceinline__ Turn8 head_turn(const RopeParams& r, int sub, int pos) {
+  if (r.rot_dim <= 2 * LPH) return head_turn_by<LPH, 1>(r, sub, pos);
+  if (r.rot_dim <= 4 * LPH) return head_turn_by<LPH, 2>(r, sub, pos);
+  return head_turn_by<LPH, 4>(r, sub, pos);
 }
 
 // Rotation of a head's values; the whole warp takes part.
@@ -247,7 +263,7 @@ template <int D>
 __device__ __forceinline__ void qk_token(const QkParams& p, int token, int pos, int part, int parts) {
   constexpr int HPW = 256 / D;
   Turn8 turn{};
-  if (p.rope.inv_freq) turn = head_turn(p.rope, threadIdx.x & (D / 8 - 1), pos);
+  if (p.rope.inv_freq) turn = head_turn<D / 8>(p.rope, threadIdx.x & (D / 8 - 1), pos);
   const int sq = p.q.data ? (p.q.heads + HPW - 1) / HPW : 0, sk = p.k.data ? (p.k.heads + HPW - 1) / HPW : 0;
   const int s0 = (sq + sk) * part / parts, s1 = (sq + sk) * (part + 1) / parts;
   if (s0 < sq)
