@@ -95,6 +95,10 @@ SHAPES = [
     (513, 136, 2560),      # the last token tile holds one token
     (1, 5120, 5120),       # tiles cut between CTAs
     (50, 1161, 4304),
+    (2048, 2048, 256),     # whole 256 x 256 tiles on pairs of CTAs, two k blocks
+    (2000, 2300, 400),     # ragged tokens, rows and k; rows of y 8-byte aligned only
+    (1025, 6001, 1040),    # one token in the last tile, odd N
+    (4097, 1100, 144),
 ]
 
 

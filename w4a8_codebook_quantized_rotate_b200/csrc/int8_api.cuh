@@ -8,6 +8,8 @@
 namespace w4a8 {
 namespace {
 
+w4a8_status status_of(cudaError_t e) { return e == cudaSuccess ? W4A8_OK : W4A8_ERR_CUDA; }
+
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // ------------------------------------------------------------------ int8 layer
@@ -18,20 +20,27 @@ bool q8_shape_ok(int64_t M, int64_t N, int64_t K, int rotate) {
   return M > 0 && M <= kMaxTokens && q8_rows_ok(N) && q8_k_ok(K, rotate);
 }
 
-// Token tile, k split and CTAs per SM of a product: the choice with the least
-// estimated time (in clocks).  A CTA takes its k blocks at the slowest of
-// its loads (89 bytes a clock and SM), the latency of a pipeline that its
-// stages do not cover, and its MMAs; then an epilogue, or the joining of a
-// split tile; the rounds of CTAs that fit at once add up, and memory (2010
-// bytes a clock) bounds it all.  The constants are fitted to 1600 measured
-// (shape, choice) pairs over 70 shapes of 1 to 2048 tokens, K 64 to 17408, N
-// 16 to 17408: the choice is 2.4 % slower than the best measured one on
-// average.  For example 1 token, K = 17408, N = 5120: split 1 / 4 / 6 took
-// 38.6 / 17.3 / 16.3 us; 727 tokens, K = 512, N = 91: tiles of 16 / 256
-// tokens 4.1 / 19.7 us.
+// Kernel, token tile, k split and CTAs per SM of a product: the choice with
+// the least estimated time (in clocks).  A CTA takes its k blocks at the
+// slowest of its loads, the latency of a pipeline that its stages do not
+// cover, and its MMAs; then an epilogue, or the joining of a split tile; the
+// rounds of CTAs that fit at once add up, and memory bounds it all.  The
+// constants are fitted to measured times: up to 128 tokens to the times and
+// choices of 48 shapes (K 64 to 17408, N 16 to 17408; the choice is 2.2 %
+// slower than the best measured one on average), beyond to 1250 times of 120 shapes of up
+// to 8192 tokens (3 to 4 %).  For example 1 token, K = 17408, N = 5120: split
+// 1 / 4 / 6 took 38.6 / 17.3 / 16.3 us; 727 tokens, K = 512, N = 91: tiles of 16 /
+// 256 tokens 4.1 / 19.7 us; 4096 tokens, K = 5120, N = 17408: pairs 236 us, tiles
+// of 128 / 256 tokens 386 / 367.
 struct Q8Plan {
   int nt, cps, split;
+  bool pair;  // int8_pair_kernel (the rest is then unused)
 };
+struct Q8Model {
+  double rate, latency, epi, epi_nt, odd, join, join_nt, join_share, mma, start, memory, write;
+};
+constexpr Q8Model kQ8Few = {43.9, 3000, 2299, 18, 1, 2543, 8.7, 140, 1.41, 2001, 3105, 1e9};
+constexpr Q8Model kQ8Many = {47.7, 2594, 413, 33.3, 2.46, 2918, 11.3, 160, 1.18, 3030, 2239, 691};
 
 // Clusters of 1 .. 8 CTAs that fit at one CTA per SM (the GPU's answer,
 // cudaOccupancyMaxActiveClusters; a cluster stays inside one of its
@@ -40,6 +49,9 @@ constexpr int kQ8Clusters[kQ8MaxSplit + 1] = {0, 148, 74, 45, 33, 26, 22, 15, 15
 
 Q8Plan q8_plan(int64_t M, int64_t K, int64_t N) {
   const int64_t kb = (K + kQ8BK - 1) / kQ8BK, rows = (N + kQ8Rows - 1) / kQ8Rows;
+  const bool few = M <= 128;
+  const Q8Model& c = few ? kQ8Few : kQ8Many;
+  const double weights = double(N) * K + double(M) * K;
   Q8Plan best{};
   double least = 1e300;
   for (const int nt : {16, 32, 64, 128, 256}) {
@@ -52,15 +64,24 @@ Q8Plan q8_plan(int64_t M, int64_t K, int64_t N) {
       const double share = std::max(1.0, std::min(ctas, slots) / fit);
       const double stage = double(kQ8Rows + nt) * kQ8BK;
       const double stages = std::min(12.0, std::floor(((cps == 1 ? 232448 : 115712) - 2048) / stage));
-      const double step = std::max({stage / 89 * share, 1275 / stages, 1.1 * nt * share});
-      const double epilogue = split == 1 ? 38 + 34.0 * nt : 812 + 0.8 * nt + 89.0 * nt / split;
-      const double t = std::max(rounds * (double((kb + split - 1) / split) * step + epilogue * share),
-                                double(N * K + M * K) / 2010);
+      const double step = std::max({stage / c.rate * share, c.latency / stages, c.mma * nt * share});
+      const double epilogue = split == 1 ? (c.epi + c.epi_nt * nt) * (N % 8 ? c.odd : 1.0)
+                                         : c.join + c.join_nt * nt + c.join_share * nt / split;
+      const double busy = rounds * (double((kb + split - 1) / split) * step + epilogue * share);
+      // (a tenth of the CTAs' time, so that choices that memory bounds alike are told apart)
+      const double t = std::max(busy, weights / c.memory + double(M) * N * 2 / c.write) + 0.1 * busy * few + c.start;
       if (t < least) {
         least = t;
-        best = Q8Plan{nt, cps, split};
+        best = Q8Plan{nt, cps, split, false};
       }
     }
+  }
+  if (!few) {
+    // pairs: rounds of 74 tiles at the slower of the MMAs (with their loads) and the epilogue
+    const double tiles = double((N + kQ2Tile - 1) / kQ2Tile) * double((M + kQ2Tile - 1) / kQ2Tile);
+    const double epilogue = N % 8 == 0 ? 6113 : N % 2 == 0 ? 11616 : 15989;
+    const double t = std::max(std::ceil(tiles / 74) * std::max(kb * 740.0, epilogue) + epilogue / 2 + 5760, weights / 2080) + 1550;
+    best.pair = t < least;
   }
   return best;
 }
@@ -107,9 +128,10 @@ cudaError_t q8_launch(const CUtensorMap& tw, const CUtensorMap& tx, const Q8Para
 w4a8_status q8_gemm(const int8_t* x_q, const float* s_x, int64_t M, const int8_t* w_q, const float* s_w, int64_t N,
                     int64_t K, uint16_t* y, const DeviceState* d, cudaStream_t st) {
   const Q8Plan P = q8_plan(M, K, N);
+  const int nt = P.pair ? 128 : P.nt;  // token rows of a load
   CUtensorMap tw, tx;
   if (!byte_map(&tw, w_q, K, N, kQ8BK, kQ8Rows, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !byte_map(&tx, x_q, K, M, kQ8BK, uint32_t(P.nt), CU_TENSOR_MAP_SWIZZLE_128B))
+      !byte_map(&tx, x_q, K, M, kQ8BK, uint32_t(nt), CU_TENSOR_MAP_SWIZZLE_128B))
     return W4A8_ERR_CUDA;
   Q8Params p;
   p.s_x = s_x;
@@ -119,6 +141,21 @@ w4a8_status q8_gemm(const int8_t* x_q, const float* s_x, int64_t M, const int8_t
   p.M = int(M);
   p.N = int(N);
   p.KB = int((K + kQ8BK - 1) / kQ8BK);
+  if (P.pair) {
+    const int64_t tiles = ((N + kQ2Tile - 1) / kQ2Tile) * ((M + kQ2Tile - 1) / kQ2Tile);
+    const unsigned ctas = unsigned(2 * std::min<int64_t>(tiles, d->sms / 2));
+    CUtensorMap ty = tx;  // (used where the rows of y are 16-byte aligned)
+    if (N % 8 == 0) {
+      EncodeTiledFn enc = encode_fn();
+      const cuuint64_t dim[2] = {cuuint64_t(N), cuuint64_t(M)}, stride[1] = {cuuint64_t(N) * 2};
+      const cuuint32_t box[2] = {64, 32}, step[2] = {1, 1};
+      if (enc(&ty, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, y, dim, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) !=
+          CUDA_SUCCESS)
+        return W4A8_ERR_CUDA;
+    }
+    return status_of(launch_pdl_cluster(int8_pair_kernel, dim3(ctas), dim3(kQ2Threads), 2u, kQ2Smem, st, tw, tx, ty, p));
+  }
   cudaError_t e;
   switch (P.nt * 2 + P.cps - 1) {
     case 32: e = q8_launch<16, 1>(tw, tx, p, P.split, st); break;
@@ -244,6 +281,7 @@ bool int8_allow_smem() {
          allow_smem(int8_gemm_kernel<64, 1>, Q8Cfg<64, 1>::kSmem) == cudaSuccess &&
          allow_smem(int8_gemm_kernel<128, 2>, Q8Cfg<128, 2>::kSmem) == cudaSuccess &&
          allow_smem(int8_gemm_kernel<128, 1>, Q8Cfg<128, 1>::kSmem) == cudaSuccess &&
+         allow_smem(int8_pair_kernel, kQ2Smem) == cudaSuccess &&
          allow_smem(int8_gemm_kernel<256, 1>, Q8Cfg<256, 1>::kSmem) == cudaSuccess &&
          allow_smem(kv_attention_kernel<64>, KaCfg<64>::kSmem) == cudaSuccess &&
          allow_smem(kv_attention_kernel<128>, KaCfg<128>::kSmem) == cudaSuccess &&
@@ -263,8 +301,6 @@ w4a8_status int8_state(DeviceState** out) {
   }
   return W4A8_OK;
 }
-
-w4a8_status status_of(cudaError_t e) { return e == cudaSuccess ? W4A8_OK : W4A8_ERR_CUDA; }
 
 }  // namespace
 }  // namespace w4a8

@@ -328,8 +328,7 @@ __global__ void __launch_bounds__(KaCfg<D>::kThreads, 1)
   const int fgroup = lane % C::KG, ftile = lane / C::KG;
   int fi = 0, fend = 0, fbase = 0, fstage = 0, fid = -1, nraw = -1;
   float fks = 0.f, fvs = 0.f;
-  bool fload = false;  // fks, fvs are of this batch
-  KaSeg fseg;
+  KaSeg fseg{};
   auto group_key = [&](int item) { return fseg.key0 + (item * C::kWarps + warp) * C::TK + 16 * fgroup; };
   auto fetch_raw = [&](int base) {
     const int item = base + ftile;

@@ -19,6 +19,7 @@
 #include "gemv.cuh"
 #include "gemv1.cuh"
 #include "int8_gemm.cuh"
+#include "int8_pair.cuh"
 #include "int8_quant.cuh"
 #include "kv_attn.cuh"
 #include "kv_cache.cuh"
