@@ -78,12 +78,9 @@ def test_header_is_plain_c(B):
     assert subprocess.run([os.path.join(out, "a")]).returncode == 0
 
 
-def test_packed_descriptors_are_the_headers_structs(B):
-    same = lambda fmt, vals, s: fmt.pack(*vals, *([0] if fmt is not B._BATCH else [])) == bytes(s(*vals))
-    assert same(B._HEADS, (4096, 1 << 33, 72, 5), Heads)
-    assert same(B._ROPE, (4096, 64, 1, 1.5), Rope)
-    assert same(B._CACHE, (1 << 40, 2 << 40, 3 << 40, 4 << 40, 77, 8, 16, 128), CacheDesc)
-    assert same(B._BATCH, (1 << 40, 9, 2 << 40, 3 << 40, 4, 5), BatchDesc)
+def test_packed_cache_is_the_headers_struct(B):
+    vals = (1 << 40, 2 << 40, 3 << 40, 4 << 40, 77, 8, 16, 128)
+    assert B._CACHE.pack(*vals, 0) == bytes(CacheDesc(*vals))
 
 
 def test_int8_layer_refusals(lib):
@@ -213,15 +210,22 @@ def test_update_and_attention_refusals(B, lib):
 
 
 def test_binding_refuses_before_the_library(B):
-    x = torch.zeros(4, 512, dtype=torch.bfloat16)
-    with pytest.raises(ValueError):
-        B.int8_quantize(x)                                    # not on a GPU
-    with pytest.raises(ValueError):
-        B.int8_quantize(x.double())
+    """What needs no GPU to be refused: tensors elsewhere or of another kind, and no tensors."""
+    x, q = torch.zeros(4, 512, dtype=torch.bfloat16), torch.zeros(4, 2, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
         B.qk_norm_rope(None, None)
     with pytest.raises(ValueError):
-        B.qk_norm_rope(torch.zeros(4, 2, 64), None)
+        B.qk_norm_rope(q, None)                               # not on a GPU
+    with pytest.raises(ValueError):
+        B.qk_norm_rope(None, [1, 2])
+    with pytest.raises(ValueError):
+        B.int8_gemm(x, None, x, None)
+    with pytest.raises(ValueError):
+        B.int8_linear(x[0], x, None)
+    with pytest.raises(ValueError):
+        B.KvCache.of(*(torch.zeros(2, 2, 16, 64, dtype=torch.int8),) * 2, *(torch.zeros(2, 2),) * 2)
+    with pytest.raises(TypeError):
+        B._m().int8_gemm(x, x)
 
 
 def test_rope_frequencies(B):

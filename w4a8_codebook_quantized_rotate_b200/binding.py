@@ -564,48 +564,36 @@ def nvfp4_linear(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
 
 # ---------------------------------------------------------------- 8-bit integer path (include/w4a8_int8.h)
 #
-# These calls are short enough on the GPU for the host's share to count: a
-# tensor's checks are one expression, and the descriptors are packed bytes.
+# These calls are short enough on the GPU for the host's share to count, so
+# their checks, outputs and the C call are compiled (csrc/marshal.cpp, built
+# to lib/w4a8_marshal.so); the functions here name the arguments.
 
-_HEADS = struct.Struct("=QqqiI")    # w4a8_heads: data, token_stride, head_stride, heads, padding
-_ROPE = struct.Struct("=QiifI")     # w4a8_rope: inv_freq, rot_dim, interleaved, factor, padding
 _CACHE = struct.Struct("=QQQQqiiiI")  # w4a8_kv_cache: codes and scales of K and V, pages, kv_heads, page, head_dim, padding
-_BATCH = struct.Struct("=QqQQqq")   # w4a8_kv_batch: table, table_stride, q_start, kv_len, batch, tokens
-_NO_HEADS = _HEADS.pack(0, 0, 0, 0, 0)
-_NO_ROPE = _ROPE.pack(0, 0, 0, 1.0, 0)
+
+_marshal = None
 
 
-def _raw_stream(stream, dev: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-
-
-def _refuse(t, dtype, dev, name, shape):
-    _cuda(t, dtype, name)
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{dev}")
-    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-
-
-def _at(t: torch.Tensor, dtype: torch.dtype, dev: int, name: str, shape: tuple | None = None) -> int:
-    """The address of a contiguous tensor of that type (and shape) on the current device ``dev``."""
-    if t.get_device() != dev or t.dtype is not dtype or not t.is_contiguous() or (shape is not None and t.shape != shape):
-        _refuse(t, dtype, dev, name, shape)
-    return t.data_ptr()
+def _m():
+    """The compiled part of the binding."""
+    global _marshal
+    if _marshal is None:
+        import importlib.util
+        path = os.path.join(os.path.dirname(LIB_PATH), "w4a8_marshal.so")
+        if not os.path.exists(path):
+            raise ImportError(f"not built: {path} (run __graft_entry__.build())")
+        load_library()
+        spec = importlib.util.spec_from_file_location("w4a8_marshal", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.set_error(W4A8Error)
+        _marshal = module
+    return _marshal
 
 
 def int8_quantize(x: torch.Tensor, rotate: bool = True, stream=None):
     """x [R, K] (bf16 or fp32) -> (codes int8 [R, K], s fp32 [R]): one scale per
     row (output channels of a weight, tokens of an activation)."""
-    if x.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError("x must be bf16 or fp32")
-    lib, dev = load_library(), torch.cuda.current_device() if x.is_cuda else 0
-    xp = _at(x, x.dtype, dev, "x")
-    r, k = x.shape
-    codes = torch.empty((r, k), dtype=torch.int8, device=x.device)
-    s = torch.empty(r, dtype=torch.float32, device=x.device)
-    _check("w4a8_int8_quantize", lib.w4a8_int8_quantize(
-        xp, x.dtype is torch.float32, r, k, bool(rotate), codes.data_ptr(), s.data_ptr(), _raw_stream(stream, dev)))
-    return codes, s
+    return (_marshal or _m()).int8_quantize(x, rotate, stream)
 
 
 def int8_linear_workspace(m: int, k: int, n: int, device) -> torch.Tensor:
@@ -619,39 +607,13 @@ def int8_linear_workspace(m: int, k: int, n: int, device) -> torch.Tensor:
 def int8_gemm(x_q: torch.Tensor, s_x: torch.Tensor, w_q: torch.Tensor, s_w: torch.Tensor,
               out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """y [M, N] bf16 = s_x s_w (x_q [M, K] int8 times w_q [N, K]^T int8)."""
-    lib, dev = load_library(), torch.cuda.current_device()
-    xp = _at(x_q, torch.int8, dev, "x_q")
-    m, k = x_q.shape
-    n = w_q.shape[0]
-    wp, sp = _at(w_q, torch.int8, dev, "w_q", (n, k)), _at(s_w, torch.float32, dev, "s_w", (n,))
-    sx = _at(s_x, torch.float32, dev, "s_x", (m,))
-    if out is None:
-        out = torch.empty((m, n), dtype=torch.bfloat16, device=x_q.device)
-    status = lib.w4a8_int8_gemm(xp, sx, m, wp, sp, n, k, _at(out, torch.bfloat16, dev, "out", (m, n)),
-                                _raw_stream(stream, dev))
-    if status:
-        raise W4A8Error("w4a8_int8_gemm", status)
-    return out
+    return (_marshal or _m()).int8_gemm(x_q, s_x, w_q, s_w, out, stream)
 
 
 def int8_linear(x: torch.Tensor, w_q: torch.Tensor, s_w: torch.Tensor, rotate: bool = True,
                 workspace: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The int8 layer on bf16 x [M, K] against weights from int8_quantize(w, rotate)."""
-    lib, dev = load_library(), torch.cuda.current_device()
-    xp = _at(x, torch.bfloat16, dev, "x")
-    m, k = x.shape
-    n = w_q.shape[0]
-    wp, sp = _at(w_q, torch.int8, dev, "w_q", (n, k)), _at(s_w, torch.float32, dev, "s_w", (n,))
-    if workspace is None:
-        workspace = int8_linear_workspace(m, k, n, x.device)
-    if out is None:
-        out = x.new_empty((m, n))
-    status = lib.w4a8_int8_linear(xp, m, k, bool(rotate), wp, sp, n, _at(out, torch.bfloat16, dev, "out", (m, n)),
-                                  _at(workspace, torch.uint8, dev, "workspace"), workspace.numel(),
-                                  _raw_stream(stream, dev))
-    if status:
-        raise W4A8Error("w4a8_int8_linear", status)
-    return out
+    return (_marshal or _m()).int8_linear(x, w_q, s_w, rotate, workspace, out, stream)
 
 
 def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
@@ -686,41 +648,6 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str | None = 
     return inv.to(device), attention
 
 
-def _heads(t: torch.Tensor, dev: int, name: str, tokens: int, dim: int) -> bytes:
-    """bf16 [tokens, heads, D] with contiguous D -> w4a8_heads."""
-    shape = t.shape
-    if t.get_device() != dev or t.dtype is not torch.bfloat16 or len(shape) != 3:
-        raise ValueError(f"{name} must be a bf16 tensor [tokens, heads, D] on the current CUDA device")
-    if shape[0] != tokens or shape[2] != dim:
-        raise ValueError(f"{name} must be [{tokens}, heads, {dim}], got {tuple(shape)}")
-    token, head, one = t.stride()
-    if one != 1:
-        raise ValueError(f"{name}: the values of a head must be contiguous")
-    # a dimension of one row has no stride of its own
-    if shape[1] == 1:
-        head = dim
-    if tokens == 1:
-        token = shape[1] * dim
-    return _HEADS.pack(t.data_ptr(), token, head, shape[1], 0)
-
-
-def _out_heads(like: torch.Tensor, out: torch.Tensor | None, dev: int, name: str, tokens: int, dim: int):
-    """The output of rows shaped like ``like`` (a new tensor where none is given) and its w4a8_heads."""
-    if out is None:
-        out = like.new_empty(like.shape)
-        heads = like.shape[1]
-        return out, _HEADS.pack(out.data_ptr(), heads * dim, dim, heads, 0)
-    return out, _heads(out, dev, name, tokens, dim)
-
-
-def _rope(inv_freq, interleaved, factor, dev) -> bytes:
-    if inv_freq is None:
-        return _NO_ROPE
-    if inv_freq.dim() != 1:
-        raise ValueError("inv_freq must be [rot_dim / 2]")
-    return _ROPE.pack(_at(inv_freq, torch.float64, dev, "inv_freq"), 2 * inv_freq.shape[0], bool(interleaved), factor, 0)
-
-
 def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, positions: torch.Tensor | None = None,
                  q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, eps: float = 1e-6,
                  inv_freq: torch.Tensor | None = None, interleaved: bool = False, rope_factor: float = 1.0,
@@ -728,28 +655,8 @@ def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, positions: torc
     """RMS norm of every head of q [T, Hq, D] and k [T, Hk, D] (a weight of None
     leaves the norm out) and the rotation by ``positions`` [T] int32 and
     ``inv_freq`` (rope_frequencies; None: no rotation).  Returns (q_out, k_out)."""
-    some = q if q is not None else k
-    if some is None:
-        raise ValueError("q or k is needed")
-    if not some.is_cuda:
-        raise ValueError("q and k must be CUDA tensors")
-    lib, dev = load_library(), torch.cuda.current_device()
-    t, _, d = some.shape
-    qs = qo = ks = ko = _NO_HEADS
-    if q is not None:
-        qs = _heads(q, dev, "q", t, d)
-        q_out, qo = _out_heads(q, q_out, dev, "q_out", t, d)
-    if k is not None:
-        ks = _heads(k, dev, "k", t, d)
-        k_out, ko = _out_heads(k, k_out, dev, "k_out", t, d)
-    status = lib.w4a8_qk_norm_rope(
-        qs, ks, t, d, None if q_weight is None else _at(q_weight, torch.float32, dev, "q_weight", (d,)),
-        None if k_weight is None else _at(k_weight, torch.float32, dev, "k_weight", (d,)), eps,
-        None if positions is None else _at(positions, torch.int32, dev, "positions", (t,)),
-        _rope(inv_freq, interleaved, rope_factor, dev), qo, ko, _raw_stream(stream, dev))
-    if status:
-        raise W4A8Error("w4a8_qk_norm_rope", status)
-    return (q_out if q is not None else None), (k_out if k is not None else None)
+    return (_marshal or _m()).qk_norm_rope(q, k, positions, q_weight, k_weight, eps, inv_freq, interleaved, rope_factor,
+                                           q_out, k_out, stream)
 
 
 class KvCache:
@@ -770,29 +677,19 @@ class KvCache:
         return self
 
     def _set(self, k_codes, v_codes, k_scales, v_scales):
-        if k_codes.dim() != 4 or not k_codes.is_cuda:
-            raise ValueError("codes must be CUDA tensors [pages, kv_heads, page, D]")
-        shape, dev = tuple(k_codes.shape), k_codes.get_device()
-        at = (_at(k_codes, torch.int8, dev, "k_codes"), _at(v_codes, torch.int8, dev, "v_codes", shape),
-              _at(k_scales, torch.float32, dev, "k_scales", shape[:2]), _at(v_scales, torch.float32, dev, "v_scales", shape[:2]))
+        if k_codes.dim() != 4:
+            raise ValueError("codes must be [pages, kv_heads, page, D]")
+        shape = tuple(k_codes.shape)
+        for t, dtype, name, want in ((k_codes, torch.int8, "k_codes", shape), (v_codes, torch.int8, "v_codes", shape),
+                                     (k_scales, torch.float32, "k_scales", shape[:2]),
+                                     (v_scales, torch.float32, "v_scales", shape[:2])):
+            _cuda(t, dtype, name)
+            if tuple(t.shape) != want or t.device != k_codes.device:
+                raise ValueError(f"{name} must be {want} on {k_codes.device}, got {tuple(t.shape)} on {t.device}")
         self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
         self.pages, self.kv_heads, self.page, self.head_dim = shape
-        self.device_index, self.desc = dev, _CACHE.pack(*at, *shape, 0)
-
-
-def _cache_desc(cache: KvCache, dev: int) -> bytes:
-    if cache.device_index != dev:
-        raise ValueError(f"the cache is on cuda:{cache.device_index}, not on the current device cuda:{dev}")
-    return cache.desc
-
-
-def _batch(block_table, q_start, kv_len, tokens: int, dev: int) -> bytes:
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [batch, pages]")
-    table = _at(block_table, torch.int32, dev, "block_table")
-    b, width = block_table.shape
-    return _BATCH.pack(table, width, _at(q_start, torch.int32, dev, "q_start", (b + 1,)),
-                       _at(kv_len, torch.int32, dev, "kv_len", (b,)), b, tokens)
+        self.device_index = k_codes.get_device()
+        self.desc = _CACHE.pack(*(t.data_ptr() for t in (k_codes, v_codes, k_scales, v_scales)), *shape, 0)
 
 
 def kv_update(cache: KvCache, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor, q_start: torch.Tensor,
@@ -805,34 +702,13 @@ def kv_update(cache: KvCache, k: torch.Tensor, v: torch.Tensor, block_table: tor
     Sequence b's rows are q_start[b] .. q_start[b + 1], the last of its
     kv_len[b] tokens; positions None: the places in the sequences.  Returns
     q_out (None without q)."""
-    lib, dev = load_library(), torch.cuda.current_device()
-    t, d = k.shape[0], cache.head_dim
-    qs = qo = _NO_HEADS
-    if q is not None:
-        qs = _heads(q, dev, "q", t, d)
-        q_out, qo = _out_heads(q, q_out, dev, "q_out", t, d)
-    status = lib.w4a8_kv_update(
-        _cache_desc(cache, dev), _batch(block_table, q_start, kv_len, t, dev), _heads(k, dev, "k", t, d),
-        _heads(v, dev, "v", t, d), qs, None if q_weight is None else _at(q_weight, torch.float32, dev, "q_weight", (d,)),
-        None if k_weight is None else _at(k_weight, torch.float32, dev, "k_weight", (d,)), eps,
-        None if positions is None else _at(positions, torch.int32, dev, "positions", (t,)),
-        _rope(inv_freq, interleaved, rope_factor, dev), qo, _raw_stream(stream, dev))
-    if status:
-        raise W4A8Error("w4a8_kv_update", status)
-    return q_out if q is not None else None
+    return (_marshal or _m()).kv_update(cache.desc, cache.device_index, k, v, block_table, q_start, kv_len, q, positions,
+                                        q_weight, k_weight, eps, inv_freq, interleaved, rope_factor, q_out, stream)
 
 
 def kv_dequant(cache: KvCache, ids: torch.Tensor, stream=None):
     """Pages ``ids`` [n] int32 -> (k, v) bf16 [n, kv_heads, page, D]."""
-    lib, dev = load_library(), torch.cuda.current_device()
-    n = ids.shape[0]
-    at = _at(ids, torch.int32, dev, "ids", (n,))
-    out = torch.empty((2, n, cache.kv_heads, cache.page, cache.head_dim), dtype=torch.bfloat16, device=ids.device)
-    k, v = out.unbind(0)
-    status = lib.w4a8_kv_dequant(_cache_desc(cache, dev), at, n, k.data_ptr(), v.data_ptr(), _raw_stream(stream, dev))
-    if status:
-        raise W4A8Error("w4a8_kv_dequant", status)
-    return k, v
+    return (_marshal or _m()).kv_dequant(cache.desc, cache.device_index, ids, stream)
 
 
 def kv_attention_workspace(tokens: int, q_heads: int, kv_heads: int, head_dim: int, device) -> torch.Tensor:
@@ -850,16 +726,8 @@ def kv_attention(q: torch.Tensor, cache: KvCache, block_table: torch.Tensor, q_s
     int8 cache that holds the same tokens; ``scale`` defaults to D ** -0.5,
     ``window`` > 0 keeps the last so many positions.  Rows behind the last
     sequence are left as they were."""
-    lib, dev = load_library(), torch.cuda.current_device()
-    t, hq, d = q.shape[0], q.shape[1], cache.head_dim
+    d = cache.head_dim
     if workspace is None:
-        workspace = kv_attention_workspace(t, hq, cache.kv_heads, d, q.device)
-    qs = _heads(q, dev, "q", t, d)
-    out, outs = _out_heads(q, out, dev, "out", t, d)
-    status = lib.w4a8_kv_attention(
-        qs, _cache_desc(cache, dev), _batch(block_table, q_start, kv_len, t, dev),
-        d ** -0.5 if scale is None else scale, window, outs,
-        _at(workspace, torch.uint8, dev, "workspace"), workspace.numel(), _raw_stream(stream, dev))
-    if status:
-        raise W4A8Error("w4a8_kv_attention", status)
-    return out
+        workspace = kv_attention_workspace(q.shape[0], q.shape[1], cache.kv_heads, d, q.device)
+    return (_marshal or _m()).kv_attention(q, cache.desc, cache.device_index, block_table, q_start, kv_len,
+                                           d ** -0.5 if scale is None else scale, window, workspace, out, stream)

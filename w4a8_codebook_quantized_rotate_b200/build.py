@@ -1,4 +1,5 @@
-"""Builds ``lib/libw4a8.so`` from ``csrc/`` with nvcc for sm_100a (in-tree)."""
+"""Builds ``lib/libw4a8.so`` from ``csrc/`` with nvcc for sm_100a, and ``lib/w4a8_marshal.so``, the compiled part of
+the binding, against it (in-tree)."""
 
 from __future__ import annotations
 
@@ -10,6 +11,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRC = os.path.join(PKG, "csrc", "w4a8_api.cu")
 OUT = os.path.join(PKG, "lib", "libw4a8.so")
+MARSHAL_SRC = os.path.join(PKG, "csrc", "marshal.cpp")
+MARSHAL_OUT = os.path.join(PKG, "lib", "w4a8_marshal.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -31,16 +34,41 @@ def sources() -> list[str]:
         os.path.join(ROOT, "include", f) for f in ("w4a8.h", "w4a8_int8.h")]
 
 
+def _fresh(out: str, srcs: list[str]) -> bool:
+    return os.path.exists(out) and all(os.path.getmtime(s) <= os.path.getmtime(out) for s in srcs)
+
+
+def build_marshal(force: bool = False) -> str:
+    """Compile the binding's compiled part (host C++ over the C ABI and torch's tensors) if it is not up to date."""
+    headers = [os.path.join(ROOT, "include", f) for f in ("w4a8.h", "w4a8_int8.h")]
+    if not force and _fresh(MARSHAL_OUT, [MARSHAL_SRC, *headers]):
+        return MARSHAL_OUT
+    import sysconfig
+
+    import torch
+    home = os.path.dirname(torch.__file__)
+    lib = os.path.join(home, "lib")
+    include = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-I", os.path.join(ROOT, "include"),
+           *(x for i in include for x in ("-isystem", i)), MARSHAL_SRC, "-o", MARSHAL_OUT + ".tmp",
+           "-L", os.path.dirname(OUT), "-lw4a8", "-Wl,-rpath,$ORIGIN",
+           "-L", lib, "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda", "-Wl,-rpath," + lib]
+    subprocess.run(cmd, check=True)
+    os.replace(MARSHAL_OUT + ".tmp", MARSHAL_OUT)
+    return MARSHAL_OUT
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile the library if any source is newer than it; return its path."""
-    if not force and os.path.exists(OUT):
-        built = os.path.getmtime(OUT)
-        if all(os.path.getmtime(s) <= built for s in sources()):
-            return OUT
+    """Compile the library, and the binding's compiled part, if any source is newer; return the library's path."""
+    if not force and _fresh(OUT, sources()):
+        build_marshal()
+        return OUT
     os.makedirs(os.path.dirname(OUT), exist_ok=True)
     cmd = [nvcc(), *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-o", OUT + ".tmp", SRC]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")
     subprocess.run(cmd, check=True)
     os.replace(OUT + ".tmp", OUT)
+    build_marshal(force)
     return OUT

@@ -46,8 +46,8 @@ __global__ void __launch_bounds__(1024) int8_quant_kernel(const void* __restrict
                                                           int8_t* __restrict__ codes, float* __restrict__ scale) {
   extern __shared__ __align__(16) float q8_row[];  // [K]
   __shared__ float warp_max[32];
+  pdl_launch_dependents();  // (the next kernel waits for this one, and this one for the last)
   pdl_wait();
-  pdl_launch_dependents();
   const int64_t base = int64_t(blockIdx.x) * K;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
   float amax = 0.f;

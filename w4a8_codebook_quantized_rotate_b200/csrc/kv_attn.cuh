@@ -253,8 +253,8 @@ __global__ void __launch_bounds__(KaCfg<D>::kThreads, 1)
   static_assert(sizeof(KaShared) <= 4096, "shared block");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  pdl_launch_dependents();  // (the next kernel waits for this one, and this one for the last)
   pdl_wait();
-  pdl_launch_dependents();
   if (threadIdx.x == 0) {
     for (int w = 0; w < C::kWarps; ++w)
       for (int s = 0; s < C::kStages; ++s) {

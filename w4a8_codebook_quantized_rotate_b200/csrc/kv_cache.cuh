@@ -142,8 +142,8 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) kv_update_kernel(const
   constexpr int LPH = D / 8, RPP = THREADS / LPH;  // rows per pass
   constexpr int kAhead = 4;                        // passes of a chunk
   __shared__ float warp_max[THREADS / 32];
+  pdl_launch_dependents();  // (the next kernel waits for this one, and this one for the last)
   pdl_wait();
-  pdl_launch_dependents();
   const int g = threadIdx.x / LPH, sub = threadIdx.x & (LPH - 1);
   const int ps = p.cache.page_shift;
   if (int(blockIdx.x) >= p.page_ctas) {
@@ -253,8 +253,8 @@ constexpr int kDqThreads = 256;
 __global__ void __launch_bounds__(kDqThreads) kv_dequant_kernel(KvCacheParams c, const int* __restrict__ ids, int n,
                                                                 uint16_t* __restrict__ k_out,
                                                                 uint16_t* __restrict__ v_out, unsigned* err) {
+  pdl_launch_dependents();  // (the next kernel waits for this one, and this one for the last)
   pdl_wait();
-  pdl_launch_dependents();
   const int slab = c.D << c.page_shift;  // codes of a (page, head), a multiple of 1024
   const int parts = (slab + 16 * kDqThreads - 1) / (16 * kDqThreads);
   const long long unit = blockIdx.x / parts;  // (kind, nth, head)

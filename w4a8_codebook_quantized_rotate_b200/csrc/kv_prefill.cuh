@@ -178,8 +178,8 @@ __global__ void __launch_bounds__(KpCfg<D>::kThreads, 1) kv_prefill_kernel(const
   const uint32_t k0 = q0 + C::kTiles * C::kQ, v0 = k0 + C::kStages * C::kKV;
   KpShared* sh = reinterpret_cast<KpShared*>(kp_smem + (v0 + C::kStages * C::kKV - smem_u32(kp_smem)));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_launch_dependents();  // (the next kernel waits for this one, and this one for the last)
   pdl_wait();
-  pdl_launch_dependents();
   if (threadIdx.x == 0) {
     for (int i = 0; i < 4; ++i) {
       mbar_init(&sh->k_full[i], kKpConvWarps);

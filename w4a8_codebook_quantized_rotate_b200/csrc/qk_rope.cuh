@@ -274,8 +274,8 @@ __device__ __forceinline__ void qk_token(const QkParams& p, int token, int pos, 
 
 template <int D>
 __global__ void __launch_bounds__(kQkThreads, 4) qk_norm_rope_kernel(const QkParams p, int parts) {
+  pdl_launch_dependents();  // (the next kernel waits for this one, and this one for the last)
   pdl_wait();
-  pdl_launch_dependents();
   const long long unit = ((long long)blockIdx.x * kQkThreads + threadIdx.x) >> 5;
   const int token = int(unit / parts), part = int(unit - (long long)token * parts);
   if (token >= p.tokens) return;
