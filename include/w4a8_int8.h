@@ -33,7 +33,9 @@ extern "C" {
  * by H_256 / 16 before it is quantised, and the weights must have been
  * (w4a8_int8_quantize with rotate); K must then be a multiple of 256.
  * Shapes: M in [1, 16 776 960], N in [1, 2^24], K a positive multiple of 16,
- * at most W4A8_MAX_K.
+ * at most W4A8_MAX_K.  Weights and their scales are read before a kernel
+ * that precedes the call on the stream has completed, if that kernel allows
+ * it (programmatic launch); those of this library that write them do not.
  * ------------------------------------------------------------------------ */
 
 /*
@@ -105,7 +107,8 @@ typedef struct {
  *   n = x * rsqrt(mean(x^2) + eps) * weight,  out = rotate(n)
  * in fp32, rounded once to bf16.  q_weight / k_weight are fp32 [D]; NULL
  * leaves that norm out.  q.data or k.data may be NULL (then only the other
- * is done); an output may be its input (same strides).  positions [T] int32
+ * is done); an output may be its input (same strides), and the rows of an
+ * output must not share memory.  positions [T] int32
  * (may be NULL without a rotation).  D is 64, 128 or 256; T in [1, 2^24].
  * Errors: NULL, SHAPE, ALIGN, ARCH, CUDA.
  */
@@ -144,7 +147,7 @@ typedef struct {
 
 typedef struct {
   const int32_t* table;   /* [batch][table_stride] page ids */
-  int64_t table_stride;
+  int64_t table_stride;   /* at most 2^30 / page */
   const int32_t* q_start; /* [batch + 1] */
   const int32_t* kv_len;  /* [batch] */
   int64_t batch;          /* in [1, 65536] */
@@ -159,8 +162,9 @@ typedef struct {
  *   if the page's first token is written by this call; codes that were there
  *   become rint(code * (scale / scale')) when it grew.
  * k, v [tokens][kv_heads][D]; q and q_out (data NULL: none) [tokens][heads][D].
- * positions NULL: a token's position is its place in the sequence.  A page
- * must not be written by two sequences of one call.
+ * positions NULL: a token's position is its place in the sequence.  A call
+ * writes each page for one sequence and one place of its block table (a page
+ * id that stands there twice gets undefined contents).
  * Errors: NULL, SHAPE, ALIGN, ARCH, CUDA.
  */
 w4a8_status w4a8_kv_update(const w4a8_kv_cache* cache, const w4a8_kv_batch* batch, const w4a8_heads* k,

@@ -104,3 +104,17 @@ def test_block_refuses_layers_that_do_not_fit(lib, block):
         blocks.AttentionBlock(block.qkv, block.out, HEADS + 1, KV, D)
     with pytest.raises(ValueError):
         blocks.AttentionBlock(block.qkv, blocks.CodebookLayer(block.qkv, HIDDEN, 512), HEADS, KV, D)   # 512 inputs
+
+
+def test_workspaces_serve_many_token_counts(lib):
+    """Token counts up and down: a few workspaces serve them all, and every result is that of a fresh layer."""
+    from w4a8_codebook_quantized_rotate_b200 import blocks
+    for make in (codebook_layer, int8_layer):
+        layer = make(lib, 320, 768, 83)
+        x = torch.randn(300, 768, device="cuda", generator=torch.Generator("cuda").manual_seed(83)).to(torch.bfloat16)
+        for m in (1, 300, 2, 7, 33, 129, 300, 64, 1, 257):
+            fresh = (blocks.CodebookLayer(layer.packed, 320, 768) if make is codebook_layer
+                     else blocks.Int8Layer(layer.w_q, layer.s_w, layer.rotate))
+            assert torch.equal(layer(x[:m]), fresh(x[:m]))
+        held = [w.numel() for w in layer._workspaces._held]
+        assert all(b >= 2 * a for a, b in zip(held, held[1:])) and len(held) < 16

@@ -200,3 +200,45 @@ def test_refusals_of_the_binding(lib):
         lib.int8_linear(x, w, s, workspace=torch.zeros(64, dtype=torch.uint8, device="cuda"))
     with pytest.raises(lib.W4A8Error):
         lib.int8_linear(x[:, :272].contiguous(), w[:, :272].contiguous(), s, rotate=True)
+
+
+def test_weights_quantised_just_before_the_product(lib):
+    """The product fetches weights ahead of the kernel before it; one that writes them must have completed."""
+    m, n, k = 4, 464, 16384   # rows of the quantiser: a last wave of a few of the 148 SMs
+    x, sx, _, _ = operands(m, 16, k, 6)
+    x, sx = dev(x), dev(sx)
+    w = torch.randn(n, k, device="cuda", generator=torch.Generator("cuda").manual_seed(6))
+    codes, s = lib.int8_quantize(w, rotate=False)
+    torch.cuda.synchronize()
+    want = lib.int8_gemm(x, sx, codes, s)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for _ in range(4):
+            old = torch.full((n, k), 77, dtype=torch.int8, device="cuda")  # what the next allocation finds in its place
+            del old
+            wq, sw = lib.int8_quantize(w, rotate=False)
+            y = lib.int8_gemm(x, sx, wq, sw)
+            del wq, sw
+    for _ in range(5):
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+
+
+def test_scratch_belongs_to_the_calls_stream(lib):
+    """Without a workspace, on another stream that is behind: what the current stream allocates meanwhile is not it."""
+    m, n, k = 200, 1000, 4096
+    bits, _ = acts(m, k, 75)
+    wq, sw = lib.int8_quantize(dev(synth.weights(n, k, synth.rng_for(75, n, "weight"))), rotate=True)
+    x = bf16(bits)
+    want = lib.int8_linear(x, wq, sw)
+    s = torch.cuda.Stream()
+    torch.full((8,), 77, dtype=torch.uint8, device="cuda")  # (a kernel's first launch may wait for the device)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(400_000_000)
+    got = lib.int8_linear(x, wq, sw, stream=s)
+    used = [torch.full((size,), 77, dtype=torch.uint8, device="cuda") for size in [m * k + 1024] * 4 + [m * n * 2] * 4]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and all((u == 77).all() for u in used)

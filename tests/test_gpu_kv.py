@@ -406,3 +406,101 @@ def test_decode_steps_together(lib):
         g.replay()
     torch.cuda.synchronize()
     assert torch.equal(again, out) and lib.get_device_error() == 0
+
+
+@pytest.mark.parametrize("lens", [[(1, 300), (1, 16)], [(150, 700), (64, 64)]])
+@pytest.mark.parametrize("scale,window", [(0.0, 0), (0.0, 5), (0.3, 1)])
+def test_attention_even_and_single(lib, lens, scale, window):
+    """A scale of zero (the mean of the values), and a window of one token (its own value), of few and of many rows."""
+    b = Batch(lens, 4, 16, 128, 70)
+    q, qx = bf16(b.rng, b.t, 32, 128)
+    out = lib.kv_attention(q, b.cache(lib), *b.args(), scale=scale, window=window)
+    assert lib.get_device_error() == 0
+    check_attention(out, *R.attention(qx, b.ref, b.table, b.start, b.kv_len, scale, window), least=2.0 ** -32)
+
+
+def test_rows_before_the_first_sequence(lib):
+    """q_start[0] > 0: the rows before it are no sequence's, and stay as they were."""
+    b = Batch([(2, 40), (1, 30)], 2, 16, 128, 71)
+    pad = lambda x: torch.cat([torch.full_like(x[:2], 9.0), x])
+    q, k, v = (bf16(b.rng, b.t, h, 128)[0] for h in (4, 2, 2))
+    table, start, kv = b.args()
+    kw, inv = dev(np.ones(128, np.float32)), dev(INV[128])
+    one, two = b.cache(lib), b.cache(lib)
+    qo = lib.kv_update(one, k, v, table, start, kv, q=q, q_weight=kw, k_weight=kw, inv_freq=inv, q_out=torch.full_like(q, -3.0))
+    want = lib.kv_attention(qo, one, table, start, kv, out=torch.full_like(q, -3.0))
+    qp = lib.kv_update(two, pad(k), pad(v), table, start + 2, kv, q=pad(q), q_weight=kw, k_weight=kw, inv_freq=inv,
+                       q_out=torch.full_like(pad(q), -3.0))
+    got = lib.kv_attention(qp, two, table, start + 2, kv, out=torch.full_like(pad(q), -3.0))
+    assert lib.get_device_error() == 0
+    assert torch.equal(qp[2:], qo) and torch.equal(got[2:], want)
+    assert (qp[:2] == -3).all() and (got[:2] == -3).all()
+    assert torch.equal(one.k_codes, two.k_codes) and torch.equal(one.v_scales, two.v_scales)
+
+
+def test_calls_on_another_stream(lib):
+    """A stream given by name, with the current one behind: the call waits for nothing of it, its own workspace
+    included, and gives the same bits."""
+    b = Batch([(1, 3000), (1, 70), (300, 400)], 2, 16, 128, 72)
+    q, _ = bf16(b.rng, b.t, 8, 128)
+    k, _ = bf16(b.rng, b.t, 2, 128)
+    kw, inv = dev(np.ones(128, np.float32)), dev(INV[128])
+    pos = torch.arange(b.t, dtype=torch.int32, device="cuda")
+    ids = torch.arange(b.pages, dtype=torch.int32, device="cuda")
+    def run(cache, stream):
+        qo, _ = lib.qk_norm_rope(q, None, pos, kw, None, inv_freq=inv, stream=stream)
+        qo = lib.kv_update(cache, k, k, *args, q=qo, k_weight=kw, inv_freq=inv, stream=stream)
+        return [qo, lib.kv_attention(qo, cache, *args, stream=stream), *lib.kv_dequant(cache, ids, stream=stream)]
+    args, one, two = b.args(), b.cache(lib), b.cache(lib)
+    want = run(one, None)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(400_000_000)
+    got = run(two, s)
+    s.synchronize()
+    assert lib.get_device_error() == 0
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+def test_cache_is_what_it_holds_at_the_call(lib):
+    """Tensors put into a cache after it was made are the ones that the next call reads."""
+    b = Batch([(1, 40), (1, 7)], 2, 16, 128, 73)
+    q, _ = bf16(b.rng, b.t, 4, 128)
+    one, two = b.cache(lib), b.cache(lib)
+    two.k_codes.zero_()
+    two.v_scales.mul_(2)
+    want = lib.kv_attention(q, two, *b.args())
+    one.k_codes, one.v_scales = two.k_codes, two.v_scales
+    assert torch.equal(lib.kv_attention(q, one, *b.args()), want)
+    for name, bad in (("k_codes", two.k_codes[1:]), ("v_codes", two.v_codes.float()), ("k_scales", two.k_scales.cpu()),
+                      ("v_scales", None)):
+        broken = b.cache(lib)
+        setattr(broken, name, bad)
+        with pytest.raises(ValueError):
+            lib.kv_attention(q, broken, *b.args())
+        with pytest.raises(ValueError):
+            lib.kv_update(broken, q[:, :2], q[:, :2], *b.args())
+
+
+def test_refused_before_anything_runs(lib):
+    """A number that is none leaves the cache as it was; heads whose size does not fit 32 bits are not cut to it."""
+    b = Batch([(1, 40), (1, 7)], 2, 16, 128, 74)
+    k, _ = bf16(b.rng, b.t, 2, 128)
+    cache = b.cache(lib)
+    before = cache.k_codes.clone()
+    for bad in (dict(eps="small"), dict(eps=None), dict(rope_factor="one", inv_freq=dev(INV[128]))):
+        with pytest.raises(TypeError):
+            lib.kv_update(cache, k, k, *b.args(), k_weight=dev(np.ones(128, np.float32)), **bad)
+    with pytest.raises(TypeError):
+        lib.kv_attention(k, cache, *b.args(), scale="one")
+    for bad in (-1, 2 ** 40):
+        with pytest.raises(ValueError):
+            lib.kv_attention(k, cache, *b.args(), window=bad)
+    torch.cuda.synchronize()
+    assert torch.equal(cache.k_codes, before)
+    wide = torch.empty((1, 1, 2 ** 32 + 64), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError):
+        lib.qk_norm_rope(wide, None, q_out=wide)
+    shared = torch.empty((1, 4, 128), dtype=torch.bfloat16, device="cuda").expand(b.t, 4, 128)
+    with pytest.raises(lib.W4A8Error):
+        lib.kv_attention(torch.zeros(b.t, 4, 128, dtype=torch.bfloat16, device="cuda"), cache, *b.args(), out=shared)

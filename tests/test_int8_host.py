@@ -78,10 +78,6 @@ def test_header_is_plain_c(B):
     assert subprocess.run([os.path.join(out, "a")]).returncode == 0
 
 
-def test_packed_cache_is_the_headers_struct(B):
-    vals = (1 << 40, 2 << 40, 3 << 40, 4 << 40, 77, 8, 16, 128)
-    assert B._CACHE.pack(*vals, 0) == bytes(CacheDesc(*vals))
-
 
 def test_int8_layer_refusals(lib):
     ws = lib.w4a8_int8_linear_workspace_bytes(5, 512, 64)
@@ -184,9 +180,15 @@ def test_update_and_attention_refusals(B, lib):
     assert _update(B, lib, batch=_batch(B, table=None)) == NULL
     assert _update(B, lib, batch=_batch(B, table=P + 2)) == ALIGN
     for bad in (dict(batch=0), dict(batch=65537), dict(tokens=0), dict(tokens=2 ** 24 + 1), dict(width=0),
-                dict(width=2 ** 27)):
+                dict(width=2 ** 27), dict(width=2 ** 26 + 1)):
         assert _update(B, lib, batch=_batch(B, **bad)) == SHAPE
         assert _attend(B, lib, batch=_batch(B, **bad)) == SHAPE
+    shared = Heads(P, 0, 128, 4), Heads(P, 504, 128, 4), Heads(P, 128, 128, 4), Heads(P, 128, 256, 4)   # of 3 tokens
+    for rows in shared:                                          # rows of an output that share memory
+        assert _attend(B, lib, out=rows) == SHAPE
+        assert _update(B, lib, q=_heads(B), qo=rows) == SHAPE
+        assert lib.w4a8_qk_norm_rope(ctypes.byref(_heads(B)), None, 3, 128, None, None, 1e-6, None, None,
+                                     ctypes.byref(rows), None, None) == SHAPE
     assert _update(B, lib, k=_heads(B, 4)) == SHAPE              # the cache has 2 heads
     assert _update(B, lib, q=_heads(B)) == NULL                  # q without q_out
     assert _update(B, lib, q=_heads(B), qo=_heads(B, 3)) == SHAPE

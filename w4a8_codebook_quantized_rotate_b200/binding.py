@@ -10,7 +10,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 
 import torch
 
@@ -568,8 +567,6 @@ def nvfp4_linear(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
 # their checks, outputs and the C call are compiled (csrc/marshal.cpp, built
 # to lib/w4a8_marshal.so); the functions here name the arguments.
 
-_CACHE = struct.Struct("=QQQQqiiiI")  # w4a8_kv_cache: codes and scales of K and V, pages, kv_heads, page, head_dim, padding
-
 _marshal = None
 
 
@@ -596,9 +593,13 @@ def int8_quantize(x: torch.Tensor, rotate: bool = True, stream=None):
     return (_marshal or _m()).int8_quantize(x, rotate, stream)
 
 
+def int8_linear_workspace_bytes(m: int, k: int, n: int) -> int:
+    return int(load_library().w4a8_int8_linear_workspace_bytes(m, k, n))
+
+
 def int8_linear_workspace(m: int, k: int, n: int, device) -> torch.Tensor:
     """A workspace for int8 layers of shape (M, K, N)."""
-    need = int(load_library().w4a8_int8_linear_workspace_bytes(m, k, n))
+    need = int8_linear_workspace_bytes(m, k, n)
     if need == 0:
         raise W4A8Error("w4a8_int8_linear_workspace_bytes", 2)
     return torch.empty(need, dtype=torch.uint8, device=device)
@@ -688,8 +689,6 @@ class KvCache:
                 raise ValueError(f"{name} must be {want} on {k_codes.device}, got {tuple(t.shape)} on {t.device}")
         self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
         self.pages, self.kv_heads, self.page, self.head_dim = shape
-        self.device_index = k_codes.get_device()
-        self.desc = _CACHE.pack(*(t.data_ptr() for t in (k_codes, v_codes, k_scales, v_scales)), *shape, 0)
 
 
 def kv_update(cache: KvCache, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor, q_start: torch.Tensor,
@@ -702,13 +701,13 @@ def kv_update(cache: KvCache, k: torch.Tensor, v: torch.Tensor, block_table: tor
     Sequence b's rows are q_start[b] .. q_start[b + 1], the last of its
     kv_len[b] tokens; positions None: the places in the sequences.  Returns
     q_out (None without q)."""
-    return (_marshal or _m()).kv_update(cache.desc, cache.device_index, k, v, block_table, q_start, kv_len, q, positions,
+    return (_marshal or _m()).kv_update(cache, k, v, block_table, q_start, kv_len, q, positions,
                                         q_weight, k_weight, eps, inv_freq, interleaved, rope_factor, q_out, stream)
 
 
 def kv_dequant(cache: KvCache, ids: torch.Tensor, stream=None):
     """Pages ``ids`` [n] int32 -> (k, v) bf16 [n, kv_heads, page, D]."""
-    return (_marshal or _m()).kv_dequant(cache.desc, cache.device_index, ids, stream)
+    return (_marshal or _m()).kv_dequant(cache, ids, stream)
 
 
 def kv_attention_workspace(tokens: int, q_heads: int, kv_heads: int, head_dim: int, device) -> torch.Tensor:
@@ -726,8 +725,4 @@ def kv_attention(q: torch.Tensor, cache: KvCache, block_table: torch.Tensor, q_s
     int8 cache that holds the same tokens; ``scale`` defaults to D ** -0.5,
     ``window`` > 0 keeps the last so many positions.  Rows behind the last
     sequence are left as they were."""
-    d = cache.head_dim
-    if workspace is None:
-        workspace = kv_attention_workspace(q.shape[0], q.shape[1], cache.kv_heads, d, q.device)
-    return (_marshal or _m()).kv_attention(q, cache.desc, cache.device_index, block_table, q_start, kv_len,
-                                           d ** -0.5 if scale is None else scale, window, workspace, out, stream)
+    return (_marshal or _m()).kv_attention(q, cache, block_table, q_start, kv_len, scale, window, workspace, out, stream)

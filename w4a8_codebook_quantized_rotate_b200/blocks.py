@@ -19,17 +19,38 @@ import torch
 from . import binding as B
 
 
+class _Workspaces:
+    """Workspaces of a layer for any number of tokens: the last one serves every call that it is large enough for;
+    where it is too small the next one is at least twice as large, and the earlier ones stay for captured graphs that
+    name them."""
+
+    def __init__(self, need):
+        self._need = need
+        self._held: list[torch.Tensor] = []
+        self._of: dict[int, torch.Tensor] = {}
+
+    def get(self, m: int, device) -> torch.Tensor:
+        ws = self._of.get(m)
+        if ws is None:
+            need = self._need(m)
+            if need == 0:
+                raise B.W4A8Error("workspace", 2)
+            if not self._held or self._held[-1].numel() < need:
+                need = max(need, 2 * self._held[-1].numel() if self._held else 0)
+                self._held.append(torch.zeros(need, dtype=torch.uint8, device=device))
+            ws = self._of[m] = self._held[-1]
+        return ws
+
+
 class CodebookLayer:
     """y = w4a8_linear(x) on a packed [N, K] layer (:func:`binding.pack_layout`)."""
 
     def __init__(self, packed: torch.Tensor, n: int, k: int):
         self.packed, self.n, self.k = packed, n, k
-        self._workspaces: dict[int, torch.Tensor] = {}
+        self._workspaces = _Workspaces(lambda m: B.linear_workspace_bytes(m, k, n))
 
     def prepare(self, m: int) -> torch.Tensor:
-        if m not in self._workspaces:
-            self._workspaces[m] = B.linear_workspace(m, self.k, self.n, self.packed.device)
-        return self._workspaces[m]
+        return self._workspaces.get(m, self.packed.device)
 
     def __call__(self, x: torch.Tensor) -> torch.Tensor:
         return B.linear(x, self.packed, self.n, workspace=self.prepare(x.shape[0]))
@@ -41,12 +62,10 @@ class Int8Layer:
     def __init__(self, w_q: torch.Tensor, s_w: torch.Tensor, rotate: bool = True):
         self.w_q, self.s_w, self.rotate = w_q, s_w, rotate
         self.n, self.k = w_q.shape
-        self._workspaces: dict[int, torch.Tensor] = {}
+        self._workspaces = _Workspaces(lambda m: B.int8_linear_workspace_bytes(m, self.k, self.n))
 
     def prepare(self, m: int) -> torch.Tensor:
-        if m not in self._workspaces:
-            self._workspaces[m] = B.int8_linear_workspace(m, self.k, self.n, self.w_q.device)
-        return self._workspaces[m]
+        return self._workspaces.get(m, self.w_q.device)
 
     def __call__(self, x: torch.Tensor) -> torch.Tensor:
         return B.int8_linear(x, self.w_q, self.s_w, rotate=self.rotate, workspace=self.prepare(x.shape[0]))
@@ -77,15 +96,15 @@ class AttentionBlock:
         self.rotation = dict(q_weight=q_weight, k_weight=k_weight, eps=eps, inv_freq=inv_freq, interleaved=interleaved,
                              rope_factor=rope_factor)
         self.scale, self.window = scale, window
-        self._workspaces: dict[int, torch.Tensor] = {}
+        self._workspace = None  # of the attention, for any number of tokens
 
     def prepare(self, tokens: int, device="cuda") -> torch.Tensor:
         """Allocate what steps of that many tokens need; returns the attention's workspace."""
         self.qkv.prepare(tokens)
         self.out.prepare(tokens)
-        if tokens not in self._workspaces:
-            self._workspaces[tokens] = B.kv_attention_workspace(tokens, self.heads, self.kv_heads, self.head_dim, device)
-        return self._workspaces[tokens]
+        if self._workspace is None:
+            self._workspace = B.kv_attention_workspace(tokens, self.heads, self.kv_heads, self.head_dim, device)
+        return self._workspace
 
     def __call__(self, x: torch.Tensor, cache: B.KvCache, block_table: torch.Tensor, q_start: torch.Tensor,
                  kv_len: torch.Tensor, positions: torch.Tensor | None = None) -> torch.Tensor:

@@ -97,11 +97,11 @@ Q8Ws q8_ws(int64_t M, int64_t K) {
   return w;
 }
 
-cudaError_t q8_quantize(const void* x, int f32, int64_t R, int64_t K, int rotate, int8_t* codes, float* s,
+cudaError_t q8_quantize(const void* x, int f32, int64_t R, int64_t K, int rotate, bool early, int8_t* codes, float* s,
                         cudaStream_t st) {
   const dim3 grid{unsigned(R)}, block{unsigned(q8_threads(R, K))};
-  return f32 ? launch_pdl(int8_quant_kernel<true>, grid, block, size_t(K) * 4, st, x, int(K), int(rotate), codes, s)
-             : launch_pdl(int8_quant_kernel<false>, grid, block, size_t(K) * 4, st, x, int(K), int(rotate), codes, s);
+  return f32 ? launch_pdl(int8_quant_kernel<true>, grid, block, size_t(K) * 4, st, x, int(K), int(rotate), early, codes, s)
+             : launch_pdl(int8_quant_kernel<false>, grid, block, size_t(K) * 4, st, x, int(K), int(rotate), early, codes, s);
 }
 
 // 2-D map of rows of bytes, box [box_cols x box_rows].
@@ -182,6 +182,14 @@ w4a8_status heads_ok(const w4a8_heads& h, int64_t D) {
     return W4A8_ERR_SHAPE;
   return aligned16(h.data) ? W4A8_OK : W4A8_ERR_ALIGN;
 }
+// Rows of tokens that are written must not share memory.
+w4a8_status heads_out_ok(const w4a8_heads& h, int64_t tokens, int64_t D) {
+  if (w4a8_status st = heads_ok(h, D); st != W4A8_OK) return st;
+  const int64_t token = (h.heads - 1) * (h.heads > 1 ? h.head_stride : 0) + D;  // values from a token's first to its last
+  const int64_t head = (tokens - 1) * h.token_stride + D;                       // and of a head over the tokens
+  const bool apart = tokens == 1 || h.token_stride >= token || (h.token_stride >= D && (h.heads == 1 || h.head_stride >= head));
+  return apart ? W4A8_OK : W4A8_ERR_SHAPE;
+}
 HeadRows head_rows(const w4a8_heads* h) {
   if (!h || !h->data) return HeadRows{nullptr, 0, 0, 0};
   return HeadRows{h->data, h->token_stride, h->head_stride, h->heads};
@@ -224,7 +232,7 @@ KvCacheParams cache_params(const w4a8_kv_cache* c) {
 w4a8_status batch_ok(const w4a8_kv_batch* b, int page) {
   if (!b || !b->table || !b->q_start || !b->kv_len) return W4A8_ERR_NULL;
   if (b->batch < 1 || b->batch > 65536 || b->tokens < 1 || b->tokens > (int64_t(1) << 24) || b->table_stride < 1 ||
-      b->table_stride * page >= (int64_t(1) << 31))
+      b->table_stride > kKvMaxTokens / page)
     return W4A8_ERR_SHAPE;
   if (!aligned4(b->table) || !aligned4(b->q_start) || !aligned4(b->kv_len)) return W4A8_ERR_ALIGN;
   return W4A8_OK;
@@ -314,7 +322,7 @@ w4a8_status w4a8_int8_quantize(const void* x, int32_t x_is_f32, int64_t R, int64
   if (!aligned16(x) || !aligned16(codes) || !aligned16(s)) return W4A8_ERR_ALIGN;
   DeviceState* d = nullptr;
   if (w4a8_status st = int8_state(&d); st != W4A8_OK) return st;
-  return status_of(q8_quantize(x, x_is_f32, R, K, rotate, codes, s, static_cast<cudaStream_t>(stream)));
+  return status_of(q8_quantize(x, x_is_f32, R, K, rotate, false, codes, s, static_cast<cudaStream_t>(stream)));
 }
 
 w4a8_status w4a8_int8_gemm(const int8_t* x_q, const float* s_x, int64_t M, const int8_t* w_q, const float* s_w,
@@ -344,7 +352,7 @@ w4a8_status w4a8_int8_linear(const uint16_t* x, int64_t M, int64_t K, int32_t ro
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int8_t* codes = static_cast<int8_t*>(workspace);
   float* s_x = reinterpret_cast<float*>(codes + w.off_s);
-  if (q8_quantize(x, 0, M, K, rotate, codes, s_x, s) != cudaSuccess) return W4A8_ERR_CUDA;
+  if (q8_quantize(x, 0, M, K, rotate, true, codes, s_x, s) != cudaSuccess) return W4A8_ERR_CUDA;
   return q8_gemm(codes, s_x, M, w_q, s_w, N, K, y, d, s);
 }
 
@@ -355,9 +363,12 @@ w4a8_status w4a8_qk_norm_rope(const w4a8_heads* q, const w4a8_heads* k, int64_t 
   if ((!has_q && !has_k) || (has_q && (!q_out || !q_out->data)) || (has_k && (!k_out || !k_out->data))) return W4A8_ERR_NULL;
   if (rope && rope->inv_freq && !positions) return W4A8_ERR_NULL;
   if (T < 1 || T > (int64_t(1) << 24) || !head_dim_ok(D)) return W4A8_ERR_SHAPE;
-  for (const w4a8_heads* h : {has_q ? q : nullptr, has_q ? q_out : nullptr, has_k ? k : nullptr, has_k ? k_out : nullptr})
+  for (const w4a8_heads* h : {has_q ? q : nullptr, has_k ? k : nullptr})
     if (h)
       if (w4a8_status st = heads_ok(*h, D); st != W4A8_OK) return st;
+  for (const w4a8_heads* h : {has_q ? q_out : nullptr, has_k ? k_out : nullptr})
+    if (h)
+      if (w4a8_status st = heads_out_ok(*h, T, D); st != W4A8_OK) return st;
   if ((has_q && q->heads != q_out->heads) || (has_k && k->heads != k_out->heads)) return W4A8_ERR_SHAPE;
   if (w4a8_status st = rope_ok(rope, D); st != W4A8_OK) return st;
   if ((q_weight && !aligned16(q_weight)) || (k_weight && !aligned16(k_weight)) || !aligned4(positions)) return W4A8_ERR_ALIGN;
@@ -382,9 +393,11 @@ w4a8_status w4a8_kv_update(const w4a8_kv_cache* cache, const w4a8_kv_batch* batc
   if (w4a8_status st = cache_ok(cache); st != W4A8_OK) return st;
   if (w4a8_status st = batch_ok(batch, cache->page); st != W4A8_OK) return st;
   const int D = cache->head_dim;
-  for (const w4a8_heads* h : {k, v, has_q ? q : nullptr, has_q ? q_out : nullptr})
+  for (const w4a8_heads* h : {k, v, has_q ? q : nullptr})
     if (h)
       if (w4a8_status st = heads_ok(*h, D); st != W4A8_OK) return st;
+  if (has_q)
+    if (w4a8_status st = heads_out_ok(*q_out, batch->tokens, D); st != W4A8_OK) return st;
   if (k->heads != cache->kv_heads || v->heads != cache->kv_heads || (has_q && q->heads != q_out->heads)) return W4A8_ERR_SHAPE;
   if (w4a8_status st = rope_ok(rope, D); st != W4A8_OK) return st;
   if ((q_weight && !aligned16(q_weight)) || (k_weight && !aligned16(k_weight)) || !aligned4(positions)) return W4A8_ERR_ALIGN;
@@ -445,8 +458,8 @@ w4a8_status w4a8_kv_attention(const w4a8_heads* q, const w4a8_kv_cache* cache, c
   if (w4a8_status st = cache_ok(cache); st != W4A8_OK) return st;
   if (w4a8_status st = batch_ok(batch, cache->page); st != W4A8_OK) return st;
   const int D = cache->head_dim;
-  for (const w4a8_heads* h : {q, out})
-    if (w4a8_status st = heads_ok(*h, D); st != W4A8_OK) return st;
+  if (w4a8_status st = heads_ok(*q, D); st != W4A8_OK) return st;
+  if (w4a8_status st = heads_out_ok(*out, batch->tokens, D); st != W4A8_OK) return st;
   if (q->heads != out->heads || window < 0 || !ka_shape_ok(batch->tokens, q->heads, cache->kv_heads, D)) return W4A8_ERR_SHAPE;
   if (!aligned16(workspace)) return W4A8_ERR_ALIGN;
   if (workspace_bytes < w4a8_kv_attention_workspace_bytes(batch->tokens, q->heads, cache->kv_heads, D))

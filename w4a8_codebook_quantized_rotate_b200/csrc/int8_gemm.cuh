@@ -187,6 +187,7 @@ __global__ void __launch_bounds__(kQ8Threads, CPS)
   } else if (warp == 1) {
     // ------------------------------------------------ MMA issuer
     if (lane == 0) {
+      pdl_wait();  // (the bounded waits below are for this launch's own loads, not for the kernels before it)
       bool ok = true;
       int s = 0;
       uint32_t phase = 0;
@@ -213,11 +214,11 @@ __global__ void __launch_bounds__(kQ8Threads, CPS)
     // ------------------------------------------------ epilogue: a warp per TMEM lane quarter
     const int q = warp & 3;
     const uint32_t acc = tmem + (uint32_t(32 * q) << 16);
+    pdl_wait();  // s_x, and y's earlier readers
     const int w_ok = lane == 0 ? int(q8_wait(&sh->acc_full, 0, sh, p.err)) : 0;
     if (__shfl_sync(0xffffffffu, w_ok, 0) != 0) {
       tc_fence_after();
       if (split == 1) {
-        pdl_wait();  // s_x, and y's earlier readers
         const int n = n0 + 32 * q + lane;
         const float sw = n < p.N ? p.s_w[n] : 0.f;
         const uint32_t tbuf = stage0 + uint32_t(q) * 2048u;  // every stage is free by now

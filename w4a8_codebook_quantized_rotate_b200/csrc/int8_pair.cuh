@@ -128,7 +128,6 @@ __global__ void __launch_bounds__(kQ2Threads, 1)
     int8_pair_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x,
                      const __grid_constant__ CUtensorMap tmap_y, const Q8Params p) {
   extern __shared__ __align__(1024) uint8_t q2_smem[];
-  pdl_launch_dependents();
   Q2Shared* sh = reinterpret_cast<Q2Shared*>(q2_smem);
   const uint32_t stage0 = (smem_u32(q2_smem) + uint32_t(sizeof(Q2Shared)) + 1023u) & ~1023u;
   const uint32_t trans0 = stage0 + uint32_t(kQ2Stages) * kQ2Stage;
@@ -186,11 +185,13 @@ __global__ void __launch_bounds__(kQ2Threads, 1)
           if (++s == kQ2Stages) { s = 0; phase ^= 1u; }
         }
       }
+      pdl_launch_dependents();  // (late: the next kernel's bounded waits must not last as long as this one)
       if (sh->abort) q8_settle();
     }
   } else if (warp == 1) {
     // ------------------------------------------------ MMA issuer (first CTA)
     if (lane == 0 && rank == 0) {
+      pdl_wait();  // (the bounded waits below are for this launch's own loads, not for the kernels before it)
       int s = 0, n = 0;
       uint32_t phase = 0;
       bool ok = true, in = false;

@@ -41,12 +41,15 @@ __host__ __device__ inline int q8_threads(int64_t rows, int64_t K) {
   return int(t < 64 ? 64 : t > 1024 ? 1024 : t);
 }
 
+// `early`: the next kernel may launch now, if it waits for this one before it
+// reads the codes.  The layer's product does so for activations; weights it
+// fetches before that wait, so a call of the quantiser alone is not early.
 template <bool F32>
-__global__ void __launch_bounds__(1024) int8_quant_kernel(const void* __restrict__ x, int K, int rotate,
+__global__ void __launch_bounds__(1024) int8_quant_kernel(const void* __restrict__ x, int K, int rotate, bool early,
                                                           int8_t* __restrict__ codes, float* __restrict__ scale) {
   extern __shared__ __align__(16) float q8_row[];  // [K]
   __shared__ float warp_max[32];
-  pdl_launch_dependents();  // (the next kernel waits for this one, and this one for the last)
+  if (early) pdl_launch_dependents();
   pdl_wait();
   const int64_t base = int64_t(blockIdx.x) * K;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;

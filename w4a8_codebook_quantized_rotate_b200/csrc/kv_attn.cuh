@@ -253,7 +253,6 @@ __global__ void __launch_bounds__(KaCfg<D>::kThreads, 1)
   static_assert(sizeof(KaShared) <= 4096, "shared block");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  pdl_launch_dependents();  // (the next kernel waits for this one, and this one for the last)
   pdl_wait();
   if (threadIdx.x == 0) {
     for (int w = 0; w < C::kWarps; ++w)
@@ -595,6 +594,7 @@ __global__ void __launch_bounds__(KaCfg<D>::kThreads, 1)
 
     // ---- the next row tile's loads go out, then join the warps
     const bool more = walk.next(p, nxt);
+    if (!more) pdl_launch_dependents();  // (late: the next kernel's bounded waits must not last as long as this one)
     if (more && ok) start(nxt);
 #pragma unroll
     for (int off = 1; off < 4; off <<= 1) {

@@ -18,6 +18,8 @@
 
 namespace w4a8 {
 
+constexpr int64_t kKvMaxTokens = int64_t(1) << 30;  // that a block table has places for, a sequence
+
 struct KvSeq {
   int start;    // row of its first new token
   int q_len;    // new tokens

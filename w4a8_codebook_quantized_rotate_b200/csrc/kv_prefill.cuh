@@ -178,7 +178,6 @@ __global__ void __launch_bounds__(KpCfg<D>::kThreads, 1) kv_prefill_kernel(const
   const uint32_t k0 = q0 + C::kTiles * C::kQ, v0 = k0 + C::kStages * C::kKV;
   KpShared* sh = reinterpret_cast<KpShared*>(kp_smem + (v0 + C::kStages * C::kKV - smem_u32(kp_smem)));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pdl_launch_dependents();  // (the next kernel waits for this one, and this one for the last)
   pdl_wait();
   if (threadIdx.x == 0) {
     for (int i = 0; i < 4; ++i) {
@@ -587,6 +586,7 @@ __global__ void __launch_bounds__(KpCfg<D>::kThreads, 1) kv_prefill_kernel(const
         p_in = i + 1 < n_tiles && mbar_test_wait(&sh->p_full[(i + 1) & 1], uint32_t(((i + 1) >> 1) & 1));
       }
     }
+    pdl_launch_dependents();  // (late: the next kernel's bounded waits must not last as long as this one)
     tc_commit(&sh->drain);  // everything that this thread issued
     mbar_wait_bounded(&sh->drain, 0, p.err, 1u << 20);
   }

@@ -12,10 +12,13 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <ATen/ops/zeros.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <cstdint>
 #include <stdexcept>
 #include <string>
@@ -25,6 +28,7 @@
 namespace {
 
 PyObject* g_error = nullptr;  // binding.W4A8Error
+PyObject* g_cache_names[4];   // attributes of a cache: codes and scales of K and V
 
 struct Refused : std::runtime_error {
   using std::runtime_error::runtime_error;
@@ -80,15 +84,37 @@ void dims(const at::Tensor& t, int64_t n, const char* name, const char* what) {
   if (t.dim() != n) refuse(std::string(name) + " must be " + what);
 }
 
-void* stream_of(PyObject* stream, int dev) {
-  if (stream == Py_None) return c10::cuda::getCurrentCUDAStream(c10::DeviceIndex(dev)).stream();
-  PyObject* v = PyObject_GetAttrString(stream, "cuda_stream");
-  if (!v) refuse("stream must be a CUDA stream");
-  void* s = PyLong_AsVoidPtr(v);
-  Py_DECREF(v);
-  if (PyErr_Occurred()) PyErr_Clear(), refuse("stream must be a CUDA stream");
-  return s;
+// Numbers are read before anything is launched (a refusal leaves Python's own error).
+float number(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) refuse("not a number");
+  return float(v);
 }
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) refuse("not a truth value");
+  return v != 0;
+}
+
+// The stream of a call, made the current one while the call runs: outputs and
+// scratch that the call allocates then belong to it, and are not handed to
+// another tensor before its work is done.
+struct OnStream {
+  c10::cuda::OptionalCUDAStreamGuard guard;
+  void* stream;
+  OnStream(PyObject* o, int dev) {
+    if (o == Py_None) {
+      stream = c10::cuda::getCurrentCUDAStream(c10::DeviceIndex(dev)).stream();
+      return;
+    }
+    PyObject* v = PyObject_GetAttrString(o, "cuda_stream");
+    if (!v) PyErr_Clear(), refuse("stream must be a CUDA stream");
+    stream = PyLong_AsVoidPtr(v);
+    Py_DECREF(v);
+    if (PyErr_Occurred()) PyErr_Clear(), refuse("stream must be a CUDA stream");
+    guard.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream), c10::DeviceIndex(dev)));
+  }
+};
 
 at::Tensor make(at::IntArrayRef shape, at::ScalarType type, int dev) {
   return at::empty(shape, at::TensorOptions().dtype(type).device(at::Device(at::kCUDA, c10::DeviceIndex(dev))));
@@ -115,7 +141,7 @@ at::Tensor out_like(PyObject* given, const at::Tensor& like, int dev, const char
 }
 
 w4a8_rope rope(PyObject* inv_freq, PyObject* interleaved, PyObject* factor, int dev) {
-  w4a8_rope r{nullptr, 0, PyObject_IsTrue(interleaved), float(PyFloat_AsDouble(factor))};
+  w4a8_rope r{nullptr, 0, truth(interleaved), number(factor)};
   if (const at::Tensor* t = optional(inv_freq, "inv_freq")) {
     dims(*t, 1, "inv_freq", "[rot_dim / 2]");
     r.inv_freq = static_cast<const double*>(address(*t, at::kDouble, dev, "inv_freq"));
@@ -125,12 +151,34 @@ w4a8_rope rope(PyObject* inv_freq, PyObject* interleaved, PyObject* factor, int 
   return r;
 }
 
-// A cache: the bytes of its w4a8_kv_cache and its device.
-const w4a8_kv_cache* cache_of(PyObject* desc, PyObject* device, int dev) {
-  if (!PyBytes_Check(desc) || PyBytes_GET_SIZE(desc) != Py_ssize_t(sizeof(w4a8_kv_cache))) refuse("not a cache");
-  const long at = PyLong_AsLong(device);
-  if (at != dev) refuse("the cache is on cuda:" + std::to_string(at) + ", not on the current device cuda:" + std::to_string(dev));
-  return reinterpret_cast<const w4a8_kv_cache*>(PyBytes_AS_STRING(desc));
+// A cache's tensors, as they are at this call.
+w4a8_kv_cache cache_of(PyObject* cache, int dev) {
+  static const char* const names[4] = {"k_codes", "v_codes", "k_scales", "v_scales"};
+  w4a8_kv_cache c{};
+  void* at[4];
+  int64_t shape[4] = {0, 0, 0, 0};
+  for (int i = 0; i < 4; ++i) {
+    PyObject* o = PyObject_GetAttr(cache, g_cache_names[i]);
+    if (!o) PyErr_Clear(), refuse("cache must be a KvCache");
+    const at::Tensor t = THPVariable_Check(o) ? THPVariable_Unpack(o) : at::Tensor();
+    Py_DECREF(o);
+    if (!t.defined()) refuse("cache must be a KvCache");
+    if (i == 0) {
+      dims(t, 4, names[i], "[pages, kv_heads, page, D]");
+      for (int d = 0; d < 4; ++d) shape[d] = t.size(d);
+    }
+    at[i] = address(t, i < 2 ? at::kChar : at::kFloat, dev, names[i], at::IntArrayRef(shape, i < 2 ? 4 : 2));
+  }
+  if (shape[1] > INT32_MAX || shape[2] > INT32_MAX || shape[3] > INT32_MAX) refuse("the cache is too large");
+  c.k_codes = static_cast<int8_t*>(at[0]);
+  c.v_codes = static_cast<int8_t*>(at[1]);
+  c.k_scales = static_cast<float*>(at[2]);
+  c.v_scales = static_cast<float*>(at[3]);
+  c.pages = shape[0];
+  c.kv_heads = int32_t(shape[1]);
+  c.page = int32_t(shape[2]);
+  c.head_dim = int32_t(shape[3]);
+  return c;
 }
 
 w4a8_kv_batch batch_of(PyObject* table, PyObject* q_start, PyObject* kv_len, int64_t tokens, int dev) {
@@ -189,10 +237,11 @@ PyObject* int8_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {  // x, ro
     if (!f32 && x.scalar_type() != at::kBFloat16) refuse("x must be bf16 or fp32");
     const void* xp = address(x, x.scalar_type(), dev, "x");
     dims(x, 2, "x", "[R, K]");
+    const OnStream on(a[2], dev);
     at::Tensor codes = make(x.sizes(), at::kChar, dev), s = make({x.size(0)}, at::kFloat, dev);
-    if (failed("w4a8_int8_quantize", w4a8_int8_quantize(xp, f32, x.size(0), x.size(1), PyObject_IsTrue(a[1]),
+    if (failed("w4a8_int8_quantize", w4a8_int8_quantize(xp, f32, x.size(0), x.size(1), truth(a[1]),
                                                         static_cast<int8_t*>(codes.data_ptr()),
-                                                        static_cast<float*>(s.data_ptr()), stream_of(a[2], dev))))
+                                                        static_cast<float*>(s.data_ptr()), on.stream)))
       return nullptr;
     return Py_BuildValue("NN", THPVariable_Wrap(codes), THPVariable_Wrap(s));
   });
@@ -209,10 +258,11 @@ PyObject* int8_gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {  // x_q, s_x,
     const auto* wp = static_cast<const int8_t*>(address(w, at::kChar, dev, "w_q", {N, K}));
     const auto* sx = static_cast<const float*>(address(tensor(a[1], "s_x"), at::kFloat, dev, "s_x", {M}));
     const auto* sw = static_cast<const float*>(address(tensor(a[3], "s_w"), at::kFloat, dev, "s_w", {N}));
+    const OnStream on(a[5], dev);
     const at::Tensor* given = optional(a[4], "out");
     at::Tensor out = given ? *given : make({M, N}, at::kBFloat16, dev);
     auto* y = static_cast<uint16_t*>(address(out, at::kBFloat16, dev, "out", {M, N}));
-    if (failed("w4a8_int8_gemm", w4a8_int8_gemm(xp, sx, M, wp, sw, N, K, y, stream_of(a[5], dev)))) return nullptr;
+    if (failed("w4a8_int8_gemm", w4a8_int8_gemm(xp, sx, M, wp, sw, N, K, y, on.stream))) return nullptr;
     return THPVariable_Wrap(out);
   });
 }
@@ -227,6 +277,8 @@ PyObject* int8_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {  // x, w_q,
     const auto* xp = static_cast<const uint16_t*>(address(x, at::kBFloat16, dev, "x"));
     const auto* wp = static_cast<const int8_t*>(address(w, at::kChar, dev, "w_q", {N, K}));
     const auto* sw = static_cast<const float*>(address(tensor(a[2], "s_w"), at::kFloat, dev, "s_w", {N}));
+    const bool rotate = truth(a[3]);
+    const OnStream on(a[6], dev);
     const at::Tensor* ws = optional(a[4], "workspace");
     at::Tensor scratch;
     if (!ws) {
@@ -242,8 +294,8 @@ PyObject* int8_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {  // x, w_q,
     at::Tensor out = given ? *given : make({M, N}, at::kBFloat16, dev);
     auto* y = static_cast<uint16_t*>(address(out, at::kBFloat16, dev, "out", {M, N}));
     if (failed("w4a8_int8_linear",
-               w4a8_int8_linear(xp, M, K, PyObject_IsTrue(a[3]), wp, sw, N, y, address(*ws, at::kByte, dev, "workspace"),
-                                size_t(ws->numel()), stream_of(a[6], dev))))
+               w4a8_int8_linear(xp, M, K, rotate, wp, sw, N, y, address(*ws, at::kByte, dev, "workspace"),
+                                size_t(ws->numel()), on.stream)))
       return nullptr;
     return THPVariable_Wrap(out);
   });
@@ -258,6 +310,9 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     dims(*some, 3, q ? "q" : "k", "[tokens, heads, D]");
     const int dev = device_for(*some, q ? "q" : "k");
     const int64_t T = some->size(0), D = some->size(2);
+    if (D > 65536) refuse("heads of " + std::to_string(D) + " values");
+    const OnStream on(a[11], dev);
+    const float eps = number(a[5]);
     w4a8_heads qs = kNone, qo = kNone, ks = kNone, ko = kNone;
     at::Tensor q_out, k_out;
     if (q) {
@@ -273,77 +328,90 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const w4a8_rope r = rope(a[6], a[7], a[8], dev);
     if (failed("w4a8_qk_norm_rope",
                w4a8_qk_norm_rope(&qs, &ks, T, int32_t(D), address<const float>(a[3], at::kFloat, dev, "q_weight", {D}),
-                                 address<const float>(a[4], at::kFloat, dev, "k_weight", {D}), float(PyFloat_AsDouble(a[5])),
-                                 address<const int32_t>(a[2], at::kInt, dev, "positions", {T}), &r, &qo, &ko,
-                                 stream_of(a[11], dev))))
+                                 address<const float>(a[4], at::kFloat, dev, "k_weight", {D}), eps,
+                                 address<const int32_t>(a[2], at::kInt, dev, "positions", {T}), &r, &qo, &ko, on.stream)))
       return nullptr;
     return Py_BuildValue("NN", q ? THPVariable_Wrap(q_out) : Py_NewRef(Py_None), k ? THPVariable_Wrap(k_out) : Py_NewRef(Py_None));
   });
 }
 
-// cache, device, k, v, block_table, q_start, kv_len, q, positions, q_weight, k_weight, eps, inv_freq, interleaved,
-// factor, q_out, stream
+// cache, k, v, block_table, q_start, kv_len, q, positions, q_weight, k_weight, eps, inv_freq, interleaved, factor, q_out,
+// stream
 PyObject* kv_update(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 17, [&]() -> PyObject* {
-    const at::Tensor &k = tensor(a[2], "k"), &v = tensor(a[3], "v");
+  return guarded(n, 16, [&]() -> PyObject* {
+    const at::Tensor &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
     const int dev = device_for(k, "k");
-    const w4a8_kv_cache* cache = cache_of(a[0], a[1], dev);
-    const at::Tensor* q = optional(a[7], "q");
+    const w4a8_kv_cache cache = cache_of(a[0], dev);
+    const at::Tensor* q = optional(a[6], "q");
     dims(k, 3, "k", "[tokens, heads, D]");
-    const int64_t T = k.size(0), D = cache->head_dim;
-    const w4a8_kv_batch batch = batch_of(a[4], a[5], a[6], T, dev);
+    const int64_t T = k.size(0), D = cache.head_dim;
+    const w4a8_kv_batch batch = batch_of(a[3], a[4], a[5], T, dev);
     const w4a8_heads ks = heads(k, dev, "k", T, D), vs = heads(v, dev, "v", T, D);
+    const OnStream on(a[15], dev);
     w4a8_heads qs = kNone, qo = kNone;
     at::Tensor q_out;
     if (q) {
       qs = heads(*q, dev, "q", T, D);
-      q_out = out_like(a[15], *q, dev, "q_out");
+      q_out = out_like(a[14], *q, dev, "q_out");
       qo = heads(q_out, dev, "q_out", T, D);
     }
-    const w4a8_rope r = rope(a[12], a[13], a[14], dev);
+    const w4a8_rope r = rope(a[11], a[12], a[13], dev);
+    const float eps = number(a[10]);
     if (failed("w4a8_kv_update",
-               w4a8_kv_update(cache, &batch, &ks, &vs, &qs, address<const float>(a[9], at::kFloat, dev, "q_weight", {D}),
-                              address<const float>(a[10], at::kFloat, dev, "k_weight", {D}), float(PyFloat_AsDouble(a[11])),
-                              address<const int32_t>(a[8], at::kInt, dev, "positions", {T}), &r, &qo, stream_of(a[16], dev))))
+               w4a8_kv_update(&cache, &batch, &ks, &vs, &qs, address<const float>(a[8], at::kFloat, dev, "q_weight", {D}),
+                              address<const float>(a[9], at::kFloat, dev, "k_weight", {D}), eps,
+                              address<const int32_t>(a[7], at::kInt, dev, "positions", {T}), &r, &qo, on.stream)))
       return nullptr;
     return q ? THPVariable_Wrap(q_out) : Py_NewRef(Py_None);
   });
 }
 
-PyObject* kv_dequant(PyObject*, PyObject* const* a, Py_ssize_t n) {  // cache, device, ids, stream
-  return guarded(n, 4, [&]() -> PyObject* {
-    const at::Tensor& ids = tensor(a[2], "ids");
+PyObject* kv_dequant(PyObject*, PyObject* const* a, Py_ssize_t n) {  // cache, ids, stream
+  return guarded(n, 3, [&]() -> PyObject* {
+    const at::Tensor& ids = tensor(a[1], "ids");
     const int dev = device_for(ids, "ids");
-    const w4a8_kv_cache* cache = cache_of(a[0], a[1], dev);
+    const w4a8_kv_cache cache = cache_of(a[0], dev);
     dims(ids, 1, "ids", "[n]");
     const auto* at = static_cast<const int32_t*>(address(ids, at::kInt, dev, "ids"));
-    const int64_t shape[4] = {ids.size(0), cache->kv_heads, cache->page, cache->head_dim};
+    const int64_t shape[4] = {ids.size(0), cache.kv_heads, cache.page, cache.head_dim};
+    const OnStream on(a[2], dev);
     at::Tensor k = make(shape, at::kBFloat16, dev), v = make(shape, at::kBFloat16, dev);
-    if (failed("w4a8_kv_dequant", w4a8_kv_dequant(cache, at, ids.size(0), static_cast<uint16_t*>(k.data_ptr()),
-                                                  static_cast<uint16_t*>(v.data_ptr()), stream_of(a[3], dev))))
+    if (failed("w4a8_kv_dequant", w4a8_kv_dequant(&cache, at, ids.size(0), static_cast<uint16_t*>(k.data_ptr()),
+                                                  static_cast<uint16_t*>(v.data_ptr()), on.stream)))
       return nullptr;
     return Py_BuildValue("NN", THPVariable_Wrap(k), THPVariable_Wrap(v));
   });
 }
 
-// q, cache, device, block_table, q_start, kv_len, scale, window, workspace, out, stream
+// q, cache, block_table, q_start, kv_len, scale (None: D ** -0.5), window, workspace, out, stream
 PyObject* kv_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 11, [&]() -> PyObject* {
+  return guarded(n, 10, [&]() -> PyObject* {
     const at::Tensor& q = tensor(a[0], "q");
     const int dev = device_for(q, "q");
     dims(q, 3, "q", "[tokens, heads, D]");
-    const w4a8_kv_cache* cache = cache_of(a[1], a[2], dev);
-    const int64_t T = q.size(0), D = cache->head_dim;
+    const w4a8_kv_cache cache = cache_of(a[1], dev);
+    const int64_t T = q.size(0), D = cache.head_dim;
     const w4a8_heads qs = heads(q, dev, "q", T, D);
-    const w4a8_kv_batch batch = batch_of(a[3], a[4], a[5], T, dev);
-    at::Tensor out = out_like(a[9], q, dev, "out");
-    const w4a8_heads os = heads(out, dev, "out", T, D);
-    const at::Tensor& ws = tensor(a[8], "workspace");
-    const long window = PyLong_AsLong(a[7]);
+    const w4a8_kv_batch batch = batch_of(a[2], a[3], a[4], T, dev);
+    const float scale = a[5] == Py_None ? 1.f / std::sqrt(float(D)) : number(a[5]);
+    const long window = PyLong_AsLong(a[6]);
     if (window < 0 || window > INT32_MAX) refuse("window must be a whole number of tokens");
-    if (failed("w4a8_kv_attention",
-               w4a8_kv_attention(&qs, cache, &batch, float(PyFloat_AsDouble(a[6])), int32_t(window), &os,
-                                 address(ws, at::kByte, dev, "workspace"), size_t(ws.numel()), stream_of(a[10], dev))))
+    const OnStream on(a[9], dev);
+    const at::Tensor* ws = optional(a[7], "workspace");
+    at::Tensor scratch;
+    if (!ws) {
+      const size_t need = w4a8_kv_attention_workspace_bytes(T, qs.heads, cache.kv_heads, cache.head_dim);
+      if (need == 0) {
+        failed("w4a8_kv_attention_workspace_bytes", W4A8_ERR_SHAPE);
+        return nullptr;
+      }
+      scratch = at::zeros({int64_t(need)}, at::TensorOptions().dtype(at::kByte).device(at::Device(at::kCUDA, c10::DeviceIndex(dev))));
+      ws = &scratch;
+    }
+    at::Tensor out = out_like(a[8], q, dev, "out");
+    const w4a8_heads os = heads(out, dev, "out", T, D);
+    if (failed("w4a8_kv_attention", w4a8_kv_attention(&qs, &cache, &batch, scale, int32_t(window), &os,
+                                                      address(*ws, at::kByte, dev, "workspace"), size_t(ws->numel()), on.stream)))
       return nullptr;
     return THPVariable_Wrap(out);
   });
@@ -363,4 +431,9 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "w4a8_marshal", nullptr, -1, kMeth
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit_w4a8_marshal() { return PyModule_Create(&kModule); }
+PyMODINIT_FUNC PyInit_w4a8_marshal() {
+  const char* const names[4] = {"k_codes", "v_codes", "k_scales", "v_scales"};
+  for (int i = 0; i < 4; ++i)
+    if (!(g_cache_names[i] = PyUnicode_InternFromString(names[i]))) return nullptr;
+  return PyModule_Create(&kModule);
+}
