@@ -250,9 +250,13 @@ bool ka_shape_ok(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t D) {
 constexpr size_t kKaZeroBytes = 1024;
 static_assert(kKaMaxCtas * 4 <= kKaZeroBytes, "counters fit");
 
-template <int D>
+// Row tiles of 8 where a sequence has that many rows on average (a decode
+// step of up to 8 query heads to a key head), else of 16.
+bool ka_few_rows(int64_t tokens, int64_t batch, int group) { return tokens * group <= 8 * batch; }
+
+template <int D, int NR>
 cudaError_t ka_launch(const KaParams& p, const w4a8_kv_cache* c, int ctas, cudaStream_t st) {
-  using C = KaCfg<D>;
+  using C = KaCfg<D, NR>;
   const int box = std::min(C::TK, int(c->page));
   const auto swizzle = D < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
   const int64_t slots = c->pages * c->kv_heads * c->page;
@@ -274,7 +278,7 @@ cudaError_t ka_launch(const KaParams& p, const w4a8_kv_cache* c, int ctas, cudaS
         e != cudaSuccess)
       return e;
   }
-  return launch_pdl(kv_attention_kernel<D>, dim3(ctas), dim3(C::kThreads), C::kSmem, st, tk, tv, q);
+  return launch_pdl(kv_attention_kernel<D, NR>, dim3(ctas), dim3(C::kThreads), C::kSmem, st, tk, tv, q);
 }
 
 // Shared-memory opt-ins of this file's kernels, once per device.
@@ -291,9 +295,12 @@ bool int8_allow_smem() {
          allow_smem(int8_gemm_kernel<128, 1>, Q8Cfg<128, 1>::kSmem) == cudaSuccess &&
          allow_smem(int8_pair_kernel, kQ2Smem) == cudaSuccess &&
          allow_smem(int8_gemm_kernel<256, 1>, Q8Cfg<256, 1>::kSmem) == cudaSuccess &&
-         allow_smem(kv_attention_kernel<64>, KaCfg<64>::kSmem) == cudaSuccess &&
-         allow_smem(kv_attention_kernel<128>, KaCfg<128>::kSmem) == cudaSuccess &&
-         allow_smem(kv_attention_kernel<256>, KaCfg<256>::kSmem) == cudaSuccess &&
+         allow_smem(kv_attention_kernel<64, 1>, KaCfg<64, 1>::kSmem) == cudaSuccess &&
+         allow_smem(kv_attention_kernel<64, 2>, KaCfg<64, 2>::kSmem) == cudaSuccess &&
+         allow_smem(kv_attention_kernel<128, 1>, KaCfg<128, 1>::kSmem) == cudaSuccess &&
+         allow_smem(kv_attention_kernel<128, 2>, KaCfg<128, 2>::kSmem) == cudaSuccess &&
+         allow_smem(kv_attention_kernel<256, 1>, KaCfg<256, 1>::kSmem) == cudaSuccess &&
+         allow_smem(kv_attention_kernel<256, 2>, KaCfg<256, 2>::kSmem) == cudaSuccess &&
          allow_smem(kv_prefill_kernel<64>, KpCfg<64>::kSmem) == cudaSuccess &&
          allow_smem(kv_prefill_kernel<128>, KpCfg<128>::kSmem) == cudaSuccess &&
          allow_smem(kv_prefill_kernel<256>, KpCfg<256>::kSmem) == cudaSuccess;
@@ -448,7 +455,7 @@ w4a8_status w4a8_kv_dequant(const w4a8_kv_cache* cache, const int32_t* ids, int6
 
 size_t w4a8_kv_attention_workspace_bytes(int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
   if (!ka_shape_ok(tokens, q_heads, kv_heads, head_dim)) return 0;
-  return kKaZeroBytes + size_t(kKaMaxCtas) * 2 * (size_t(kKaRows) * head_dim + 2 * kKaRows) * 4;
+  return kKaZeroBytes + size_t(kKaMaxCtas) * 2 * (size_t(kKaMaxRows) * head_dim + 2 * kKaMaxRows) * 4;
 }
 
 w4a8_status w4a8_kv_attention(const w4a8_heads* q, const w4a8_kv_cache* cache, const w4a8_kv_batch* batch, float scale,
@@ -481,9 +488,15 @@ w4a8_status w4a8_kv_attention(const w4a8_heads* q, const w4a8_kv_cache* cache, c
   p.err = d->err;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int ctas = std::min(d->sms, kKaMaxCtas);
-  return status_of(D == 64    ? ka_launch<64>(p, cache, ctas, s)
-                   : D == 128 ? ka_launch<128>(p, cache, ctas, s)
-                              : ka_launch<256>(p, cache, ctas, s));
+  const bool few = ka_few_rows(batch->tokens, batch->batch, p.group);
+  switch (D + few) {
+    case 64: return status_of(ka_launch<64, 2>(p, cache, ctas, s));
+    case 65: return status_of(ka_launch<64, 1>(p, cache, ctas, s));
+    case 128: return status_of(ka_launch<128, 2>(p, cache, ctas, s));
+    case 129: return status_of(ka_launch<128, 1>(p, cache, ctas, s));
+    case 256: return status_of(ka_launch<256, 2>(p, cache, ctas, s));
+    default: return status_of(ka_launch<256, 1>(p, cache, ctas, s));
+  }
 }
 
 }  // extern "C"

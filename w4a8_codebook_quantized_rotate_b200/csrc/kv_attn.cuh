@@ -18,10 +18,18 @@
 //
 // The cache is read once, so at decode sizes its bytes bound the kernel
 // (6.5 TB/s: 23 bytes a clock and SM, against which the fp16 expansion of
-// the codes costs about one instruction per byte and 32 lanes).  A row tile
-// is 16 rows, the query heads of one key head (and neighbouring new tokens,
-// if the group is smaller); work is a list of items of a TK-key tile per
-// warp,
+// the codes costs about one instruction per byte and 32 lanes).  The codes
+// are the first operand of both products (16 keys, or 16 columns of V, to an
+// MMA) and the rows the second, so a row tile is one block of 8 rows, the
+// query heads of a key head in a decode step, or two (16 rows: larger groups,
+// or several new tokens, whose expansions are then shared; the rule is
+// ka_few_rows).  Rows as the first operand, always 16, took 217 / 70.6 us
+// where 8 take 179 / 56.7 (48 sequences of up to 16384 keys, 32/8 heads of
+// 128 / one of 131072, 24/4 heads of 256): twice the MMAs and scores, half of
+// them for rows that are not there.  The scores' fragment is transposed in
+// registers between the products.
+//
+// Work is a list of items of a TK-key tile per warp,
 // [sequence][key head][row tile][item], of which every CTA takes an equal
 // contiguous share (one CTA per SM), so ragged batches and single long
 // contexts fill the GPU alike.  Each warp keeps its own running maximum, sum
@@ -43,6 +51,9 @@
 // ldmatrix.trans on code pairs, whose even and odd codes make two output
 // tiles.  Tokens of an 8-token group are taken in the order tau, which keeps
 // the swizzled K reads free of bank conflicts.
+//
+// Eight warps of three stages: twelve of two hide no more latency (220 us
+// for the batch above, at 216, both with rows as the first operand).
 #pragma once
 
 #include <cuda.h>
@@ -55,31 +66,33 @@
 namespace w4a8 {
 
 constexpr float kKvLeastScale = 0x1p-80f;  // V scales below count as 0 (in the sum of p, as this)
-constexpr int kKaRows = 16;
+constexpr int kKaMaxRows = 16;                   // rows of a tile: 8 or 16
 constexpr int kKaTileBytes = 4096;               // one warp's K (or V) tile
 constexpr int kKaMaxCtas = 160;
 
-template <int D>
+// NR: blocks of 8 rows (1 or 2) in a row tile.
+template <int D, int NR>
 struct KaCfg {
   static constexpr int TK = kKaTileBytes / D;  // keys of a warp's tile: 64, 32, 16
   static constexpr int KG = TK / 16;           // groups of 16 keys
-  // 12 warps with 168 registers hide latencies better than 8 with 250 (the kernel is bound by its dependent
-  // instructions, not by memory); heads of 256 need the registers for their accumulator.
+  static constexpr int R = 8 * NR;
   static constexpr int kWarps = 8;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kStages = 3;
   static constexpr int kItem = kWarps * TK;  // keys of an item
   static constexpr int kSteps = D / 16;
-  static constexpr bool kQRegs = D <= 128;     // q fragments in registers
+  static constexpr bool kQRegs = D * NR <= 256;  // q fragments in registers
   static constexpr int kBatch = 32 / KG;       // tiles whose page ids a warp holds
   static constexpr uint32_t kRowBytes = D < 128 ? D : 128;  // bytes of a row in a TMA box
   static constexpr int kColBlocks = D / int(kRowBytes);
   static constexpr uint32_t kRing = kWarps * kStages * 2 * kKaTileBytes;
-  static constexpr uint32_t kJoin = kWarps * kKaRows * 32 * 4;  // 32 columns of every warp; the CTAs' weights
-  static_assert(kKaRows * kKaMaxCtas * 4 <= kJoin, "weights of a row tile's CTAs");
-  static constexpr uint32_t kQ = kKaRows * D * 2;
+  // joining the warps: TPR threads a row, two columns each; the rows of the buffer are 4 words apart in banks
+  static constexpr int TPR = kThreads / R, kJoinCols = 2 * TPR, kJoinStride = kJoinCols + 4;
+  static constexpr uint32_t kJoin = kWarps * R * kJoinStride * 4;  // kJoinCols columns of every warp; the CTAs' weights
+  static_assert(R * kKaMaxCtas * 4 <= kJoin, "weights of a row tile's CTAs");
+  static constexpr uint32_t kQ = R * D * 2;
   static constexpr size_t kSmem = 1024 + kRing + kJoin + kQ + 4096;
-  static constexpr int kSlotFloats = kKaRows * D + 2 * kKaRows;
+  static constexpr int kSlotFloats = R * D + 2 * R;
 };
 
 struct KaParams {
@@ -96,13 +109,13 @@ struct KaParams {
   unsigned* err;
 };
 
-constexpr int kKaMaxWarps = 12, kKaMaxStages = 3;
+constexpr int kKaMaxWarps = 8, kKaMaxStages = 3;
 struct KaShared {
   uint64_t full[kKaMaxWarps][kKaMaxStages];
   float scales[kKaMaxWarps][kKaMaxStages][3][4];  // ks, log2(vs), 1 / vs of each group of 16 keys
-  float warp_z[kKaMaxWarps][kKaRows];
-  float warp_l[kKaMaxWarps][kKaRows];
-  float row_factor[kKaRows];
+  float warp_z[kKaMaxWarps][kKaMaxRows];
+  float warp_l[kKaMaxWarps][kKaMaxRows];
+  float row_factor[kKaMaxRows];
   long long base;   // first item of sequence b0
   long long total;  // items of the batch
   int b0, small_only;
@@ -149,12 +162,13 @@ __device__ __forceinline__ bool kp_takes_big(const KaParams& p) {  // whole warp
 
 // Row tiles of a sequence, and items of each (the same for all of them: a
 // tile skips the keys outside its own range).
-template <int D>
+template <int D, int NR>
 __device__ __forceinline__ void ka_counts(const KvSeq& s, const KaParams& p, bool small_only, int& tiles, int& items) {
   const KvRange r = kv_range(s, 0, s.q_len - 1, p.window);
-  const int lo = r.lo & ~(KaCfg<D>::TK - 1);
-  tiles = (s.q_len * p.group + kKaRows - 1) / kKaRows;
-  items = s.q_len == 0 ? 0 : (s.kv_len - lo + KaCfg<D>::kItem - 1) / KaCfg<D>::kItem;
+  using C = KaCfg<D, NR>;
+  const int lo = r.lo & ~(C::TK - 1);
+  tiles = (s.q_len * p.group + C::R - 1) / C::R;
+  items = s.q_len == 0 ? 0 : (s.kv_len - lo + C::kItem - 1) / C::kItem;
   if (small_only && s.q_len * p.group >= kKpMinRows) tiles = items = 0;
 }
 
@@ -168,15 +182,16 @@ struct KaSeg {
   KvRange range;
 };
 
-template <int D>
+template <int D, int NR>
 struct KaWalk {
+  using C = KaCfg<D, NR>;
   long long pos, end, base;
   int b, tiles, items;
   bool small_only;
   KvSeq s;
   __device__ __forceinline__ void load(const KaParams& p) {
     s = kv_load_seq(p.batch, b, p.cache.page_shift);
-    ka_counts<D>(s, p, small_only, tiles, items);
+    ka_counts<D, NR>(s, p, small_only, tiles, items);
   }
   __device__ __forceinline__ bool next(const KaParams& p, KaSeg& g) {
     if (pos >= end) return false;
@@ -196,9 +211,9 @@ struct KaWalk {
     g.start = base + unit * items;
     const long long left = end - pos;
     g.item1 = left < items - g.item0 ? g.item0 + int(left) : items;
-    g.key0 = kv_range(s, 0, s.q_len - 1, p.window).lo & ~(KaCfg<D>::TK - 1);
-    const int j0 = g.tile * kKaRows / p.group;
-    const int last_row = min(s.q_len * p.group, (g.tile + 1) * kKaRows) - 1;
+    g.key0 = kv_range(s, 0, s.q_len - 1, p.window).lo & ~(C::TK - 1);
+    const int j0 = g.tile * C::R / p.group;
+    const int last_row = min(s.q_len * p.group, (g.tile + 1) * C::R) - 1;
     g.range = kv_range(s, j0, last_row / p.group, p.window);
     pos += g.item1 - g.item0;
     return true;
@@ -236,14 +251,21 @@ __device__ __forceinline__ uint32_t ka_tau(uint32_t i) {
 template <int D>
 __device__ __forceinline__ uint32_t ka_at(uint32_t r, uint32_t c) {
   if constexpr (D < 128) return r * 64u + ((c ^ ((r >> 1) & 3u)) << 4);
-  return (c >> 3) * uint32_t(KaCfg<D>::TK * 128) + r * 128u + (((c & 7u) ^ (r & 7u)) << 4);
+  return (c >> 3) * uint32_t(kKaTileBytes / D * 128) + r * 128u + (((c & 7u) ^ (r & 7u)) << 4);
 }
 
-template <int D>
-__global__ void __launch_bounds__(KaCfg<D>::kThreads, 1)
+// Transpose of an 8 x 8 matrix of 16-bit values held as a fragment (row lane / 4, columns 2 (lane % 4) and the next).
+__device__ __forceinline__ uint32_t ka_transpose(uint32_t v) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+  return d;
+}
+
+template <int D, int NR>
+__global__ void __launch_bounds__(KaCfg<D, NR>::kThreads, 1)
     kv_attention_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                         const KaParams p) {
-  using C = KaCfg<D>;
+  using C = KaCfg<D, NR>;
   extern __shared__ __align__(1024) uint8_t ka_smem[];
   const uint32_t ring = (smem_u32(ka_smem) + 1023u) & ~1023u;
   uint8_t* after = ka_smem + (ring - smem_u32(ka_smem)) + C::kRing;
@@ -271,7 +293,7 @@ __global__ void __launch_bounds__(KaCfg<D>::kThreads, 1)
       if (b0 + lane < p.batch.batch) {
         const KvSeq s = kv_load_seq(p.batch, b0 + lane, p.cache.page_shift);
         if (s.bad) record_error(p.err, kErrInput);
-        ka_counts<D>(s, p, small_only, tiles, items);
+        ka_counts<D, NR>(s, p, small_only, tiles, items);
       }
       total += (long long)p.cache.kv_heads * tiles * items;
     }
@@ -284,7 +306,7 @@ __global__ void __launch_bounds__(KaCfg<D>::kThreads, 1)
     for (int b0 = 0; b0 < p.batch.batch && at < 0 && i0 < total; b0 += 32) {
       int tiles = 0, items = 0;
       if (b0 + lane < p.batch.batch)
-        ka_counts<D>(kv_load_seq(p.batch, b0 + lane, p.cache.page_shift), p, small_only, tiles, items);
+        ka_counts<D, NR>(kv_load_seq(p.batch, b0 + lane, p.cache.page_shift), p, small_only, tiles, items);
       const long long own = (long long)p.cache.kv_heads * tiles * items;
       long long sum = own;
 #pragma unroll
@@ -312,7 +334,7 @@ __global__ void __launch_bounds__(KaCfg<D>::kThreads, 1)
   const long long ctas = total < gridDim.x ? total : gridDim.x;
   if (int(blockIdx.x) >= ctas) return;
   const long long i0 = ka_first_item(blockIdx.x, total, ctas);
-  KaWalk<D> walk;
+  KaWalk<D, NR> walk;
   walk.pos = i0;
   walk.end = ka_first_item(blockIdx.x + 1, total, ctas);
   walk.base = sh->base;
@@ -403,9 +425,9 @@ __global__ void __launch_bounds__(KaCfg<D>::kThreads, 1)
     const int c_first_item = nfirst, c_end_item = fend;
     // ---- q rows of the tile into fragments: half a warp per row
     const int rows = seg.s.q_len * p.group;
-    if (warp < kKaRows / 2) {
+    if (warp < C::R / 2) {
       const int r = 2 * warp + (lane >> 4), l16 = lane & 15;
-      const int row = seg.tile * kKaRows + r;
+      const int row = seg.tile * C::R + r;
       float v[D / 16];
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) v[i] = 0.f;
@@ -435,68 +457,88 @@ __global__ void __launch_bounds__(KaCfg<D>::kThreads, 1)
       for (int i = 0; i < D / 16; i += 2) {
         const int d = l16 * (D / 16) + i;
         const int step = (d >> 6) * 4 + ((d >> 2) & 3), ln = (r & 7) * 4 + ((d >> 4) & 3);
-        const int reg = ((d & 2) ? 2 : 0) + (r >> 3);
+        const int reg = ((d & 2) ? NR : 0) + (r >> 3);
         const __half2 h = __floats2half2_rn(v[i] * up, v[i + 1] * up);
-        qf[(step * 32 + ln) * 4 + reg] = *reinterpret_cast<const uint32_t*>(&h);
+        qf[(step * 32 + ln) * (2 * NR) + reg] = *reinterpret_cast<const uint32_t*>(&h);
       }
     }
     __syncthreads();
-    uint32_t qr[C::kQRegs ? C::kSteps : 1][4];
+    auto q_frag = [&](int step, uint32_t (&f)[2 * NR]) {  // b0 of every row block, then b1
+      if constexpr (NR == 2) {
+        const uint4 v = *reinterpret_cast<const uint4*>(qf + (step * 32 + lane) * 4);
+        f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+      } else {
+        const uint2 v = *reinterpret_cast<const uint2*>(qf + (step * 32 + lane) * 2);
+        f[0] = v.x, f[1] = v.y;
+      }
+    };
+    uint32_t qr[C::kQRegs ? C::kSteps : 1][2 * NR];
     if constexpr (C::kQRegs) {
 #pragma unroll
-      for (int s = 0; s < C::kSteps; ++s) {
-        const uint4 f = *reinterpret_cast<const uint4*>(qf + (s * 32 + lane) * 4);
-        qr[s][0] = f.x, qr[s][1] = f.y, qr[s][2] = f.z, qr[s][3] = f.w;
-      }
+      for (int s = 0; s < C::kSteps; ++s) q_frag(s, qr[s]);
     }
-    const float f0 = sh->row_factor[g], f1 = sh->row_factor[g + 8];
-    int lim[2], low[2];  // the last key a row sees, and the first
+    // this lane's rows: 8 n + 2 t + e
+    float f[NR][2];
+    int lim[NR][2], low[NR][2];  // the last key a row sees, and the first
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int row = min(seg.tile * kKaRows + g + 8 * i, rows - 1);
-      lim[i] = seg.s.kv_len - seg.s.q_len + row / p.group;
-      low[i] = p.window > 0 ? lim[i] - p.window + 1 : 0;
-    }
-    const int lim_min = seg.s.kv_len - seg.s.q_len + seg.tile * kKaRows / p.group;
+    for (int n = 0; n < NR; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * n + 2 * t + e, row = min(seg.tile * C::R + r, rows - 1);
+        f[n][e] = sh->row_factor[r];
+        lim[n][e] = seg.s.kv_len - seg.s.q_len + row / p.group;
+        low[n][e] = p.window > 0 ? lim[n][e] - p.window + 1 : 0;
+      }
+    const int lim_min = seg.s.kv_len - seg.s.q_len + seg.tile * C::R / p.group;
     const int low_max = p.window > 0 ? seg.range.hi - p.window : 0;
 
-    float o[D / 8][4];
+    float o[D / 16][NR][4];  // (even d, row e = 0), (even, 1), (odd, 0), (odd, 1) of 16 columns
+    float z[NR][2], l[NR][2];
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    float z0 = -INFINITY, z1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    for (int n = 0; n < NR; ++n) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
+      z[n][0] = z[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
+    }
 
     for (int item = c_first_item; item < c_end_item; ++item) {
       const int key = seg.key0 + (item * C::kWarps + warp) * C::TK;
       if (ok) ok = __all_sync(0xffffffffu, ka_wait(&sh->full[warp][stage], phase, sh, p.err));
       if (!ok) break;
       const uint32_t kt = ring + uint32_t((warp * C::kStages + stage) * 2) * kKaTileBytes, vt = kt + kKaTileBytes;
-      // ---- scores
-      float s[C::TK / 8][4];
+      // ---- scores: keys 16 kb + tau(g) and 16 kb + 8 + tau(g) of every row
+      float s[C::KG][NR][4];
 #pragma unroll
-      for (int j = 0; j < C::TK / 8; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+      for (int kb = 0; kb < C::KG; ++kb)
+#pragma unroll
+        for (int n = 0; n < NR; ++n) s[kb][n][0] = s[kb][n][1] = s[kb][n][2] = s[kb][n][3] = 0.f;
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {
-        uint32_t qs[4][4];
+        uint32_t qs[4][2 * NR];
 #pragma unroll
         for (int st = 0; st < 4; ++st) {
           if constexpr (C::kQRegs) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) qs[st][i] = qr[4 * c + st][i];
+            for (int i = 0; i < 2 * NR; ++i) qs[st][i] = qr[4 * c + st][i];
           } else {
-            const uint4 f = *reinterpret_cast<const uint4*>(qf + ((4 * c + st) * 32 + lane) * 4);
-            qs[st][0] = f.x, qs[st][1] = f.y, qs[st][2] = f.z, qs[st][3] = f.w;
+            q_frag(4 * c + st, qs[st]);
           }
         }
 #pragma unroll
-        for (int j = 0; j < C::TK / 8; ++j) {
-          uint32_t w[4];
-          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                       : "r"(kt + ka_at<D>(uint32_t(8 * j) + ka_tau<D>(g), uint32_t(4 * c + t))));
+        for (int kb = 0; kb < C::KG; ++kb) {
+          uint32_t w[2][4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[h][0]), "=r"(w[h][1]), "=r"(w[h][2]), "=r"(w[h][3])
+                         : "r"(kt + ka_at<D>(uint32_t(16 * kb + 8 * h) + ka_tau<D>(g), uint32_t(4 * c + t))));
 #pragma unroll
           for (int st = 0; st < 4; ++st) {
-            const uint32_t x = w[st] ^ 0x80808080u;
-            ka_mma(s[j], qs[st], ka_codes(x, 0x4140u), ka_codes(x, 0x4342u));
+            const uint32_t x = w[0][st] ^ 0x80808080u, y = w[1][st] ^ 0x80808080u;
+            const uint32_t a[4] = {ka_codes(x, 0x4140u), ka_codes(y, 0x4140u), ka_codes(x, 0x4342u), ka_codes(y, 0x4342u)};
+#pragma unroll
+            for (int n = 0; n < NR; ++n) ka_mma(s[kb][n], a, qs[st][n], qs[st][NR + n]);
           }
         }
       }
@@ -507,71 +549,74 @@ __global__ void __launch_bounds__(KaCfg<D>::kThreads, 1)
       const bool edge = key + C::TK - 1 > lim_min || key < low_max;
       if (edge) {
 #pragma unroll
-        for (int j = 0; j < C::TK / 8; ++j) {
-          const int ka = key + 8 * j + int(ka_tau<D>(2 * t)), kc = key + 8 * j + int(ka_tau<D>(2 * t + 1));
-          if (ka > lim[0] || ka < low[0]) s[j][0] = -INFINITY;
-          if (kc > lim[0] || kc < low[0]) s[j][1] = -INFINITY;
-          if (ka > lim[1] || ka < low[1]) s[j][2] = -INFINITY;
-          if (kc > lim[1] || kc < low[1]) s[j][3] = -INFINITY;
+        for (int kb = 0; kb < C::KG; ++kb)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int at = key + 16 * kb + 8 * h + int(ka_tau<D>(g));
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (at > lim[n][e] || at < low[n][e]) s[kb][n][2 * h + e] = -INFINITY;
+          }
+      }
+      float x[NR][2];
+      bool more_z = false;
+#pragma unroll
+      for (int n = 0; n < NR; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          x[n][e] = -INFINITY;
+#pragma unroll
+          for (int kb = 0; kb < C::KG; ++kb)
+            // (fmaxf drops the NaN of a wholly masked group under a K scale of 0)
+            x[n][e] = fmaxf(x[n][e], fmaf(fmaxf(s[kb][n][e], s[kb][n][2 + e]), f[n][e] * ks[kb], lv[kb] - 15.f));
+          more_z |= x[n][e] > z[n][e];
         }
-      }
-      float x0 = -INFINITY, x1 = -INFINITY;
+      if (__any_sync(0xffffffffu, more_z)) {  // (a row's keys are spread over 8 lanes)
 #pragma unroll
-      for (int kb = 0; kb < C::KG; ++kb) {
-        const float g0 = fmaxf(fmaxf(s[2 * kb][0], s[2 * kb][1]), fmaxf(s[2 * kb + 1][0], s[2 * kb + 1][1]));
-        const float g1 = fmaxf(fmaxf(s[2 * kb][2], s[2 * kb][3]), fmaxf(s[2 * kb + 1][2], s[2 * kb + 1][3]));
-        const float k = ks[kb], off = lv[kb] - 15.f;
-        // (fmaxf drops the NaN of a wholly masked group under a K scale of 0)
-        x0 = fmaxf(x0, fmaf(g0, f0 * k, off));
-        x1 = fmaxf(x1, fmaf(g1, f1 * k, off));
-      }
+        for (int n = 0; n < NR; ++n)
 #pragma unroll
-      for (int off = 1; off < 4; off <<= 1) {
-        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, off));
-        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, off));
-      }
-      if (__any_sync(0xffffffffu, x0 > z0 || x1 > z1)) {
-        const float n0 = fmaxf(z0, x0), n1 = fmaxf(z1, x1);
-        const float r0 = z0 == -INFINITY ? 0.f : ex2(z0 - n0), r1 = z1 == -INFINITY ? 0.f : ex2(z1 - n1);
-        l0 *= r0;
-        l1 *= r1;
+          for (int e = 0; e < 2; ++e) {
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          o[i][0] *= r0;
-          o[i][1] *= r0;
-          o[i][2] *= r1;
-          o[i][3] *= r1;
-        }
-        z0 = n0;
-        z1 = n1;
+            for (int off = 4; off < 32; off <<= 1) x[n][e] = fmaxf(x[n][e], __shfl_xor_sync(0xffffffffu, x[n][e], off));
+            const float nz = fmaxf(z[n][e], x[n][e]);
+            const float grow = z[n][e] == -INFINITY ? 0.f : ex2(z[n][e] - nz);
+            l[n][e] *= grow;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              o[i][n][e] *= grow;
+              o[i][n][2 + e] *= grow;
+            }
+            z[n][e] = nz;
+          }
       }
-      const float u0 = z0 == -INFINITY ? 0.f : z0, u1 = z1 == -INFINITY ? 0.f : z1;
       // ---- P', the sum of p, and the product with V
 #pragma unroll
       for (int kb = 0; kb < C::KG; ++kb) {
-        const float k0 = f0 * ks[kb], k1 = f1 * ks[kb], o0 = lv[kb] - u0, o1 = lv[kb] - u1, w = iv[kb];
-        uint32_t a[4];
-        float s0 = 0.f, s1 = 0.f;
+        const float w = iv[kb];
+        uint32_t b[NR][2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float* x = s[2 * kb + i];
-          float p0 = ex2(fmaf(x[0], k0, o0)), p1 = ex2(fmaf(x[1], k0, o0));
-          float p2 = ex2(fmaf(x[2], k1, o1)), p3 = ex2(fmaf(x[3], k1, o1));
-          if (edge) {  // (a masked score times a K scale of 0 is no zero)
-            p0 = x[0] == -INFINITY ? 0.f : p0;
-            p1 = x[1] == -INFINITY ? 0.f : p1;
-            p2 = x[2] == -INFINITY ? 0.f : p2;
-            p3 = x[3] == -INFINITY ? 0.f : p3;
+        for (int n = 0; n < NR; ++n) {
+          float pr[4];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float kf = f[n][e] * ks[kb], off = lv[kb] - (z[n][e] == -INFINITY ? 0.f : z[n][e]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float sc = s[kb][n][2 * h + e];
+              pr[2 * h + e] = ex2(fmaf(sc, kf, off));
+              if (edge && sc == -INFINITY) pr[2 * h + e] = 0.f;  // (a masked score times a K scale of 0 is no zero)
+            }
+            l[n][e] = fmaf(pr[e] + pr[2 + e], w, l[n][e]);
           }
-          s0 += p0 + p1;
-          s1 += p2 + p3;
-          const __half2 h0 = __floats2half2_rn(p0, p1), h1 = __floats2half2_rn(p2, p3);
-          a[2 * i] = *reinterpret_cast<const uint32_t*>(&h0);
-          a[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const __half2 hh = __floats2half2_rn(pr[2 * h], pr[2 * h + 1]);
+            b[n][h] = ka_transpose(*reinterpret_cast<const uint32_t*>(&hh));
+            if (w >= 1.f / kKvLeastScale) b[n][h] = 0u;  // a page without a V scale: its values are zeros
+          }
         }
-        l0 = fmaf(s0, w, l0);
-        l1 = fmaf(s1, w, l1);
-        if (w >= 1.f / kKvLeastScale) a[0] = a[1] = a[2] = a[3] = 0u;  // a page without a V scale: its values are zeros
         const uint32_t vrow = uint32_t(16 * kb + ((lane >> 3) & 1) * 8) + ka_tau<D>(lane & 7);
 #pragma unroll
         for (int c2 = 0; c2 < D / 32; ++c2) {
@@ -581,10 +626,13 @@ __global__ void __launch_bounds__(KaCfg<D>::kThreads, 1)
                        : "r"(vt + ka_at<D>(vrow, uint32_t(2 * c2 + (lane >> 4)))));
 #pragma unroll
           for (int i = 0; i < 4; ++i) r[i] ^= 0x80808080u;
-          ka_mma(o[4 * c2], a, ka_codes(r[0], 0x4240u), ka_codes(r[1], 0x4240u));
-          ka_mma(o[4 * c2 + 1], a, ka_codes(r[0], 0x4341u), ka_codes(r[1], 0x4341u));
-          ka_mma(o[4 * c2 + 2], a, ka_codes(r[2], 0x4240u), ka_codes(r[3], 0x4240u));
-          ka_mma(o[4 * c2 + 3], a, ka_codes(r[2], 0x4341u), ka_codes(r[3], 0x4341u));
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const uint32_t a[4] = {ka_codes(r[2 * hf], 0x4240u), ka_codes(r[2 * hf], 0x4341u),
+                                   ka_codes(r[2 * hf + 1], 0x4240u), ka_codes(r[2 * hf + 1], 0x4341u)};
+#pragma unroll
+            for (int n = 0; n < NR; ++n) ka_mma(o[2 * c2 + hf][n], a, b[n][0], b[n][1]);
+          }
         }
       }
       __syncwarp();  // every lane has used the tile: its stage takes the next one
@@ -597,27 +645,29 @@ __global__ void __launch_bounds__(KaCfg<D>::kThreads, 1)
     if (!more) pdl_launch_dependents();  // (late: the next kernel's bounded waits must not last as long as this one)
     if (more && ok) start(nxt);
 #pragma unroll
-    for (int off = 1; off < 4; off <<= 1) {
-      l0 += __shfl_xor_sync(0xffffffffu, l0, off);
-      l1 += __shfl_xor_sync(0xffffffffu, l1, off);
-    }
-    if (t == 0) {
-      sh->warp_z[warp][g] = z0;
-      sh->warp_z[warp][g + 8] = z1;
-      sh->warp_l[warp][g] = l0;
-      sh->warp_l[warp][g + 8] = l1;
-    }
-    __syncthreads();
-    float top0 = -INFINITY, top1 = -INFINITY;
+    for (int n = 0; n < NR; ++n)
 #pragma unroll
-    for (int w = 0; w < C::kWarps; ++w) {
-      top0 = fmaxf(top0, sh->warp_z[w][g]);
-      top1 = fmaxf(top1, sh->warp_z[w][g + 8]);
-    }
-    const float w0 = z0 == -INFINITY ? 0.f : ex2(z0 - top0), w1 = z1 == -INFINITY ? 0.f : ex2(z1 - top1);
-    // this thread's place in the joined tile: row jr, columns 2 jc, 2 jc + 1 of each 32 (threads past 256 have none)
-    const int jr = (tid >> 4) & 15, jc = tid & 15;
-    const bool joins = tid < 256;
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], off);
+        if (g == 0) {
+          sh->warp_z[warp][8 * n + 2 * t + e] = z[n][e];
+          sh->warp_l[warp][8 * n + 2 * t + e] = l[n][e];
+        }
+      }
+    __syncthreads();
+    float wt[NR][2];  // of this warp's sums
+#pragma unroll
+    for (int n = 0; n < NR; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < C::kWarps; ++w) top = fmaxf(top, sh->warp_z[w][8 * n + 2 * t + e]);
+        wt[n][e] = z[n][e] == -INFINITY ? 0.f : ex2(z[n][e] - top);
+      }
+    // this thread's place in the joined tile: row jr, columns 2 jc, 2 jc + 1 of each kJoinCols
+    const int jr = tid / C::TPR, jc = tid % C::TPR;
     float jz = -INFINITY, jl = 0.f;
 #pragma unroll
     for (int w = 0; w < C::kWarps; ++w) jz = fmaxf(jz, sh->warp_z[w][jr]);
@@ -627,53 +677,54 @@ __global__ void __launch_bounds__(KaCfg<D>::kThreads, 1)
     const bool whole = seg.item0 == 0 && seg.item1 == seg.items;
     const int slot = int(blockIdx.x) * 2 + (i0 >= seg.start ? 0 : 1);
     float* part = p.part + (size_t)slot * C::kSlotFloats;
-    const int row = seg.tile * kKaRows + jr;
+    const int row = seg.tile * C::R + jr;
     const int oj = row / p.group, oh = seg.head * p.group + row - oj * p.group;
     uint16_t* dst = p.out.data + (long long)(seg.s.start + oj) * p.out.token + oh * p.out.head;
     const float norm = jl > 0.f ? __fdiv_rn(1.f, jl) : 0.f;
+    constexpr int kCols = C::kJoinCols < D ? C::kJoinCols : D;
 #pragma unroll
-    for (int c2 = 0; c2 < D / 32; ++c2) {
-      float* mine = join + warp * (kKaRows * 32);
+    for (int c0 = 0; c0 < D; c0 += kCols) {
+      float* mine = join + warp * (C::R * C::kJoinStride);
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const float(&e)[4] = o[4 * c2 + 2 * hf];
-        const float(&d)[4] = o[4 * c2 + 2 * hf + 1];
-        *reinterpret_cast<float4*>(mine + g * 32 + 16 * hf + 4 * t) =
-            make_float4(e[0] * w0, d[0] * w0, e[1] * w0, d[1] * w0);
-        *reinterpret_cast<float4*>(mine + (g + 8) * 32 + 16 * hf + 4 * t) =
-            make_float4(e[2] * w1, d[2] * w1, e[3] * w1, d[3] * w1);
-      }
+      for (int i = 0; i < kCols / 16; ++i)
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float(&v)[4] = o[c0 / 16 + i][n];
+            *reinterpret_cast<float2*>(mine + (8 * n + 2 * t + e) * C::kJoinStride + 16 * i + 2 * g) =
+                make_float2(v[e] * wt[n][e], v[2 + e] * wt[n][e]);
+          }
       __syncthreads();
       float x = 0.f, y = 0.f;
 #pragma unroll
       for (int w = 0; w < C::kWarps; ++w) {
-        const float2 v = *reinterpret_cast<const float2*>(join + w * (kKaRows * 32) + jr * 32 + 2 * jc);
+        const float2 v = *reinterpret_cast<const float2*>(join + (w * C::R + jr) * C::kJoinStride + 2 * jc);
         x += v.x;
         y += v.y;
       }
-      if (!joins) {
-      } else if (!whole) {
-        *reinterpret_cast<float2*>(part + jr * D + 32 * c2 + 2 * jc) = make_float2(x, y);
+      if (!whole) {
+        *reinterpret_cast<float2*>(part + jr * D + c0 + 2 * jc) = make_float2(x, y);
       } else if (row < rows && ok) {
         const __nv_bfloat162 b = __floats2bfloat162_rn(x * norm, y * norm);
-        *reinterpret_cast<__nv_bfloat162*>(dst + 32 * c2 + 2 * jc) = b;
+        *reinterpret_cast<__nv_bfloat162*>(dst + c0 + 2 * jc) = b;
       }
       __syncthreads();
     }
     if (!whole) {
-      if (joins && jc == 0) {
-        part[kKaRows * D + jr] = jz;
-        part[kKaRows * D + kKaRows + jr] = jl;
+      if (jc == 0) {
+        part[C::R * D + jr] = jz;
+        part[C::R * D + C::R + jr] = jl;
       }
       const int c_first = ka_item_cta(seg.start, total, ctas), c_last = ka_item_cta(seg.start + seg.items - 1, total, ctas);
       __threadfence();
       __syncthreads();
       if (tid == 0) sh->last = atomicAdd(p.counters + c_first, 1u) == unsigned(c_last - c_first);
       __syncthreads();
-      if (sh->last && joins) {
+      if (sh->last) {
         __threadfence();
         // Slot of CTA c: its first row tile's, but for the CTA in which the tile starts behind another one.  A row's
-        // 16 threads take the CTAs' maxima and sums 16 at a time, and leave the CTAs' weights in shared memory; the
+        // threads take the CTAs' maxima and sums, one each at a time, and leave the CTAs' weights in shared memory; the
         // accumulators then come in eight at a time (one at a time waits a round trip to L2 for each).
         const int n_cta = c_last - c_first + 1;
         const float* slot0 = p.part + (size_t)(c_first * 2 + (ka_first_item(c_first, total, ctas) >= seg.start ? 0 : 1)) * C::kSlotFloats;
@@ -682,56 +733,63 @@ __global__ void __launch_bounds__(KaCfg<D>::kThreads, 1)
         };
         float* weight = join + jr * kKaMaxCtas;
         float top = -INFINITY, sum = 0.f;
-        for (int c = jc; c < n_cta; c += 16) {
-          const float* m = slot_of(c) + kKaRows * D + jr;
-          const float cz = __ldcg(m), cl = __ldcg(m + kKaRows);
+        for (int c = jc; c < n_cta; c += C::TPR) {
+          const float* m = slot_of(c) + C::R * D + jr;
+          const float cz = __ldcg(m), cl = __ldcg(m + C::R);
           const float nt = fmaxf(top, cz);
           if (nt > -INFINITY) sum = sum * ex2(top - nt) + (cz > -INFINITY ? cl * ex2(cz - nt) : 0.f);
           top = nt;
           weight[c] = cz;
         }
 #pragma unroll
-        for (int off = 1; off < 16; off <<= 1) {
+        for (int off = 1; off < C::TPR; off <<= 1) {
           const float ot = __shfl_xor_sync(0xffffffffu, top, off), os = __shfl_xor_sync(0xffffffffu, sum, off);
           const float nt = fmaxf(top, ot);
           if (nt > -INFINITY) sum = sum * ex2(top - nt) + os * ex2(ot - nt);
           top = nt;
         }
-        for (int c = jc; c < n_cta; c += 16) weight[c] = weight[c] == -INFINITY ? 0.f : ex2(weight[c] - top);
+        for (int c = jc; c < n_cta; c += C::TPR) weight[c] = weight[c] == -INFINITY ? 0.f : ex2(weight[c] - top);
         __syncwarp();
-        float acc[D / 16];
+        constexpr int VW = D / C::TPR < 4 ? D / C::TPR : 4, NV = D / C::TPR / VW;  // columns VW jc .. of each VW TPR
+        float acc[NV][VW];
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) acc[i] = 0.f;
-        constexpr int kAhead = D <= 128 ? 8 : 4;
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int k = 0; k < VW; ++k) acc[i][k] = 0.f;
+        constexpr int kAhead = D / C::TPR <= 8 ? 8 : 4;
         for (int c0 = 0; c0 < n_cta; c0 += kAhead) {
-          float4 v[kAhead][D / 64];
+          float v[kAhead][NV][VW];
 #pragma unroll
           for (int u = 0; u < kAhead; ++u) {
-            const float* src = slot_of(min(c0 + u, n_cta - 1)) + jr * D + jc * 4;
+            const float* src = slot_of(min(c0 + u, n_cta - 1)) + jr * D + jc * VW;
 #pragma unroll
-            for (int i = 0; i < D / 64; ++i) v[u][i] = __ldcg(reinterpret_cast<const float4*>(src + i * 64));
+            for (int i = 0; i < NV; ++i) {
+              if constexpr (VW == 4) {
+                const float4 q = __ldcg(reinterpret_cast<const float4*>(src + i * VW * C::TPR));
+                v[u][i][0] = q.x, v[u][i][1] = q.y, v[u][i][2] = q.z, v[u][i][3] = q.w;
+              } else {
+                const float2 q = __ldcg(reinterpret_cast<const float2*>(src + i * VW * C::TPR));
+                v[u][i][0] = q.x, v[u][i][1] = q.y;
+              }
+            }
           }
 #pragma unroll
           for (int u = 0; u < kAhead; ++u) {
             const float f = c0 + u < n_cta ? weight[c0 + u] : 0.f;
 #pragma unroll
-            for (int i = 0; i < D / 64; ++i) {
-              acc[4 * i] += f * v[u][i].x;
-              acc[4 * i + 1] += f * v[u][i].y;
-              acc[4 * i + 2] += f * v[u][i].z;
-              acc[4 * i + 3] += f * v[u][i].w;
-            }
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+              for (int k = 0; k < VW; ++k) acc[i][k] += f * v[u][i][k];
           }
         }
         const float n = sum > 0.f ? __fdiv_rn(1.f, sum) : 0.f;
         if (row < rows) {
 #pragma unroll
-          for (int i = 0; i < D / 64; ++i) {
-            const __nv_bfloat162 x = __floats2bfloat162_rn(acc[4 * i] * n, acc[4 * i + 1] * n);
-            const __nv_bfloat162 y = __floats2bfloat162_rn(acc[4 * i + 2] * n, acc[4 * i + 3] * n);
-            *reinterpret_cast<uint2*>(dst + jc * 4 + i * 64) =
-                make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-          }
+          for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int k = 0; k < VW; k += 2)
+              *reinterpret_cast<__nv_bfloat162*>(dst + i * VW * C::TPR + jc * VW + k) =
+                  __floats2bfloat162_rn(acc[i][k] * n, acc[i][k + 1] * n);
         }
         if (tid == 0) p.counters[c_first] = 0u;  // ready for the next launch on this workspace
       }
