@@ -99,7 +99,15 @@ Q8Ws q8_ws(int64_t M, int64_t K) {
 
 cudaError_t q8_quantize(const void* x, int f32, int64_t R, int64_t K, int rotate, bool early, int8_t* codes, float* s,
                         cudaStream_t st) {
-  const dim3 grid{unsigned(R)}, block{unsigned(q8_threads(R, K))};
+  const dim3 grid{unsigned(R)};
+  if (R > kQ8FewRows) {
+    const Q8Wide w = q8_wide(K);
+    const dim3 block{unsigned(32 * w.warps)};
+    const size_t smem = size_t(w.rounds - 1) * w.warps * 4096;
+    return f32 ? launch_pdl(int8_quant_wide_kernel<true>, grid, block, smem, st, x, int(K), int(rotate), early, codes, s, w.rounds)
+               : launch_pdl(int8_quant_wide_kernel<false>, grid, block, smem, st, x, int(K), int(rotate), early, codes, s, w.rounds);
+  }
+  const dim3 block{unsigned(q8_threads(K))};
   return f32 ? launch_pdl(int8_quant_kernel<true>, grid, block, size_t(K) * 4, st, x, int(K), int(rotate), early, codes, s)
              : launch_pdl(int8_quant_kernel<false>, grid, block, size_t(K) * 4, st, x, int(K), int(rotate), early, codes, s);
 }
@@ -285,6 +293,8 @@ cudaError_t ka_launch(const KaParams& p, const w4a8_kv_cache* c, int ctas, cudaS
 bool int8_allow_smem() {
   return allow_smem(int8_quant_kernel<false>, size_t(kMaxK) * 4) == cudaSuccess &&
          allow_smem(int8_quant_kernel<true>, size_t(kMaxK) * 4) == cudaSuccess &&
+         allow_smem(int8_quant_wide_kernel<false>, size_t(kMaxK) * 4) == cudaSuccess &&
+         allow_smem(int8_quant_wide_kernel<true>, size_t(kMaxK) * 4) == cudaSuccess &&
          allow_smem(int8_gemm_kernel<16, 2>, Q8Cfg<16, 2>::kSmem) == cudaSuccess &&
          allow_smem(int8_gemm_kernel<16, 1>, Q8Cfg<16, 1>::kSmem) == cudaSuccess &&
          allow_smem(int8_gemm_kernel<32, 2>, Q8Cfg<32, 2>::kSmem) == cudaSuccess &&
@@ -427,6 +437,7 @@ w4a8_status w4a8_kv_update(const w4a8_kv_cache* cache, const w4a8_kv_batch* batc
   const bool small = batch->tokens <= 4 * batch->batch;
   const int threads = small ? 64 : 256;
   const int64_t q_ctas = has_q ? (batch->tokens * p.q_parts * 32 + threads - 1) / threads : 0;
+  p.stride = int((page_ctas + q_ctas) / page_ctas);
   const dim3 grid{unsigned(page_ctas + q_ctas)}, block{unsigned(threads)};
   switch (D + small) {
     case 64: return status_of(launch_pdl(kv_update_kernel<64, 256>, grid, block, 0, s, p));
