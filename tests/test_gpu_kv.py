@@ -504,3 +504,40 @@ def test_refused_before_anything_runs(lib):
     shared = torch.empty((1, 4, 128), dtype=torch.bfloat16, device="cuda").expand(b.t, 4, 128)
     with pytest.raises(lib.W4A8Error):
         lib.kv_attention(torch.zeros(b.t, 4, 128, dtype=torch.bfloat16, device="cuda"), cache, *b.args(), out=shared)
+
+
+@pytest.mark.parametrize("lens,hq,hk,page,d,window", [
+    ([(700, 1500)], 32, 8, 32, 128, 0),                       # less than a wave of tiles: all in parts
+    ([(130, 130), (64, 6000), (200, 1000)], 16, 4, 64, 64, 0),  # parts of very different ranges
+    ([(1300, 2000), (900, 900)], 32, 8, 16, 128, 300),        # a wave and a rest; the window leaves most keys out
+    ([(1024, 1100)], 24, 4, 64, 256, 0),
+    ([(1, 5), (1, 4)], 1024, 8, 16, 64, 0),                   # one tile of keys: parts without any
+    ([(1, 80)] * 5, 2048, 16, 16, 128, 0),
+])
+def test_attention_parts(lib, lens, hq, hk, page, d, window):
+    """Row tiles split along their keys: against the oracle, the same bits again, and a clean workspace."""
+    b = Batch(lens, hk, page, d, 75)
+    q, qx = bf16(b.rng, b.t, hq, d)
+    cache, ws = b.cache(lib), lib.kv_attention_workspace(b.t, hq, hk, d, "cuda")
+    out = lib.kv_attention(q, cache, *b.args(), window=window, workspace=ws)
+    assert lib.get_device_error() == 0
+    check_attention(out, *R.attention(qx, b.ref, b.table, b.start, b.kv_len, d ** -0.5, window), least=2.0 ** -32)
+    assert not ws[:1024].any()
+    ws[1024:] = 255                                           # (NaN in every partial result that is not written)
+    for _ in range(3):
+        assert torch.equal(lib.kv_attention(q, cache, *b.args(), window=window, workspace=ws), out)
+    assert not ws[:1024].any()
+
+
+def test_sequences_that_share_rows_leave_the_workspace_clean(lib):
+    """q_start that goes back and forth: results are undefined, the next call's are not."""
+    b = Batch([(700, 1500)], 8, 32, 128, 76)
+    q, _ = bf16(b.rng, b.t, 32, 128)
+    cache, ws = b.cache(lib), lib.kv_attention_workspace(b.t, 32, 8, 128, "cuda")
+    want = lib.kv_attention(q, cache, *b.args(), workspace=ws)
+    table, _, kv = b.args()
+    start = torch.tensor([0, b.t] * 5, dtype=torch.int32, device="cuda")
+    lib.kv_attention(q, cache, table.repeat(9, 1), start, kv.repeat(9), workspace=ws)
+    assert lib.get_device_error() == 8
+    assert not ws[:1024].any()
+    assert torch.equal(lib.kv_attention(q, cache, *b.args(), workspace=ws), want)

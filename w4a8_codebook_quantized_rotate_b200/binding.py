@@ -710,9 +710,13 @@ def kv_dequant(cache: KvCache, ids: torch.Tensor, stream=None):
     return (_marshal or _m()).kv_dequant(cache, ids, stream)
 
 
+def kv_attention_workspace_bytes(tokens: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(load_library().w4a8_kv_attention_workspace_bytes(tokens, q_heads, kv_heads, head_dim))
+
+
 def kv_attention_workspace(tokens: int, q_heads: int, kv_heads: int, head_dim: int, device) -> torch.Tensor:
     """A zero-filled workspace for kv_attention."""
-    need = int(load_library().w4a8_kv_attention_workspace_bytes(tokens, q_heads, kv_heads, head_dim))
+    need = kv_attention_workspace_bytes(tokens, q_heads, kv_heads, head_dim)
     if need == 0:
         raise W4A8Error("w4a8_kv_attention_workspace_bytes", 2)
     return torch.zeros(need, dtype=torch.uint8, device=device)

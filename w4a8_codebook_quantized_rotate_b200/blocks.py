@@ -96,15 +96,13 @@ class AttentionBlock:
         self.rotation = dict(q_weight=q_weight, k_weight=k_weight, eps=eps, inv_freq=inv_freq, interleaved=interleaved,
                              rope_factor=rope_factor)
         self.scale, self.window = scale, window
-        self._workspace = None  # of the attention, for any number of tokens
+        self._workspaces = _Workspaces(lambda m: B.kv_attention_workspace_bytes(m, heads, kv_heads, head_dim))
 
     def prepare(self, tokens: int, device="cuda") -> torch.Tensor:
         """Allocate what steps of that many tokens need; returns the attention's workspace."""
         self.qkv.prepare(tokens)
         self.out.prepare(tokens)
-        if self._workspace is None:
-            self._workspace = B.kv_attention_workspace(tokens, self.heads, self.kv_heads, self.head_dim, device)
-        return self._workspace
+        return self._workspaces.get(tokens, device)
 
     def __call__(self, x: torch.Tensor, cache: B.KvCache, block_table: torch.Tensor, q_start: torch.Tensor,
                  kv_len: torch.Tensor, positions: torch.Tensor | None = None) -> torch.Tensor:

@@ -256,7 +256,12 @@ bool ka_shape_ok(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t D) {
 }
 
 constexpr size_t kKaZeroBytes = 1024;
-static_assert(kKaMaxCtas * 4 <= kKaZeroBytes, "counters fit");
+static_assert((kKaMaxCtas + kKaMaxCtas / 2) * 4 <= kKaZeroBytes, "counters fit");
+
+// CTAs that the tensor-memory kernel may have, of 256 rows (for its choice).
+int64_t kp_ctas_bound(int64_t rows, int64_t batch, int64_t kv_heads) {
+  return (rows / 256 + std::min<int64_t>(batch, rows / kKpMinRows)) * kv_heads;
+}
 
 // Row tiles of 8 where a sequence has that many rows on average (a decode
 // step of up to 8 query heads to a key head), else of 16.
@@ -278,10 +283,11 @@ cudaError_t ka_launch(const KaParams& p, const w4a8_kv_cache* c, int ctas, cudaS
   // sequences' lengths which of them are its own).
   const int64_t rows = int64_t(p.batch.tokens) * p.group;
   const int64_t units = rows / KpCfg<D>::kRows + std::min<int64_t>(p.batch.batch, rows / kKpMinRows);
-  q.both = (rows / 256 + std::min<int64_t>(p.batch.batch, rows / kKpMinRows)) * c->kv_heads >= kKpMinCtas;
+  q.both = kp_ctas_bound(rows, p.batch.batch, c->kv_heads) >= kKpMinCtas;
   if (q.both) {
-    if (units * c->kv_heads >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
-    if (cudaError_t e = launch_pdl(kv_prefill_kernel<D>, dim3(unsigned(units * c->kv_heads)), dim3(KpCfg<D>::kThreads),
+    const int64_t grid = units * c->kv_heads + p.sms;  // (the units' parts are at most one wave)
+    if (grid >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    if (cudaError_t e = launch_pdl(kv_prefill_kernel<D>, dim3(unsigned(grid)), dim3(KpCfg<D>::kThreads),
                                    KpCfg<D>::kSmem, st, q);
         e != cudaSuccess)
       return e;
@@ -466,7 +472,10 @@ w4a8_status w4a8_kv_dequant(const w4a8_kv_cache* cache, const int32_t* ids, int6
 
 size_t w4a8_kv_attention_workspace_bytes(int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
   if (!ka_shape_ok(tokens, q_heads, kv_heads, head_dim)) return 0;
-  return kKaZeroBytes + size_t(kKaMaxCtas) * 2 * (size_t(kKaMaxRows) * head_dim + 2 * kKaMaxRows) * 4;
+  const int64_t rows = tokens * (q_heads / kv_heads);
+  const size_t stream = size_t(kKaMaxCtas) * 2 * (size_t(kKaMaxRows) * head_dim + 2 * kKaMaxRows) * 4;
+  const size_t parts = size_t(kKaMaxCtas) * (head_dim <= 128 ? 256 : 128) * (head_dim + 2) * 4;
+  return kKaZeroBytes + (kp_ctas_bound(rows, tokens, kv_heads) >= kKpMinCtas ? std::max(stream, parts) : stream);
 }
 
 w4a8_status w4a8_kv_attention(const w4a8_heads* q, const w4a8_kv_cache* cache, const w4a8_kv_batch* batch, float scale,
@@ -494,11 +503,12 @@ w4a8_status w4a8_kv_attention(const w4a8_heads* q, const w4a8_kv_cache* cache, c
   p.group = q->heads / cache->kv_heads;
   p.box_shift = 0;
   p.both = 0;
+  p.sms = std::min(d->sms, kKaMaxCtas);
   p.counters = static_cast<unsigned*>(workspace);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kKaZeroBytes);
   p.err = d->err;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int ctas = std::min(d->sms, kKaMaxCtas);
+  const int ctas = p.sms;
   const bool few = ka_few_rows(batch->tokens, batch->batch, p.group);
   switch (D + few) {
     case 64: return status_of(ka_launch<64, 2>(p, cache, ctas, s));

@@ -104,8 +104,9 @@ struct KaParams {
   int group;         // query heads of a key head
   int box_shift;     // log2 of a TMA box's rows
   int both;          // the tensor-memory kernel is launched as well
-  float* part;       // [CTA][2][kSlotFloats]
-  unsigned* counters;  // [CTA]
+  int sms;
+  float* part;       // [CTA][2][kSlotFloats]; the tensor-memory kernel's parts before that
+  unsigned* counters;  // [kKaMaxCtas] by CTA, then the tensor-memory kernel's, by split unit
   unsigned* err;
 };
 
@@ -146,6 +147,7 @@ W4A8_HD int ka_item_cta(long long i, long long total, long long ctas) {
 // against 140 for this whole kernel.
 constexpr int kKpMinRows = 128;
 constexpr int kKpMinCtas = 32;
+constexpr int kKpMaxParts = 4;
 __device__ __forceinline__ bool kp_takes_big(const KaParams& p) {  // whole warp
   const int lane = threadIdx.x & 31;
   long long ctas = 0;

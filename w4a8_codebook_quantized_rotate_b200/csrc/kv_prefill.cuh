@@ -25,6 +25,12 @@
 // Every row tile has two score buffers: the scores of the next key tile are
 // made while the softmax of this one runs, so the softmax warps, which bound
 // the kernel, do not wait for the MMAs.
+// The CTAs that are left over after whole waves of one CTA an SM are split
+// along their keys where that fills the SMs better (a rest of at most half a
+// wave, in up to four parts); the parts' O, maxima and sums meet in the
+// workspace, where the last one to arrive adds them in their order (two
+// sequences of up to 2048 new tokens on up to 8192, 32/8 heads of 128: 492 us,
+// 530 unsplit).
 // Bounds: per 256 x 128 (rows x keys) and D = 128 the MMAs take 2048 clocks
 // of an SM (2560 with the operand reads of 64-key tiles), its exponentials (16
 // a clock) 2048, so the softmax keeps to about four other instructions a
@@ -69,8 +75,9 @@ struct KpShared {
   uint64_t drain;
   float ks[8][4], lv[8][4], iv[8][4];  // ks, log2(vs), 1 / vs of a tile's key groups (ring of 8 tiles)
   uint32_t tmem_base;
-  int found;
-  int b, tile;
+  int found, last;
+  int b, tile, head;
+  int slot, part, parts;  // of a split unit's parts this CTA is `part`
   volatile int abort;
 };
 
@@ -139,12 +146,29 @@ __device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t smem_addr, uint32_t l
          (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
 
+// Units (row tiles of a key head) of the batch; 0 where the streaming kernel
+// takes all of it.
+template <int D>
+__device__ __forceinline__ int kp_units(const KaParams& p) {  // whole warp
+  if (!kp_takes_big(p)) return 0;
+  const int lane = threadIdx.x & 31;
+  int units = 0;
+  for (int b0 = 0; b0 < p.batch.batch; b0 += 32) {
+    if (b0 + lane < p.batch.batch) {
+      const int rows = kv_load_seq(p.batch, b0 + lane, p.cache.page_shift).q_len * p.group;
+      if (rows >= kKpMinRows) units += (rows + KpCfg<D>::kRows - 1) / KpCfg<D>::kRows;
+    }
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) units += __shfl_xor_sync(0xffffffffu, units, off);
+  return units * p.cache.kv_heads;
+}
+
 // The row tile (of kRows rows) that unit u is; the tiles of a sequence are
 // taken from its last, whose range of keys is longest.  False past the last
-// one, and where the streaming kernel takes the whole batch.
+// one.
 template <int D>
 __device__ __forceinline__ bool kp_find(const KaParams& p, int u, int& seq, int& tile) {
-  if (!kp_takes_big(p)) return false;
   const int lane = threadIdx.x & 31;
   int before = 0;
   for (int b0 = 0; b0 < p.batch.batch; b0 += 32) {
@@ -194,11 +218,20 @@ __global__ void __launch_bounds__(KpCfg<D>::kThreads, 1) kv_prefill_kernel(const
     sh->abort = 0;
     fence_barrier_init();
   }
-  const int head = int(blockIdx.x) % p.cache.kv_heads, unit = int(blockIdx.x) / p.cache.kv_heads;
   if (warp == 1) {
+    const int units = kp_units<D>(p), rest = units % p.sms, whole = units - rest;
+    // 1 where the rest is more than half a wave (or where sequences share rows, and so have more units than CTAs)
+    const int parts = rest > 0 && units <= int(gridDim.x) - p.sms ? min(kKpMaxParts, p.sms / rest) : 1;
+    const int over = int(blockIdx.x) - whole;                          // place among the parts of the rest
+    const int nth = over < 0 ? int(blockIdx.x) : whole + over / parts;
     int b = 0, tile = 0;
-    const bool found = kp_find<D>(p, unit, b, tile);
-    if (lane == 0) sh->found = found, sh->b = b, sh->tile = tile;
+    const bool found = nth < units && kp_find<D>(p, nth / p.cache.kv_heads, b, tile);
+    if (lane == 0) {
+      sh->found = found, sh->b = b, sh->tile = tile, sh->head = nth % p.cache.kv_heads;
+      sh->parts = over < 0 ? 1 : parts;
+      sh->part = over < 0 ? 0 : over % parts;
+      sh->slot = over < 0 ? 0 : over / parts;
+    }
   }
   __syncthreads();
   if (!sh->found) return;
@@ -214,8 +247,10 @@ __global__ void __launch_bounds__(KpCfg<D>::kThreads, 1) kv_prefill_kernel(const
   const int rows = seq.q_len * p.group, row0 = sh->tile * C::kRows;
   const int last = min(rows, row0 + C::kRows) - 1;
   const KvRange range = kv_range(seq, row0 / p.group, last / p.group, p.window);
-  const int key0 = range.lo & ~(C::TK - 1);
-  const int n_tiles = (range.hi - key0 + C::TK - 1) / C::TK;
+  const int key_lo = range.lo & ~(C::TK - 1), all_tiles = (range.hi - key_lo + C::TK - 1) / C::TK;
+  const int head = sh->head, part = sh->part, parts = sh->parts;
+  const int tile0 = int((long long)all_tiles * part / parts);
+  const int n_tiles = int((long long)all_tiles * (part + 1) / parts) - tile0, key0 = key_lo + tile0 * C::TK;
   constexpr int kMmaWarp = C::kSoftWarps + kKpConvWarps;
 
   if (warp < C::kSoftWarps) {
@@ -392,14 +427,15 @@ __global__ void __launch_bounds__(KpCfg<D>::kThreads, 1) kv_prefill_kernel(const
     }
     // ---- O / l
     if (ok) ok = kp_wait_warp(&sh->drain, 0, sh, p.err);
-    if (ok) {
-      tc_fence_after();
+    tc_fence_after();
+    uint16_t* dst = p.out.data + (long long)(seq.start + j) * p.out.token + h * p.out.head;
+    const uint32_t ocol = tmem + trow + C::kOCol + uint32_t(t * D);
+    if (parts == 1) {
       const float norm = l > 0.f ? __fdiv_rn(1.f, l) : 0.f;
-      uint16_t* dst = p.out.data + (long long)(seq.start + j) * p.out.token + h * p.out.head;
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
+      for (int c = 0; c < D && ok; c += 32) {
         uint32_t v[32];
-        tmem_ld_32x32b_x32(tmem + trow + C::kOCol + uint32_t(t * D + c), v);
+        tmem_ld_32x32b_x32(ocol + uint32_t(c), v);
         tc_wait_ld();
         if (live) {
 #pragma unroll
@@ -410,6 +446,65 @@ __global__ void __launch_bounds__(KpCfg<D>::kThreads, 1) kv_prefill_kernel(const
             *reinterpret_cast<uint4*>(dst + c + e) = float_to_bf16x8(o);
           }
         }
+      }
+    } else {
+      // [part][O: D / 4][row][4], z [row], l [row]
+      constexpr size_t kPart = size_t(C::kRows) * (D + 2);
+      const int pr = 128 * t + r;
+      float* slot = p.part + size_t(sh->slot) * parts * kPart;
+      float* mine = slot + size_t(part) * kPart;
+      if (n_tiles > 0) {
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+          uint32_t v[16];
+          tmem_ld_32x32b_x16(ocol + uint32_t(c), v);
+          tc_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; e += 4)
+            *reinterpret_cast<uint4*>(mine + (size_t((c + e) / 4) * C::kRows + pr) * 4) =
+                make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        }
+      }
+      mine[C::kRows * D + pr] = ok ? z : -INFINITY;
+      mine[C::kRows * D + C::kRows + pr] = l;
+      __threadfence();
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kSoftWarps) : "memory");
+      if (threadIdx.x == 0) sh->last = atomicAdd(p.counters + kKaMaxCtas + sh->slot, 1u) == unsigned(parts - 1);
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kSoftWarps) : "memory");
+      if (sh->last) {
+        __threadfence();
+        float w[kKpMaxParts], top = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int s = 0; s < kKpMaxParts; ++s) {
+          w[s] = s < parts ? __ldcg(slot + s * kPart + C::kRows * D + pr) : -INFINITY;
+          top = fmaxf(top, w[s]);
+        }
+#pragma unroll
+        for (int s = 0; s < kKpMaxParts; ++s) {  // (a part of which the row sees nothing has z = -inf, and O unset)
+          w[s] = w[s] == -INFINITY ? 0.f : ex2(w[s] - top);
+          if (w[s] > 0.f) sum = fmaf(w[s], __ldcg(slot + s * kPart + C::kRows * D + C::kRows + pr), sum);
+        }
+        const float norm = sum > 0.f ? __fdiv_rn(1.f, sum) : 0.f;
+        if (live) {
+#pragma unroll 2
+          for (int c = 0; c < D; c += 8) {
+            float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int s = 0; s < kKpMaxParts; ++s)
+              if (w[s] > 0.f) {
+                const float* at = slot + s * kPart + (size_t(c / 4) * C::kRows + pr) * 4;
+                const float4 a = __ldcg(reinterpret_cast<const float4*>(at));
+                const float4 b = __ldcg(reinterpret_cast<const float4*>(at + 4 * C::kRows));
+                o[0] = fmaf(w[s], a.x, o[0]), o[1] = fmaf(w[s], a.y, o[1]), o[2] = fmaf(w[s], a.z, o[2]);
+                o[3] = fmaf(w[s], a.w, o[3]), o[4] = fmaf(w[s], b.x, o[4]), o[5] = fmaf(w[s], b.y, o[5]);
+                o[6] = fmaf(w[s], b.z, o[6]), o[7] = fmaf(w[s], b.w, o[7]);
+              }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[k] *= norm;
+            *reinterpret_cast<uint4*>(dst + c) = float_to_bf16x8(o);
+          }
+        }
+        if (threadIdx.x == 0) p.counters[kKaMaxCtas + sh->slot] = 0u;  // ready for the next launch on this workspace
       }
     }
   } else if (warp < kMmaWarp) {
