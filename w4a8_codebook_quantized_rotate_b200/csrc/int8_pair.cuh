@@ -16,6 +16,7 @@
 // and a transpose of 2-byte values took 11000 clocks a tile, 16-byte stores
 // of each thread to its own row 15000, against 512 per 128 of K of MMAs.)
 // Eight epilogue warps, two to a lane quarter, each half of the columns.
+// With the quantiser (20 us), 4096 tokens of K = 5120, N = 17408 take 252 us.
 //
 // Barriers: `full` lives in the first CTA and counts both CTAs' bytes;
 // `empty` and `acc_full` are in both, arrived at by commits that name both;
