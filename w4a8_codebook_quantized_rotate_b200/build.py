@@ -53,7 +53,7 @@ def build_marshal(force: bool = False) -> str:
     cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-I", os.path.join(ROOT, "include"),
            *(x for i in include for x in ("-isystem", i)), MARSHAL_SRC, "-o", MARSHAL_OUT + ".tmp",
            "-L", os.path.dirname(OUT), "-lw4a8", "-Wl,-rpath,$ORIGIN",
-           "-L", lib, "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda", "-Wl,-rpath," + lib]
+           "-L", lib, "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-lc10", "-lc10_cuda", "-Wl,-rpath," + lib]
     subprocess.run(cmd, check=True)
     os.replace(MARSHAL_OUT + ".tmp", MARSHAL_OUT)
     return MARSHAL_OUT

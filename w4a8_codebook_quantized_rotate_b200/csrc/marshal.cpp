@@ -11,7 +11,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/zeros.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -20,6 +20,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <optional>
 #include <stdexcept>
 #include <string>
 
@@ -117,7 +118,8 @@ struct OnStream {
 };
 
 at::Tensor make(at::IntArrayRef shape, at::ScalarType type, int dev) {
-  return at::empty(shape, at::TensorOptions().dtype(type).device(at::Device(at::kCUDA, c10::DeviceIndex(dev))));
+  // (past the dispatcher, which costs as much again as the allocation)
+  return at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, c10::DeviceIndex(dev)), std::nullopt);
 }
 
 // bf16 rows [tokens, heads, dim], the values of a head contiguous.
