@@ -30,7 +30,8 @@
 // wave, in up to four parts); the parts' O, maxima and sums meet in the
 // workspace, where the last one to arrive adds them in their order (two
 // sequences of up to 2048 new tokens on up to 8192, 32/8 heads of 128: 492 us,
-// 530 unsplit).
+// 530 unsplit; 476 with the softmax's sums and exponents' arguments two to an
+// instruction and its maxima over three).
 // Bounds: per 256 x 128 (rows x keys) and D = 128 the MMAs take 2048 clocks
 // of an SM (2560 with the operand reads of 64-key tiles), its exponentials (16
 // a clock) 2048, so the softmax keeps to about four other instructions a
@@ -137,6 +138,12 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
 
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 // MN-major operand with 128-byte swizzling: rows (k) of 64 values, 8-row
@@ -327,12 +334,10 @@ __global__ void __launch_bounds__(KpCfg<D>::kThreads, 1) kv_prefill_kernel(const
         for (int c = 0; c < C::TK / 32; ++c) {
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
-            float m[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) m[e] = __uint_as_float(v[c][16 * g + e]);
-#pragma unroll
-            for (int e = 4; e < 16; ++e) m[e & 3] = fmaxf(m[e & 3], __uint_as_float(v[c][16 * g + e]));
-            const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+            auto s = [&](int e) { return __uint_as_float(v[c][16 * g + e]); };
+            const float m0 = max3(s(0), s(1), s(2)), m1 = max3(s(3), s(4), s(5)), m2 = max3(s(6), s(7), s(8));
+            const float m3 = max3(s(9), s(10), s(11)), m4 = max3(s(12), s(13), s(14));
+            const float top = fmaxf(max3(m0, m1, m2), max3(m3, m4, s(15)));
             x = fmaxf(x, fmaf(top, f * ks[2 * c + g], lv[2 * c + g]));
           }
         }
@@ -383,17 +388,18 @@ __global__ void __launch_bounds__(KpCfg<D>::kThreads, 1) kv_prefill_kernel(const
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             const float kf = f * ks[2 * c + g], off = lv[2 * c + g] - ref;
-            float s0 = 0.f, s1 = 0.f;
+            const uint64_t kf2 = pack2(kf, kf), off2 = pack2(off, off);
+            uint64_t sum = pack2(0.f, 0.f);
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
-              const float a = ex2(fmaf(__uint_as_float(v[c][16 * g + e]), kf, off));
-              const float b = ex2(fmaf(__uint_as_float(v[c][16 * g + e + 1]), kf, off));
-              s0 += a;
-              s1 += b;
+              const float2 x2 = unpack2(fma2(pack2(__uint_as_float(v[c][16 * g + e]), __uint_as_float(v[c][16 * g + e + 1])), kf2, off2));
+              const float a = ex2(x2.x), b = ex2(x2.y);
+              sum = q8_add2(sum, pack2(a, b));
               const __half2 hh = __floats2half2_rn(a, b);
               w[8 * g + e / 2] = *reinterpret_cast<const uint32_t*>(&hh);
             }
-            l = fmaf(s0 + s1, iv[2 * c + g], l);
+            const float2 s2 = unpack2(sum);
+            l = fmaf(s2.x + s2.y, iv[2 * c + g], l);
           }
           // (into the columns of scores that are read already)
           tmem_st_32x32b_x16(sbuf + uint32_t(16 * c), w);
