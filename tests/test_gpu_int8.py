@@ -242,3 +242,17 @@ def test_scratch_belongs_to_the_calls_stream(lib):
     used = [torch.full((size,), 77, dtype=torch.uint8, device="cuda") for size in [m * k + 1024] * 4 + [m * n * 2] * 4]
     torch.cuda.synchronize()
     assert torch.equal(got, want) and all((u == 77).all() for u in used)
+
+
+@pytest.mark.parametrize("r,k,rotate,f32", [(300, 16, False, False), (400, 17408, True, False), (297, 32768, True, False),
+                                            (301, 4304, False, False), (500, 2304, True, True), (1000, 256, True, False),
+                                            (298, 32752, False, True)])
+def test_many_rows_are_the_few(lib, r, k, rotate, f32):
+    """The kernel of many rows gives each row the codes and scale that the one of few rows gives it."""
+    x = torch.randn(r, k, device="cuda", generator=torch.Generator("cuda").manual_seed(k))
+    x *= 10.0 ** torch.randint(-20, 20, (r, 1), device="cuda").float()
+    x[3] = 0
+    x = x if f32 else x.to(torch.bfloat16)
+    codes, s = lib.int8_quantize(x, rotate=rotate)
+    parts = [lib.int8_quantize(x[i:i + 200].contiguous(), rotate=rotate) for i in range(0, r, 200)]
+    assert torch.equal(codes, torch.cat([c for c, _ in parts])) and torch.equal(s, torch.cat([t for _, t in parts]))

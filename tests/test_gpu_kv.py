@@ -541,3 +541,13 @@ def test_sequences_that_share_rows_leave_the_workspace_clean(lib):
     assert lib.get_device_error() == 8
     assert not ws[:1024].any()
     assert torch.equal(lib.kv_attention(q, cache, *b.args(), workspace=ws), want)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("hq,hk", [(8, 2), (24, 4), (7, 1), (12, 1), (16, 16)])
+def test_attention_row_tiles(lib, d, hq, hk):
+    """Row tiles of 8 that a sequence fills in part, once and several times, among empty sequences; groups that do
+    not divide 8, and one of more rows than 8."""
+    b = Batch([(5, 40), (0, 9), (0, 0), (3, 1000), (0, 70), (1, 1), (0, 16), (1, 333)], hk, 32, d, 77, behind=2)
+    attend(lib, b, hq, d)
+    attend(lib, b, hq, d, window=20)

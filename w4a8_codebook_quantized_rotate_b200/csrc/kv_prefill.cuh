@@ -32,6 +32,11 @@
 // sequences of up to 2048 new tokens on up to 8192, 32/8 heads of 128: 492 us,
 // 530 unsplit; 476 with the softmax's sums and exponents' arguments two to an
 // instruction and its maxima over three).
+// Slower at that size: P' in buffers of its own, so that the scores wait only
+// for the softmax (493), and tiles of 128 keys with one buffer of scores (651,
+// the scores read twice).  Without its exponentials, its expansion or its
+// loads the kernel takes 440 to 455, so none of them alone bounds it: the
+// hand-offs between the roles do, about 150 clocks each.
 // Bounds: per 256 x 128 (rows x keys) and D = 128 the MMAs take 2048 clocks
 // of an SM (2560 with the operand reads of 64-key tiles), its exponentials (16
 // a clock) 2048, so the softmax keeps to about four other instructions a
