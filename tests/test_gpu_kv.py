@@ -551,3 +551,35 @@ def test_attention_row_tiles(lib, d, hq, hk):
     b = Batch([(5, 40), (0, 9), (0, 0), (3, 1000), (0, 70), (1, 1), (0, 16), (1, 333)], hk, 32, d, 77, behind=2)
     attend(lib, b, hq, d)
     attend(lib, b, hq, d, window=20)
+
+
+@pytest.mark.parametrize("lens,hq,hk,page,d,window", [
+    ([(256, 3000)], 32, 32, 16, 128, 0),
+    ([(200, 2200), (150, 3333), (1, 77)], 32, 16, 32, 128, 0),
+    ([(129, 2700), (3, 50), (260, 2600)], 32, 16, 64, 64, 0),
+    ([(150, 3150), (0, 9), (135, 2512)], 32, 16, 128, 256, 0),
+    ([(70, 3129), (128, 1000)], 64, 16, 16, 256, 0),
+    ([(131, 3640), (1, 5)], 56, 8, 16, 64, 0),
+    ([(700, 900)], 64, 16, 32, 128, 1),
+    ([(600, 1700)], 32, 16, 64, 256, 260),
+    ([(130, 130), (128, 6000), (200, 1000)], 16, 4, 64, 128, 0),
+    ([(400, 6000), (32, 32)], 16, 4, 64, 128, 0),      # parts of a unit with one tile of keys
+])
+def test_attention_many_rows_and_keys(lib, lens, hq, hk, page, d, window):
+    """Batches whose rows and keys pay for the tensor-memory kernel (kv_tiles_pay), alone and beside short ones."""
+    attend(lib, Batch(lens, hk, page, d, 78 + d + window, behind=2), hq, d, window, least=2.0 ** -32)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_attention_many_rows_and_keys_ranges(lib, d):
+    """Page scales from 0 to 1e6, queries of far sizes, a negative scale, on the tensor-memory kernel."""
+    b = Batch([(130, 3000), (140, 2150)], 16, 16, d, d + 2)
+    b.ref.scales[1][:] *= 10.0 ** b.rng.integers(-6, 7, b.ref.scales[1].shape)
+    b.ref.scales[1][::3] = 0.0
+    b.ref.scales[0][::4] = 0.0
+    attend(lib, b, 32, d, q_scale=8.0, least=2.0 ** -32)
+    q, _ = bf16(b.rng, b.t, 32, d)
+    size = (10.0 ** b.rng.integers(-30, 3, (b.t, 32, 1))).astype(np.float32)
+    q = (q.float() * dev(size)).to(torch.bfloat16)
+    got = lib.kv_attention(q, b.cache(lib), *b.args(), scale=-0.1)
+    check_attention(got, *R.attention(q.double().cpu().numpy(), b.ref, b.table, b.start, b.kv_len, -0.1), least=2.0 ** -32)

@@ -258,7 +258,13 @@ bool ka_shape_ok(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t D) {
 constexpr size_t kKaZeroBytes = 1024;
 static_assert((kKaMaxCtas + kKaMaxCtas / 2) * 4 <= kKaZeroBytes, "counters fit");
 
-// CTAs that the tensor-memory kernel may have, of 256 rows (for its choice).
+// The host knows only the batch's totals and the block table's width: it
+// launches the tensor-memory kernel too where that would pay at the table's
+// width, and the average sequence has rows for it or the total is so large
+// that a few of many sequences may (a launch that finds nothing to do costs
+// 5 us).
+constexpr int64_t kKpMinCtas = 4, kKpSureCtas = 32;
+// Tiles of 256 rows that the tensor-memory kernel may have.
 int64_t kp_ctas_bound(int64_t rows, int64_t batch, int64_t kv_heads) {
   return (rows / 256 + std::min<int64_t>(batch, rows / kKpMinRows)) * kv_heads;
 }
@@ -283,7 +289,11 @@ cudaError_t ka_launch(const KaParams& p, const w4a8_kv_cache* c, int ctas, cudaS
   // sequences' lengths which of them are its own).
   const int64_t rows = int64_t(p.batch.tokens) * p.group;
   const int64_t units = rows / KpCfg<D>::kRows + std::min<int64_t>(p.batch.batch, rows / kKpMinRows);
-  q.both = kp_ctas_bound(rows, p.batch.batch, c->kv_heads) >= kKpMinCtas;
+  const int64_t bound = kp_ctas_bound(rows, p.batch.batch, c->kv_heads);
+  const int64_t capacity = p.batch.table_stride * c->page;
+  const int64_t keys = p.window > 0 ? std::min<int64_t>(capacity, int64_t(p.window) + p.batch.tokens) : capacity;
+  q.both = bound >= kKpMinCtas && (bound >= kKpSureCtas || rows >= kKpMinRows * int64_t(p.batch.batch)) &&
+           kv_tiles_pay(units * c->kv_heads, rows * (keys + 512) * c->kv_heads, keys, D, p.sms);
   if (q.both) {
     const int64_t grid = units * c->kv_heads + p.sms;  // (the units' parts are at most one wave)
     if (grid >= (int64_t(1) << 31)) return cudaErrorInvalidValue;

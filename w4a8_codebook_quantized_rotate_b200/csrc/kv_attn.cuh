@@ -142,28 +142,39 @@ W4A8_HD int ka_item_cta(long long i, long long total, long long ctas) {
   return int(((i + 1) * ctas + total - 1) / total - 1);
 }
 
-// A sequence of at least kKpMinRows rows (new tokens x query heads of a key
-// head) is left to the tensor-memory kernel (kv_prefill.cuh) when the batch
-// has enough such tiles of 256 rows: that kernel does about 4.5 TFLOP/s a CTA
-// against 140 for this whole kernel.  (With its tiles split along the keys it
-// would win from fewer on, but the host, which knows only the totals, would
-// then launch it for decode batches as well, where it finds nothing to do and
-// costs 2 us.)
+// Sequences of at least kKpMinRows rows (new tokens x query heads of a key
+// head) are left to the tensor-memory kernel (kv_prefill.cuh) where that pays
+// (kv_tiles_pay).
 constexpr int kKpMinRows = 128;
-constexpr int kKpMinCtas = 32;
-constexpr int kKpMaxParts = 4;
-__device__ __forceinline__ bool kp_takes_big(const KaParams& p) {  // whole warp
+template <int D>
+constexpr int kKpRows = D <= 128 ? 256 : 128;  // of one of its units
+
+// Units of the batch that it takes; 0 where the streaming kernel takes all.
+template <int D>
+__device__ __forceinline__ int kp_units(const KaParams& p) {  // whole warp
   const int lane = threadIdx.x & 31;
-  long long ctas = 0;
+  int units = 0, most = 0;
+  long long work = 0;
   for (int b0 = 0; b0 < p.batch.batch; b0 += 32) {
     if (b0 + lane < p.batch.batch) {
-      const long long rows = (long long)kv_load_seq(p.batch, b0 + lane, p.cache.page_shift).q_len * p.group;
-      if (rows >= kKpMinRows) ctas += (rows + 255) / 256 * p.cache.kv_heads;
+      const KvSeq s = kv_load_seq(p.batch, b0 + lane, p.cache.page_shift);
+      const int rows = s.q_len * p.group;
+      if (rows >= kKpMinRows) {
+        const KvRange r = kv_range(s, 0, s.q_len - 1, p.window);
+        units += (rows + kKpRows<D> - 1) / kKpRows<D>;
+        work += (long long)rows * (r.hi - r.lo + 512);
+        most = max(most, r.hi - r.lo);
+      }
     }
   }
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) ctas += __shfl_xor_sync(0xffffffffu, ctas, off);
-  return ctas >= kKpMinCtas;
+  for (int off = 16; off > 0; off >>= 1) {
+    units += __shfl_xor_sync(0xffffffffu, units, off);
+    work += __shfl_xor_sync(0xffffffffu, work, off);
+    most = max(most, __shfl_xor_sync(0xffffffffu, most, off));
+  }
+  const int heads = p.cache.kv_heads;
+  return kv_tiles_pay((long long)units * heads, work * heads, most, D, p.sms) ? units * heads : 0;
 }
 
 // Row tiles of a sequence, and items of each (the same for all of them: a
@@ -292,7 +303,7 @@ __global__ void __launch_bounds__(KaCfg<D, NR>::kThreads, 1)
   }
   if (warp == 0) {
     // The batch's items, then the sequence that holds this CTA's first one.
-    const bool small_only = p.both && kp_takes_big(p);
+    const bool small_only = p.both && kp_units<D>(p) > 0;
     long long total = 0;
     for (int b0 = 0; b0 < p.batch.batch; b0 += 32) {
       int tiles = 0, items = 0;

@@ -67,4 +67,23 @@ W4A8_HD KvRange kv_range(const KvSeq& s, int j0, int j1, int window) {
   return r;
 }
 
+// Whether the tensor-memory attention kernel takes a batch's sequences of many
+// rows, by both kernels' estimated times in ns (whole numbers, so that the two
+// kernels, which each ask, agree).  `units` are its row tiles times key heads,
+// row_keys the sum of rows * (keys + 512) times key heads, most_keys the longest
+// range.  The streaming kernel does 140 TFLOP/s after 8 us and spends on each
+// row tile what 512 more keys would cost; the other one takes rate ns for 64 keys
+// of a unit after its base, with units in waves of one to an SM, or up to four
+// parts of each.  Measured, streaming / tensor-memory, us: 130 new tokens of
+// 32/8 heads of 128 on 230 keys 14 / 28, 260 of 8/2 on 6000 keys 53 / 58, 500
+// of 8/2 on 6000 90 / 58, 260 of 12/1 heads of 256 on 6000 133 / 70.
+constexpr int kKpMaxParts = 4;
+W4A8_HD bool kv_tiles_pay(int64_t units, int64_t row_keys, int64_t most_keys, int D, int sms) {
+  if (units == 0) return false;
+  const int64_t base = D == 64 ? 20000 : D == 128 ? 27000 : 33000, rate = D == 64 ? 1150 : D == 128 ? 1400 : 1500;
+  const int64_t parts = units * kKpMaxParts <= sms ? kKpMaxParts : units < sms ? sms / units : 1;
+  const int64_t waves = (units * parts + sms - 1) / sms;
+  return 8000 + row_keys * D / 35000 > base + rate * ((most_keys + 63) / 64) * waves / parts;
+}
+
 }  // namespace w4a8

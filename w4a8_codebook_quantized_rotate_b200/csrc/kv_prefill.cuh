@@ -59,7 +59,8 @@ struct KpCfg {
   static constexpr int TK = 64;                          // keys of a tile
   static constexpr int kStages = D <= 128 ? 4 : 2;       // of K, and of V
   static constexpr int KG = TK / 16;                     // key groups (one page each)
-  static constexpr int kRows = 128 * kTiles;
+  static constexpr int kRows = kKpRows<D>;
+  static_assert(kRows == 128 * kTiles, "TMEM lanes");
   static constexpr int kSoftWarps = 4 * kTiles;
   static constexpr int kThreads = 32 * (kSoftWarps + kKpConvWarps + 2);  // softmax, converters, two MMA warps
   static constexpr uint32_t kQ = 128 * D * 2;            // a tile of q, fp16
@@ -156,24 +157,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 __device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t smem_addr, uint32_t lbo) {
   return uint64_t((smem_addr >> 4) & 0x3FFFu) | (uint64_t(lbo >> 4) << 16) | (uint64_t(1024 >> 4) << 32) |
          (uint64_t(1) << 46) | (uint64_t(2) << 61);
-}
-
-// Units (row tiles of a key head) of the batch; 0 where the streaming kernel
-// takes all of it.
-template <int D>
-__device__ __forceinline__ int kp_units(const KaParams& p) {  // whole warp
-  if (!kp_takes_big(p)) return 0;
-  const int lane = threadIdx.x & 31;
-  int units = 0;
-  for (int b0 = 0; b0 < p.batch.batch; b0 += 32) {
-    if (b0 + lane < p.batch.batch) {
-      const int rows = kv_load_seq(p.batch, b0 + lane, p.cache.page_shift).q_len * p.group;
-      if (rows >= kKpMinRows) units += (rows + KpCfg<D>::kRows - 1) / KpCfg<D>::kRows;
-    }
-  }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) units += __shfl_xor_sync(0xffffffffu, units, off);
-  return units * p.cache.kv_heads;
 }
 
 // The row tile (of kRows rows) that unit u is; the tiles of a sequence are
