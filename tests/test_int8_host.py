@@ -256,6 +256,7 @@ SRC = r"""
 #include "kv_index.h"
 using namespace w4a8;
 extern "C" {
+int pays(long long units, long long row_keys, long long most, int d, int sms) { return kv_tiles_pay(units, row_keys, most, d, sms); }
 void seq(int start, int end, int kv, long long tokens, long long table, int* out) {
   KvSeq s = kv_seq(start, end, kv, tokens, table);
   out[0] = s.start; out[1] = s.q_len; out[2] = s.kv_len; out[3] = s.bad;
@@ -346,3 +347,18 @@ def test_every_item_has_one_cta():
         for i in range(total):
             c = of(i, total, ctas)
             assert edges[c] <= i < edges[c + 1]
+
+
+def test_choice_of_the_attention_kernel(index):
+    """Measured on both sides (us, streaming / tensor-memory): new tokens, heads, D, keys, units."""
+    import ctypes
+    f = index.pays
+    f.argtypes, f.restype = [ctypes.c_longlong] * 3 + [ctypes.c_int] * 2, ctypes.c_int
+    for q, hq, hk, d, keys, stream, tensor in ((130, 32, 8, 128, 230, 14, 28), (500, 8, 2, 128, 6000, 90, 58),
+                                               (260, 12, 1, 256, 6000, 133, 70), (260, 24, 4, 256, 6000, 250, 72),
+                                               (64, 24, 4, 64, 6000, 30, 46), (260, 8, 2, 64, 6000, 36, 47)):
+        rows = q * hq // hk
+        units = -(-rows // (256 if d <= 128 else 128)) * hk
+        assert bool(f(units, rows * (keys + 512) * hk, keys, d, 148)) == (tensor < stream)
+    assert not f(0, 0, 0, 128, 148)
+    assert f(2 ** 23, 2 ** 60, 2 ** 30, 256, 148)            # nothing wraps at the largest sizes

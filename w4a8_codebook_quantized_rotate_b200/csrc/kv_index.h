@@ -83,7 +83,8 @@ W4A8_HD bool kv_tiles_pay(int64_t units, int64_t row_keys, int64_t most_keys, in
   const int64_t base = D == 64 ? 20000 : D == 128 ? 27000 : 33000, rate = D == 64 ? 1150 : D == 128 ? 1400 : 1500;
   const int64_t parts = units * kKpMaxParts <= sms ? kKpMaxParts : units < sms ? sms / units : 1;
   const int64_t waves = (units * parts + sms - 1) / sms;
-  return 8000 + row_keys * D / 35000 > base + rate * ((most_keys + 63) / 64) * waves / parts;
+  // (divided first: rows * heads of a q that fits in memory, times 2^30 keys and D, would pass 64 bits)
+  return 8000 + row_keys / 35000 * D > base + rate * ((most_keys + 63) / 64) * waves / parts;
 }
 
 }  // namespace w4a8
