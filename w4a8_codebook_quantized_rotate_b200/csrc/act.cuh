@@ -144,9 +144,11 @@ __global__ void __launch_bounds__(kActMaxThreads) rotate_quant_kernel(const uint
   const int nwarps = blockDim.x >> 5;
   // The previous kernel may still read this workspace: wait for it before
   // writing.  Then the next kernel may launch (it streams its weights, and
-  // waits for this grid before reading what it writes).
+  // waits for this grid before reading what it writes) -- but not behind the
+  // public call: its codes may be weights, which the int8 product
+  // (int8_gemm.cuh) fetches ahead of that wait.
   pdl_wait();
-  pdl_launch_dependents();
+  if constexpr (OUT != kActI8Row) pdl_launch_dependents();
   const int m = blockIdx.x;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int nblocks = K / kRotBlock;
