@@ -10,7 +10,8 @@
  * of values, codes and scales must be 16-byte aligned; the index arrays
  * (positions, block table, q_start, kv_len, page lists) 4-byte aligned.
  * Quantisation is the one of w4a8_rotate_quant_act: symmetric, absmax / 127,
- * round half to even.  Inputs are finite.
+ * round half to even.  Inputs are finite, and so are, in fp32, the norms' sums
+ * of squares and the attention's scores times log2(e).
  */
 #ifndef W4A8_INT8_H_
 #define W4A8_INT8_H_

@@ -1,0 +1,66 @@
+"""Edges of the int8 paged cache's calls (include/w4a8_int8.h), against the
+oracle and the bars of test_gpu_kv.py, or against the same call without the
+edge, bit for bit."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import int8_ref as R
+from test_gpu_kv import INV, Batch, bf16, check_attention, dev
+
+pytestmark = pytest.mark.gpu
+
+# (lens, query heads, key heads, least) of a batch for the streaming kernel, and one whose rows and keys pay for the
+# tensor-memory kernel at every head size
+FEW, MANY = ([(1, 400), (8, 90)], 4, 2, 2.0 ** -39), ([(200, 1300)], 32, 16, 2.0 ** -32)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("lens,hq,hk,least,powers", [(*FEW, (-124, -112, 112, 118, 124)), (*MANY, (-124, 124))])
+def test_queries_at_the_ends_of_the_range(lib, d, lens, hq, hk, least, powers):
+    """Queries of 2^-124 to 2^124 (finite, up to 2^126) and K scales that bring the scores back to a few units: the
+    row's power of two must reach them all."""
+    b = Batch(lens, hk, 16, d, 80 + d)
+    x, _ = bf16(b.rng, b.t, hq, d)
+    k_scales = b.ref.scales[0].copy()
+    for power in powers:
+        q = (x.float() * 2.0 ** power).to(torch.bfloat16)
+        assert q.isfinite().all()
+        b.ref.scales[0] = (k_scales.astype(np.float64) * 2.0 ** -power).astype(np.float32)
+        got = lib.kv_attention(q, b.cache(lib), *b.args())
+        assert lib.get_device_error() == 0
+        check_attention(got, *R.attention(q.double().cpu().numpy(), b.ref, b.table, b.start, b.kv_len, d ** -0.5), least=least)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("lens,hq,hk,least", [FEW, MANY])
+@pytest.mark.parametrize("power,window", [(118, 0), (34, 70), (30, 0)])
+def test_one_key_takes_all_the_weight(lib, d, lens, hq, hk, least, power, window):
+    """Scores of about 2^22, 2^26 and 2^110: a row's largest score is far ahead, and its output that key's value, where
+    the two largest are further apart than twice what fp32 loses (2^-18 of sum |q_d K_d| scale each, so 2^-16 of it and 64
+    more leave the others below 2^-90).  The value: p vs rounded to fp16 (2^-11), the sum (2^-16), the output (2^-8)."""
+    b = Batch(lens, hk, 16, d, 90 + d)
+    x, _ = bf16(b.rng, b.t, hq, d)
+    q = (x.float() * 2.0 ** power).to(torch.bfloat16)
+    b.ref.scales[0] *= np.float32(2.0 ** -8)
+    got = lib.kv_attention(q, b.cache(lib), *b.args(), window=window).double().cpu().numpy()
+    assert lib.get_device_error() == 0 and np.isfinite(got).all()
+    q, group, seen = q.double().cpu().numpy(), hq // hk, 0
+    for i, n in enumerate(b.q_len):
+        length = int(b.kv_len[i])
+        pages = b.table[i][:-(-length // 16)]
+        for h in range(hk):
+            k, v = (np.concatenate([b.ref.values(kind, p, h) for p in pages])[:length] for kind in (0, 1))
+            for j in range(n):
+                end = length - n + j + 1
+                keys = slice(max(0, end - window) if window else 0, end)
+                rows = q[b.start[i] + j, h * group:(h + 1) * group]
+                s, top = rows @ k[keys].T * d ** -0.5, (np.abs(rows) @ np.abs(k[keys]).T).max(1) * d ** -0.5
+                best = np.partition(s, -2, axis=1)
+                for g in np.flatnonzero(best[:, -1] - best[:, -2] > 2.0 ** -16 * top + 64):
+                    want = v[keys][np.argmax(s[g])]
+                    out = got[b.start[i] + j, h * group + g]
+                    assert (np.abs(out - want) <= (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -16) * np.abs(want) + 2.0 ** -73).all()
+                    seen += 1
+    assert seen > 0.9 * b.t * hq

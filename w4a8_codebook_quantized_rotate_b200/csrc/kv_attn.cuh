@@ -7,8 +7,9 @@
 // softmax(scale q_i . K_j) V_j with K_j = ks_j k_j, V_j = vs_j c_j: k_j, c_j are
 // the int8 codes, ks_j, vs_j their pages' scales.  The codes are exact in
 // fp16, so both products run on fp16 operands with fp32 accumulation.
-//   * q is taken to fp16 with a power of two per row (exact: bf16 has fewer
-//     significant bits, the power keeps its range).
+//   * q is taken to fp16 with a power of two per row (ka_row_power): exact for
+//     values down to 2^-30 of the row's largest, since bf16 has fewer significant
+//     bits; smaller ones are off by at most 2^-38 of the largest.
 //   * P' is taken to fp16.  z_i is the running maximum of t_ij less 15: page
 //     scales of one head may be far apart, and the largest p need not carry
 //     the largest share of the result, so the reference is the share; what
@@ -260,6 +261,10 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// The power of two e that takes a row of q to fp16: its largest value lands in [2^13, 2^14), for any finite value (-114
+// at 2^127; at the small end 126, as 2^-e must be a normal number too: values below 2^-113 land below 2^13).
+__device__ __forceinline__ int ka_row_power(float top) { return min(126, 127 + 13 - int(__float_as_uint(top) >> 23)); }
+
 template <int D>
 __device__ __forceinline__ uint32_t ka_tau(uint32_t i) {
   return D < 128 ? i : (i >> 1) | ((i & 1u) << 2);
@@ -465,8 +470,7 @@ __global__ void __launch_bounds__(KaCfg<D, NR>::kThreads, 1)
       for (int i = 0; i < D / 16; ++i) top = fmaxf(top, fabsf(v[i]));
 #pragma unroll
       for (int off = 8; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-      // the row's power of two: its largest value lands in [2^13, 2^14)
-      const int e = min(100, max(-100, 127 + 13 - int(__float_as_uint(top) >> 23)));
+      const int e = ka_row_power(top);
       // (a negative scale goes into q, so that larger products stay larger scores)
       const float up = copysignf(__uint_as_float(uint32_t(127 + e) << 23), p.scale_log2);
       if (l16 == 0) sh->row_factor[r] = __uint_as_float(uint32_t(127 - e) << 23) * fabsf(p.scale_log2);
@@ -587,7 +591,9 @@ __global__ void __launch_bounds__(KaCfg<D, NR>::kThreads, 1)
 #pragma unroll
           for (int kb = 0; kb < C::KG; ++kb)
             // (fmaxf drops the NaN of a wholly masked group under a K scale of 0)
-            x[n][e] = fmaxf(x[n][e], fmaf(fmaxf(s[kb][n][e], s[kb][n][2 + e]), f[n][e] * ks[kb], lv[kb] - 15.f));
+            x[n][e] = fmaxf(x[n][e], fmaf(fmaxf(s[kb][n][e], s[kb][n][2 + e]), f[n][e] * ks[kb], lv[kb]));
+          // (rounded up: no t of the tile is more than 15 above z, however large the scores are)
+          x[n][e] = __fadd_ru(x[n][e], -15.f);
           more_z |= x[n][e] > z[n][e];
         }
       if (__any_sync(0xffffffffu, more_z)) {  // (a row's keys are spread over 8 lanes)
@@ -618,11 +624,12 @@ __global__ void __launch_bounds__(KaCfg<D, NR>::kThreads, 1)
           float pr[4];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float kf = f[n][e] * ks[kb], off = lv[kb] - (z[n][e] == -INFINITY ? 0.f : z[n][e]);
+            const float kf = f[n][e] * ks[kb], ref = z[n][e] == -INFINITY ? 0.f : z[n][e];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const float sc = s[kb][n][2 * h + e];
-              pr[2 * h + e] = ex2(fmaf(sc, kf, off));
+              // (t rounded as it is in z: in one multiply-add with z they would differ by what t's rounding lost)
+              pr[2 * h + e] = ex2(fmaf(sc, kf, lv[kb]) - ref);
               if (edge && sc == -INFINITY) pr[2 * h + e] = 0.f;  // (a masked score times a K scale of 0 is no zero)
             }
             l[n][e] = fmaf(pr[e] + pr[2 + e], w, l[n][e]);

@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(KpCfg<D>::kThreads, 1) kv_prefill_kernel(const
 #pragma unroll
         for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[e]));
       }
-      const int e2 = min(100, max(-100, 127 + 13 - int(__float_as_uint(top) >> 23)));
+      const int e2 = ka_row_power(top);
       float up = __uint_as_float(uint32_t(127 + e2) << 23);
       f = __uint_as_float(uint32_t(127 - e2) << 23) * p.scale_log2;
       if (f < 0.f) {  // a negative scale goes into q, so that larger products stay larger scores
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(KpCfg<D>::kThreads, 1) kv_prefill_kernel(const
     }
     const int lim = seq.kv_len - seq.q_len + j;                      // last key of the row
     const int low = p.window > 0 ? lim - p.window + 1 : 0;           // first
-    const int lim0 = seq.kv_len - seq.q_len + (row0 + 128 * t) / p.group;   // last key of the tile's first row
+    int lim0 = seq.kv_len - seq.q_len + (row0 + 128 * t) / p.group;         // last key of the tile's first row
     const int low1 = p.window > 0 ? range.hi - p.window : 0;         // first key of the CTA's last row
     float z = -INFINITY, l = 0.f;
     bool ok = true;
@@ -344,8 +344,8 @@ __global__ void __launch_bounds__(KpCfg<D>::kThreads, 1) kv_prefill_kernel(const
           if (m > -INFINITY) x = fmaxf(x, fmaf(m, f * ks[g], lv[g]));
         }
       }
-      if (__any_sync(0xffffffffu, x - 7.f > z + 8.f)) {  // (z = -inf: the first visible key)
-        const float nz = fmaxf(z, x - 7.f);
+      if (__any_sync(0xffffffffu, x - z > 15.f)) {  // (z = -inf: the first visible key)
+        const float nz = fmaxf(z, __fadd_ru(x, -7.f));
         const float grow = z == -INFINITY ? 0.f : ex2(z - nz);
         if (i > 0) {
           // O's last product must be done
@@ -366,6 +366,16 @@ __global__ void __launch_bounds__(KpCfg<D>::kThreads, 1) kv_prefill_kernel(const
         }
         l *= grow;
         z = nz;
+        // Scores beyond 2^20 (of any row of the warp): this tile, once more, and the rest take the path of edge tiles, which
+        // rounds t as it is rounded in z.  The other path has t and -z in one multiply-add, which differs from that by what
+        // t's rounding lost: 2^-4 at 2^20, more than fp16's range from 2^24 on.
+        if (__any_sync(0xffffffffu, fabsf(z) > 0x1p20f && z > -INFINITY)) {
+          lim0 = -1;
+          if (!edge) {
+            --i;
+            continue;
+          }
+        }
       }
       const float ref = z == -INFINITY ? 0.f : z;
       // ---- P' and the sum of p
@@ -398,12 +408,12 @@ __global__ void __launch_bounds__(KpCfg<D>::kThreads, 1) kv_prefill_kernel(const
           uint32_t y[16], w[8];
           tmem_ld_32x32b_x16(sbuf + uint32_t(16 * g), y);
           tc_wait_ld();
-          const float kf = f * ks[g], off = lv[g] - ref;
+          const float kf = f * ks[g];
           const int k0g = key + 16 * g;
           float sum = 0.f;
 #pragma unroll
           for (int e = 0; e < 16; e += 2) {
-            float a = ex2(fmaf(__uint_as_float(y[e]), kf, off)), b = ex2(fmaf(__uint_as_float(y[e + 1]), kf, off));
+            float a = ex2(fmaf(__uint_as_float(y[e]), kf, lv[g]) - ref), b = ex2(fmaf(__uint_as_float(y[e + 1]), kf, lv[g]) - ref);
             a = k0g + e <= lim && k0g + e >= low ? a : 0.f;
             b = k0g + e + 1 <= lim && k0g + e + 1 >= low ? b : 0.f;
             sum += a + b;
