@@ -64,3 +64,25 @@ def test_one_key_takes_all_the_weight(lib, d, lens, hq, hk, least, power, window
                     assert (np.abs(out - want) <= (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -16) * np.abs(want) + 2.0 ** -73).all()
                     seen += 1
     assert seen > 0.9 * b.t * hq
+
+
+@pytest.mark.parametrize("good,bad", [(32, (0, 10 ** 6)), (32, (0, -3)), (32, (5, 40)), (64, (0, 10 ** 6)), (700, (0, 10 ** 6))])
+def test_a_bad_sequence_behind_many_is_reported(lib, good, bad):
+    """The last sequence's numbers do not fit, behind 32 or more that fill every unit of the update's launch: its end
+    past the rows, or a length that the table has no places for.  The others' results are those without it."""
+    b = Batch([(1, 1 + i % 20) for i in range(good)], 2, 16, 64, 100)
+    k, _ = bf16(b.rng, b.t, 2, 64)
+    q, _ = bf16(b.rng, b.t, 4, 64)
+    one, two = b.cache(lib), b.cache(lib)
+    want = lib.kv_update(one, k, k, *b.args(), q=q)
+    assert lib.get_device_error() == 0
+    table = dev(np.concatenate([b.table, b.table[:1]]))
+    start = dev(np.append(b.start, b.start[-1] + bad[0]).astype(np.int32))
+    kv = dev(np.append(b.kv_len, bad[1]).astype(np.int32))
+    got = lib.kv_update(two, k, k, table, start, kv, q=q)
+    assert lib.get_device_error() == 8                        # W4A8_ERR_INPUT
+    assert torch.equal(got, want)
+    assert torch.equal(one.k_codes, two.k_codes) and torch.equal(one.k_scales, two.k_scales)
+    out = lib.kv_attention(want, one, *b.args())
+    assert lib.get_device_error() == 0
+    assert torch.equal(lib.kv_attention(want, one, table, start, kv), out) and lib.get_device_error() == 8

@@ -100,6 +100,7 @@ struct KvUpdateParams {
   int page_ctas;        // units * kv_heads * 2
   int stride;           // every so many CTAs one takes a page, as far as there are any; the others take q
   int q_parts;          // warps that share a token's heads
+  int checker;          // the CTA that looks at the sequences behind the 32nd, or -1
   unsigned* err;
 };
 
@@ -145,6 +146,14 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) kv_update_kernel(const
   pdl_wait();
   const int g = threadIdx.x / LPH, sub = threadIdx.x & (LPH - 1);
   const int ps = p.cache.page_shift;
+  if (int(blockIdx.x) == p.checker) {
+    // The pages' search ends at the group of 32 sequences that holds its page, and reports what it sees.  Batches of more
+    // have one CTA that looks at the rest, so that a bad sequence is reported wherever it stands.
+#pragma unroll 1
+    for (int b = 32 + threadIdx.x; b < p.batch.batch; b += THREADS)
+      if (kv_load_seq(p.batch, b, ps).bad) record_error(p.err, kErrInput);
+    return;
+  }
   const int turn_at = int(blockIdx.x) / p.stride;
   if (turn_at >= p.page_ctas || int(blockIdx.x) != turn_at * p.stride) {
     // ------------------------------------------------ q: a warp per share of a token's heads
