@@ -130,7 +130,8 @@ w4a8_status w4a8_qk_norm_rope(const w4a8_heads* q, const w4a8_heads* k, int64_t 
  * A batch is B sequences.  Sequence b has the new tokens (rows) q_start[b]
  * .. q_start[b + 1] - 1, which are the last of the kv_len[b] tokens that the
  * cache holds of it; its token t lies in page table[b][t / page].  Entries
- * past a sequence's pages are not read.  Rows from q_start[B] up to `tokens`
+ * past a sequence's pages are not read, nor, by w4a8_kv_attention with a
+ * window, those of pages that lie before every new token's window.  Rows from q_start[B] up to `tokens`
  * belong to no sequence: outputs there are left as they were.  Numbers that
  * do not fit together (rows outside [0, tokens], more new tokens than
  * kv_len, kv_len past the table) leave that sequence out, and page ids

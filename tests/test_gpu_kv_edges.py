@@ -86,3 +86,33 @@ def test_a_bad_sequence_behind_many_is_reported(lib, good, bad):
     out = lib.kv_attention(want, one, *b.args())
     assert lib.get_device_error() == 0
     assert torch.equal(lib.kv_attention(want, one, table, start, kv), out) and lib.get_device_error() == 8
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("lens,hq,hk,window", [
+    ([(1, 300 + 13 * i) for i in range(12)] + [(5, 411), (3, 20), (1, 7)], 4, 2, 37),      # a few rows
+    ([(1, 290), (1, 291), (1, 305), (2, 1000)], 4, 2, 1),
+    ([(900, 1700), (1, 333)], 32, 16, 100),                                                # many: the other kernel
+])
+def test_pages_behind_the_window_may_be_gone(lib, d, page, lens, hq, hk, window):
+    """Entries of pages that every new token's window has passed are not read: -1 there is no error, and what the pages
+    held is not looked at."""
+    b = Batch(lens, hk, page, d, page + d + window)
+    q, _ = bf16(b.rng, b.t, hq, d)
+    want = lib.kv_attention(q, b.cache(lib), *b.args(), window=window)
+    assert lib.get_device_error() == 0
+    gone = []
+    for i, n in enumerate(b.q_len):
+        first = max(0, int(b.kv_len[i]) - n - window + 1)     # the first key that a token of the sequence sees
+        gone += b.table[i, :first // page].tolist()
+        b.table[i, :first // page] = -1
+    assert len(gone) > 0
+    cache = b.cache(lib)
+    for t in (cache.k_scales, cache.v_scales):
+        t[gone] = float("nan")
+    for bad in (-1, b.pages, 2 ** 31 - 1):
+        b.table[b.table == -1] = bad
+        assert torch.equal(lib.kv_attention(q, cache, *b.args(), window=window), want)
+        assert lib.get_device_error() == 0
+        b.table[b.table == bad] = -1

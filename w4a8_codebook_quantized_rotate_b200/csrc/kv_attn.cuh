@@ -375,13 +375,14 @@ __global__ void __launch_bounds__(KaCfg<D, NR>::kThreads, 1)
   auto group_key = [&](int item) { return fseg.key0 + (item * C::kWarps + warp) * C::TK + 16 * fgroup; };
   auto fetch_raw = [&](int base) {
     const int item = base + ftile;
-    return item < fend && group_key(item) < fseg.range.hi
+    return item < fend && group_key(item) >= fseg.range.lo && group_key(item) < fseg.range.hi
                ? __ldg(p.batch.table + (long long)fseg.b * p.batch.table_stride + (group_key(item) >> p.cache.page_shift))
                : -1;
   };
   auto take_batch = [&](int base) {  // nraw, fetched for `base`, becomes the batch at hand
     fid = nraw;
-    if (fid >= p.cache.pages || (fid < 0 && base + ftile < fend && group_key(base + ftile) < fseg.range.hi)) {
+    if (fid >= p.cache.pages ||
+        (fid < 0 && base + ftile < fend && group_key(base + ftile) >= fseg.range.lo && group_key(base + ftile) < fseg.range.hi)) {
       record_error(p.err, kErrInput);
       fid = -1;
     }
@@ -429,6 +430,7 @@ __global__ void __launch_bounds__(KaCfg<D, NR>::kThreads, 1)
     fi = max(s.item0, first > 0 ? first / C::kItem + (first % C::kItem >= C::TK ? 1 : 0) : 0);
     fend = min(s.item1, (s.range.hi - s.key0 - warp * C::TK + C::kItem - 1) / C::kItem);
     nfirst = fi;
+    fseg.range.lo = kv_first_key(fseg.range, p.cache.page_shift);  // (what the feed looks up starts there)
     nraw = fetch_raw(fi);
     if (fi < fend) take_batch(fi);
     for (int n = 0; n < C::kStages && fi < fend; ++n) issue();

@@ -67,6 +67,11 @@ W4A8_HD KvRange kv_range(const KvSeq& s, int j0, int j1, int window) {
   return r;
 }
 
+// The first key of the pages that a range sees.  The kernels' first tile may
+// start before it, in pages that the window has passed and the caller may
+// have given to another sequence: their table entries are not read.
+W4A8_HD int kv_first_key(const KvRange& r, int page_shift) { return (r.lo >> page_shift) << page_shift; }
+
 // Whether the tensor-memory attention kernel takes a batch's sequences of many
 // rows, by both kernels' estimated times in ns (whole numbers, so that the two
 // kernels, which each ask, agree).  `units` are its row tiles times key heads,

@@ -579,7 +579,8 @@ __global__ void __launch_bounds__(KpCfg<D>::kThreads, 1) kv_prefill_kernel(const
       __syncwarp();
     };
     uint4 wk[NP], wv[NP];
-    int ids = checked(fetch_ids(0), 0), raw = fetch_ids(1);
+    // (the first tile may start in pages that the window has passed)
+    int ids = key0 + 16 * lane < kv_first_key(range, ps) ? -1 : checked(fetch_ids(0), 0), raw = fetch_ids(1);
     load(0, 0, ids, wk);
     load(1, 0, ids, wv);
     float2 sc = fetch_scales(ids);
