@@ -9,7 +9,8 @@ or whose input width the rotation block does not divide).
 
 Everything runs on the calls of :mod:`.binding`, on the current stream; with
 :meth:`AttentionBlock.prepare` called for the token count, a step allocates
-only its outputs and can be captured into a CUDA graph.
+only its outputs and can be captured into a CUDA graph (a capture that would
+have to allocate a workspace is refused).
 """
 
 from __future__ import annotations
@@ -19,26 +20,37 @@ import torch
 from . import binding as B
 
 
+def _capturing(device: torch.device) -> bool:
+    return device.type == "cuda" and torch.cuda.is_current_stream_capturing()
+
+
 class _Workspaces:
-    """Workspaces of a layer for any number of tokens: the last one serves every call that it is large enough for;
-    where it is too small the next one is at least twice as large, and the earlier ones stay for captured graphs that
-    name them."""
+    """Workspaces of a layer for any number of tokens, on each device: the last one serves every call that it is large
+    enough for; where it is too small the next one is at least twice as large, and the earlier ones stay for captured
+    graphs that name them.  None is made inside a capture: its zero fill would be recorded instead of run, and calls
+    before the first replay would find words that must be zero as the memory held them."""
 
     def __init__(self, need):
         self._need = need
         self._held: list[torch.Tensor] = []
-        self._of: dict[int, torch.Tensor] = {}
+        self._of: dict[tuple[torch.device, int], torch.Tensor] = {}
 
     def get(self, m: int, device) -> torch.Tensor:
-        ws = self._of.get(m)
+        device = torch.device(device)
+        if device.type == "cuda" and device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
+        ws = self._of.get((device, m))
         if ws is None:
             need = self._need(m)
             if need == 0:
                 raise B.W4A8Error("workspace", 2)
-            if not self._held or self._held[-1].numel() < need:
-                need = max(need, 2 * self._held[-1].numel() if self._held else 0)
-                self._held.append(torch.zeros(need, dtype=torch.uint8, device=device))
-            ws = self._of[m] = self._held[-1]
+            ws = next((w for w in reversed(self._held) if w.device == device), None)
+            if ws is None or ws.numel() < need:
+                if _capturing(device):
+                    raise RuntimeError(f"no workspace for {m} tokens yet: call prepare({m}) before the capture")
+                ws = torch.zeros(need if ws is None else max(need, 2 * ws.numel()), dtype=torch.uint8, device=device)
+                self._held.append(ws)
+            self._of[device, m] = ws
         return ws
 
 
@@ -98,11 +110,11 @@ class AttentionBlock:
         self.scale, self.window = scale, window
         self._workspaces = _Workspaces(lambda m: B.kv_attention_workspace_bytes(m, heads, kv_heads, head_dim))
 
-    def prepare(self, tokens: int, device="cuda") -> torch.Tensor:
-        """Allocate what steps of that many tokens need; returns the attention's workspace."""
-        self.qkv.prepare(tokens)
-        self.out.prepare(tokens)
-        return self._workspaces.get(tokens, device)
+    def prepare(self, tokens: int, device=None) -> torch.Tensor:
+        """Allocate what steps of that many tokens need (the attention's part on ``device``, by default the layers');
+        returns the attention's workspace."""
+        layers = [layer.prepare(tokens) for layer in (self.qkv, self.out)]
+        return self._workspaces.get(tokens, layers[0].device if device is None else device)
 
     def __call__(self, x: torch.Tensor, cache: B.KvCache, block_table: torch.Tensor, q_start: torch.Tensor,
                  kv_len: torch.Tensor, positions: torch.Tensor | None = None) -> torch.Tensor:
