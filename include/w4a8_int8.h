@@ -108,9 +108,10 @@ typedef struct {
  *   n = x * rsqrt(mean(x^2) + eps) * weight,  out = rotate(n)
  * in fp32, rounded once to bf16.  q_weight / k_weight are fp32 [D]; NULL
  * leaves that norm out.  q.data or k.data may be NULL (then only the other
- * is done); an output may be its input (same strides), and the rows of an
- * output must not share memory.  positions [T] int32
- * (may be NULL without a rotation).  D is 64, 128 or 256; T in [1, 2^24].
+ * is done).  An output may be its input (same address and strides, else
+ * SHAPE); otherwise outputs share no memory with each other or with an input,
+ * and the rows of an output none among themselves (SHAPE).  positions [T]
+ * int32 (may be NULL without a rotation).  D is 64, 128 or 256; T in [1, 2^24].
  * Errors: NULL, SHAPE, ALIGN, ARCH, CUDA.
  */
 w4a8_status w4a8_qk_norm_rope(const w4a8_heads* q, const w4a8_heads* k, int64_t T, int32_t D,
@@ -163,7 +164,8 @@ typedef struct {
  *   scale' = max(scale, absmax(new values) / 127), where scale counts as 0
  *   if the page's first token is written by this call; codes that were there
  *   become rint(code * (scale / scale')) when it grew.
- * k, v [tokens][kv_heads][D]; q and q_out (data NULL: none) [tokens][heads][D].
+ * k, v [tokens][kv_heads][D]; q and q_out (data NULL: none) [tokens][heads][D];
+ * q_out may be q, as in w4a8_qk_norm_rope.
  * positions NULL: a token's position is its place in the sequence.  A call
  * writes each page for one sequence and one place of its block table (a page
  * id that stands there twice gets undefined contents).
@@ -197,9 +199,10 @@ size_t w4a8_kv_attention_workspace_bytes(int64_t tokens, int32_t q_heads, int32_
  * them (w4a8_kv_update):
  *   out_i = sum_j softmax_j(scale q_i . K_j) V_j,  j <= position of i,
  *   and j > position - window when window > 0,
- * K, V = code * scale (a V scale below 2^-80 may count as 0).  q, out [tokens][q_heads][D], q_heads a multiple of
- * kv_heads and at most 128 of them to a key head (head h reads key head
- * h / (q_heads / kv_heads)).
+ * K, V = code * scale (a V scale below 2^-80 may count as 0).  q, out
+ * [tokens][q_heads][D], q_heads a multiple of kv_heads and at most 128 of them
+ * to a key head (head h reads key head h / (q_heads / kv_heads)); out may be q,
+ * as in w4a8_qk_norm_rope.
  * Errors: NULL, SHAPE, ALIGN, WORKSPACE, ARCH, CUDA.
  */
 w4a8_status w4a8_kv_attention(const w4a8_heads* q, const w4a8_kv_cache* cache, const w4a8_kv_batch* batch,

@@ -116,3 +116,32 @@ def test_pages_behind_the_window_may_be_gone(lib, d, page, lens, hq, hk, window)
         assert torch.equal(lib.kv_attention(q, cache, *b.args(), window=window), want)
         assert lib.get_device_error() == 0
         b.table[b.table == bad] = -1
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("lens,hq,hk", [FEW[:3], MANY[:3], ([(1, 3000)], 8, 2), ([(200, 1300), (1, 500), (3, 40)], 32, 16)])
+def test_attention_in_place(lib, d, lens, hq, hk):
+    """The output over its queries, parts of a longer row: the bits of a call with an output of its own."""
+    b = Batch(lens, hk, 16, d, 110 + d, behind=2)
+    rows, _ = bf16(b.rng, b.t, hq + 3, d)
+    q, cache = rows[:, 1:1 + hq], b.cache(lib)
+    want, rest = lib.kv_attention(q, cache, *b.args()), rows.clone()
+    n = int(b.start[-1])
+    lib.kv_attention(q, cache, *b.args(), out=q)
+    assert lib.get_device_error() == 0
+    rest[:n, 1:1 + hq] = want[:n]
+    assert torch.equal(rows, rest)
+    with pytest.raises(lib.W4A8Error):
+        lib.kv_attention(q, cache, *b.args(), out=q.as_strided(q.shape, (hq * d, d, 1)))
+
+
+def test_strides_of_one_token_or_one_head_do_not_matter(lib):
+    """In place, where a dimension of one has another stride than the input's."""
+    w, inv = dev(np.ones(128, np.float32)), dev(INV[64])
+    for t, h, strides in ((1, 4, (4096, 128, 1)), (3, 1, (512, 4096, 1))):
+        x, _ = bf16(np.random.default_rng(111), t, 4, 128)
+        x = x[:, :h]
+        pos = torch.arange(t, dtype=torch.int32, device="cuda")
+        want, _ = lib.qk_norm_rope(x, None, pos, w, inv_freq=inv)
+        lib.qk_norm_rope(x, None, pos, w, inv_freq=inv, q_out=x.as_strided(x.shape, strides))
+        assert torch.equal(x, want) and lib.get_device_error() == 0

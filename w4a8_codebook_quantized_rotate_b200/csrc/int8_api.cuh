@@ -198,6 +198,12 @@ w4a8_status heads_out_ok(const w4a8_heads& h, int64_t tokens, int64_t D) {
   const bool apart = tokens == 1 || h.token_stride >= token || (h.token_stride >= D && (h.heads == 1 || h.head_stride >= head));
   return apart ? W4A8_OK : W4A8_ERR_SHAPE;
 }
+// An output that starts where its input does must be that input, row for row: under other strides rows would be written
+// that other threads have yet to read.
+bool heads_in_place_ok(const w4a8_heads& in, const w4a8_heads& out, int64_t tokens) {
+  return in.data != out.data || ((tokens == 1 || in.token_stride == out.token_stride) &&
+                                 (in.heads == 1 || in.head_stride == out.head_stride));
+}
 HeadRows head_rows(const w4a8_heads* h) {
   if (!h || !h->data) return HeadRows{nullptr, 0, 0, 0};
   return HeadRows{h->data, h->token_stride, h->head_stride, h->heads};
@@ -403,6 +409,7 @@ w4a8_status w4a8_qk_norm_rope(const w4a8_heads* q, const w4a8_heads* k, int64_t 
     if (h)
       if (w4a8_status st = heads_out_ok(*h, T, D); st != W4A8_OK) return st;
   if ((has_q && q->heads != q_out->heads) || (has_k && k->heads != k_out->heads)) return W4A8_ERR_SHAPE;
+  if ((has_q && !heads_in_place_ok(*q, *q_out, T)) || (has_k && !heads_in_place_ok(*k, *k_out, T))) return W4A8_ERR_SHAPE;
   if (w4a8_status st = rope_ok(rope, D); st != W4A8_OK) return st;
   if ((q_weight && !aligned16(q_weight)) || (k_weight && !aligned16(k_weight)) || !aligned4(positions)) return W4A8_ERR_ALIGN;
   DeviceState* d = nullptr;
@@ -432,6 +439,7 @@ w4a8_status w4a8_kv_update(const w4a8_kv_cache* cache, const w4a8_kv_batch* batc
   if (has_q)
     if (w4a8_status st = heads_out_ok(*q_out, batch->tokens, D); st != W4A8_OK) return st;
   if (k->heads != cache->kv_heads || v->heads != cache->kv_heads || (has_q && q->heads != q_out->heads)) return W4A8_ERR_SHAPE;
+  if (has_q && !heads_in_place_ok(*q, *q_out, batch->tokens)) return W4A8_ERR_SHAPE;
   if (w4a8_status st = rope_ok(rope, D); st != W4A8_OK) return st;
   if ((q_weight && !aligned16(q_weight)) || (k_weight && !aligned16(k_weight)) || !aligned4(positions)) return W4A8_ERR_ALIGN;
   const int64_t units = kv_touched_bound(batch->tokens, batch->batch, cache->page);
@@ -499,6 +507,7 @@ w4a8_status w4a8_kv_attention(const w4a8_heads* q, const w4a8_kv_cache* cache, c
   if (w4a8_status st = heads_ok(*q, D); st != W4A8_OK) return st;
   if (w4a8_status st = heads_out_ok(*out, batch->tokens, D); st != W4A8_OK) return st;
   if (q->heads != out->heads || window < 0 || !ka_shape_ok(batch->tokens, q->heads, cache->kv_heads, D)) return W4A8_ERR_SHAPE;
+  if (!heads_in_place_ok(*q, *out, batch->tokens)) return W4A8_ERR_SHAPE;
   if (!aligned16(workspace)) return W4A8_ERR_ALIGN;
   if (workspace_bytes < w4a8_kv_attention_workspace_bytes(batch->tokens, q->heads, cache->kv_heads, D))
     return W4A8_ERR_WORKSPACE;
