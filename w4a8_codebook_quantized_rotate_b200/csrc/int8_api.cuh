@@ -264,17 +264,6 @@ bool ka_shape_ok(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t D) {
 constexpr size_t kKaZeroBytes = 1024;
 static_assert((kKaMaxCtas + kKaMaxCtas / 2) * 4 <= kKaZeroBytes, "counters fit");
 
-// The host knows only the batch's totals and the block table's width: it
-// launches the tensor-memory kernel too where that would pay at the table's
-// width, and the average sequence has rows for it or the total is so large
-// that a few of many sequences may (a launch that finds nothing to do costs
-// 5 us).
-constexpr int64_t kKpMinCtas = 4, kKpSureCtas = 32;
-// Tiles of 256 rows that the tensor-memory kernel may have.
-int64_t kp_ctas_bound(int64_t rows, int64_t batch, int64_t kv_heads) {
-  return (rows / 256 + std::min<int64_t>(batch, rows / kKpMinRows)) * kv_heads;
-}
-
 // Row tiles of 8 where a sequence has that many rows on average (a decode
 // step of up to 8 query heads to a key head), else of 16.
 bool ka_few_rows(int64_t tokens, int64_t batch, int group) { return tokens * group <= 8 * batch; }
@@ -293,15 +282,11 @@ cudaError_t ka_launch(const KaParams& p, const w4a8_kv_cache* c, int ctas, cudaS
   q.box_shift = page_shift_of(box);
   // The tensor-memory kernel goes first where the batch may have rows for it (each kernel decides from the
   // sequences' lengths which of them are its own).
-  const int64_t rows = int64_t(p.batch.tokens) * p.group;
-  const int64_t units = rows / KpCfg<D>::kRows + std::min<int64_t>(p.batch.batch, rows / kKpMinRows);
-  const int64_t bound = kp_ctas_bound(rows, p.batch.batch, c->kv_heads);
-  const int64_t capacity = p.batch.table_stride * c->page;
-  const int64_t keys = p.window > 0 ? std::min<int64_t>(capacity, int64_t(p.window) + p.batch.tokens) : capacity;
-  q.both = bound >= kKpMinCtas && (bound >= kKpSureCtas || rows >= kKpMinRows * int64_t(p.batch.batch)) &&
-           kv_tiles_pay(units * c->kv_heads, rows * (keys + 512) * c->kv_heads, keys, D, p.sms);
+  q.both = kv_tiles_may_pay(p.batch.tokens, p.batch.batch, p.group, c->kv_heads, p.batch.table_stride * c->page, p.window,
+                            D, p.sms);
   if (q.both) {
-    const int64_t grid = units * c->kv_heads + p.sms;  // (the units' parts are at most one wave)
+    const int64_t units = kp_tiles_bound(int64_t(p.batch.tokens) * p.group, p.batch.batch, kp_rows(D)) * c->kv_heads;
+    const int64_t grid = units + p.sms;  // (the units' parts are at most one wave)
     if (grid >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
     if (cudaError_t e = launch_pdl(kv_prefill_kernel<D>, dim3(unsigned(grid)), dim3(KpCfg<D>::kThreads),
                                    KpCfg<D>::kSmem, st, q);
@@ -494,7 +479,7 @@ size_t w4a8_kv_attention_workspace_bytes(int64_t tokens, int32_t q_heads, int32_
   const int64_t rows = tokens * (q_heads / kv_heads);
   const size_t stream = size_t(kKaMaxCtas) * 2 * (size_t(kKaMaxRows) * head_dim + 2 * kKaMaxRows) * 4;
   const size_t parts = size_t(kKaMaxCtas) * (head_dim <= 128 ? 256 : 128) * (head_dim + 2) * 4;
-  return kKaZeroBytes + (kp_ctas_bound(rows, tokens, kv_heads) >= kKpMinCtas ? std::max(stream, parts) : stream);
+  return kKaZeroBytes + (kp_tiles_bound(rows, tokens, 256) * kv_heads >= kKpMinCtas ? std::max(stream, parts) : stream);
 }
 
 w4a8_status w4a8_kv_attention(const w4a8_heads* q, const w4a8_kv_cache* cache, const w4a8_kv_batch* batch, float scale,

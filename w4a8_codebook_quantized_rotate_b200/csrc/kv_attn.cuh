@@ -137,20 +137,9 @@ __device__ __forceinline__ bool ka_wait(uint64_t* bar, uint32_t parity, KaShared
   return false;
 }
 
-// A CTA's share of `total` items among the first min(ctas, total) CTAs.
-W4A8_HD long long ka_first_item(long long c, long long total, long long ctas) { return total * c / ctas; }
-W4A8_HD int ka_item_cta(long long i, long long total, long long ctas) {
-  return int(((i + 1) * ctas + total - 1) / total - 1);
-}
-
-// Sequences of at least kKpMinRows rows (new tokens x query heads of a key
-// head) are left to the tensor-memory kernel (kv_prefill.cuh) where that pays
-// (kv_tiles_pay).
-constexpr int kKpMinRows = 128;
-template <int D>
-constexpr int kKpRows = D <= 128 ? 256 : 128;  // of one of its units
-
-// Units of the batch that it takes; 0 where the streaming kernel takes all.
+// Units (row tiles times key heads) of the batch that the tensor-memory kernel
+// (kv_prefill.cuh) takes: those of the sequences of at least kKpMinRows rows,
+// where that pays (kv_tiles_pay).  0 where the streaming kernel takes all.
 template <int D>
 __device__ __forceinline__ int kp_units(const KaParams& p) {  // whole warp
   const int lane = threadIdx.x & 31;
@@ -159,12 +148,11 @@ __device__ __forceinline__ int kp_units(const KaParams& p) {  // whole warp
   for (int b0 = 0; b0 < p.batch.batch; b0 += 32) {
     if (b0 + lane < p.batch.batch) {
       const KvSeq s = kv_load_seq(p.batch, b0 + lane, p.cache.page_shift);
-      const int rows = s.q_len * p.group;
-      if (rows >= kKpMinRows) {
-        const KvRange r = kv_range(s, 0, s.q_len - 1, p.window);
-        units += (rows + kKpRows<D> - 1) / kKpRows<D>;
-        work += (long long)rows * (r.hi - r.lo + 512);
-        most = max(most, r.hi - r.lo);
+      if (kv_has_tiles(s, p.group)) {
+        const KvTiles t = kv_tiles_of(s, p.group, p.window, kp_rows(D));
+        units += t.tiles;
+        work += t.row_keys;
+        most = max(most, t.keys);
       }
     }
   }

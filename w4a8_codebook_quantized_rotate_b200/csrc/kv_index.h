@@ -92,4 +92,45 @@ W4A8_HD bool kv_tiles_pay(int64_t units, int64_t row_keys, int64_t most_keys, in
   return 8000 + row_keys / 35000 * D > base + rate * ((most_keys + 63) / 64) * waves / parts;
 }
 
+// What a sequence adds to that estimate: nothing below kKpMinRows rows (new
+// tokens x query heads of a key head), which the streaming kernel keeps.
+constexpr int kKpMinRows = 128;
+W4A8_HD constexpr int kp_rows(int D) { return D <= 128 ? 256 : 128; }  // of a row tile
+struct KvTiles {  // of a sequence that has any (kv_has_tiles)
+  int tiles, keys;
+  int64_t row_keys;
+};
+W4A8_HD bool kv_has_tiles(const KvSeq& s, int group) { return s.q_len * group >= kKpMinRows; }
+W4A8_HD KvTiles kv_tiles_of(const KvSeq& s, int group, int window, int tile_rows) {
+  const int rows = s.q_len * group;
+  const KvRange r = kv_range(s, 0, s.q_len - 1, window);
+  return KvTiles{(rows + tile_rows - 1) / tile_rows, r.hi - r.lo, int64_t(rows) * (r.hi - r.lo + 512)};
+}
+
+// The host knows only the batch's totals and the block table's width: it
+// launches the tensor-memory kernel too where that would pay at the table's
+// width, and the average sequence has rows for it or the total is so large
+// that a few of many sequences may (a launch that finds nothing to do costs
+// 5 us).
+constexpr int64_t kKpMinCtas = 4, kKpSureCtas = 32;
+inline int64_t kv_min(int64_t a, int64_t b) { return a < b ? a : b; }
+// Tiles of that many rows that the batch may have, for each key head.
+inline int64_t kp_tiles_bound(int64_t rows, int64_t batch, int tile_rows) {
+  return rows / tile_rows + kv_min(batch, rows / kKpMinRows);
+}
+inline bool kv_tiles_may_pay(int64_t tokens, int64_t batch, int group, int kv_heads, int64_t capacity, int window, int D,
+                             int sms) {
+  const int64_t rows = tokens * group, bound = kp_tiles_bound(rows, batch, 256) * kv_heads;
+  const int64_t keys = window > 0 ? kv_min(capacity, int64_t(window) + tokens) : capacity;
+  return bound >= kKpMinCtas && (bound >= kKpSureCtas || rows >= kKpMinRows * batch) &&
+         kv_tiles_pay(kp_tiles_bound(rows, batch, kp_rows(D)) * kv_heads, rows * (keys + 512) * kv_heads, keys, D, sms);
+}
+
+// The streaming kernel's items over its CTAs: a CTA's share of `total` items
+// among the first `ctas` = min(CTAs, total) CTAs, and the CTA of an item.
+W4A8_HD long long ka_first_item(long long c, long long total, long long ctas) { return total * c / ctas; }
+W4A8_HD int ka_item_cta(long long i, long long total, long long ctas) {
+  return int(((i + 1) * ctas + total - 1) / total - 1);
+}
+
 }  // namespace w4a8

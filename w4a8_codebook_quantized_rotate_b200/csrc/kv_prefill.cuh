@@ -59,7 +59,7 @@ struct KpCfg {
   static constexpr int TK = 64;                          // keys of a tile
   static constexpr int kStages = D <= 128 ? 4 : 2;       // of K, and of V
   static constexpr int KG = TK / 16;                     // key groups (one page each)
-  static constexpr int kRows = kKpRows<D>;
+  static constexpr int kRows = kp_rows(D);
   static_assert(kRows == 128 * kTiles, "TMEM lanes");
   static constexpr int kSoftWarps = 4 * kTiles;
   static constexpr int kThreads = 32 * (kSoftWarps + kKpConvWarps + 2);  // softmax, converters, two MMA warps
