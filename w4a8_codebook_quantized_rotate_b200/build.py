@@ -13,6 +13,7 @@ SRC = os.path.join(PKG, "csrc", "w4a8_api.cu")
 OUT = os.path.join(PKG, "lib", "libw4a8.so")
 MARSHAL_SRC = os.path.join(PKG, "csrc", "marshal.cpp")
 MARSHAL_OUT = os.path.join(PKG, "lib", "w4a8_marshal.so")
+MARSHAL_AGAINST = MARSHAL_OUT + ".against"
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -38,10 +39,24 @@ def _fresh(out: str, srcs: list[str]) -> bool:
     return os.path.exists(out) and all(os.path.getmtime(s) <= os.path.getmtime(out) for s in srcs)
 
 
+def marshal_against() -> str:
+    """What the binding's compiled part is compiled against, as text: this Python and this torch (whose C++ classes it
+    uses, so another build of torch needs another one)."""
+    import sys
+
+    import torch
+    return f"python {sys.version}\ntorch {torch.__version__} {torch.version.git_version} {os.path.dirname(torch.__file__)}\n"
+
+
 def build_marshal(force: bool = False) -> str:
-    """Compile the binding's compiled part (host C++ over the C ABI and torch's tensors) if it is not up to date."""
+    """Compile the binding's compiled part (host C++ over the C ABI and torch's tensors) if it is not up to date: older
+    than its sources, or compiled against another Python or torch than this one (kept beside it, in MARSHAL_AGAINST)."""
     headers = [os.path.join(ROOT, "include", f) for f in ("w4a8.h", "w4a8_int8.h")]
-    if not force and _fresh(MARSHAL_OUT, [MARSHAL_SRC, *headers]):
+    against, was = marshal_against(), ""
+    if os.path.exists(MARSHAL_AGAINST):
+        with open(MARSHAL_AGAINST) as f:
+            was = f.read()
+    if not force and was == against and _fresh(MARSHAL_OUT, [MARSHAL_SRC, *headers]):
         return MARSHAL_OUT
     import sysconfig
 
@@ -56,6 +71,8 @@ def build_marshal(force: bool = False) -> str:
            "-L", lib, "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-lc10", "-lc10_cuda", "-Wl,-rpath," + lib]
     subprocess.run(cmd, check=True)
     os.replace(MARSHAL_OUT + ".tmp", MARSHAL_OUT)
+    with open(MARSHAL_AGAINST, "w") as f:
+        f.write(against)
     return MARSHAL_OUT
 
 
