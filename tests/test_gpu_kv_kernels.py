@@ -9,6 +9,7 @@ import torch
 
 import kv_index
 import test_gpu_kv as T
+import test_gpu_kv_edges as E
 from oracle import int8_ref as R
 from test_gpu_kv import Batch, attend, bf16, check_attention
 
@@ -83,3 +84,20 @@ def test_few_and_even_keys_on_the_tensor_memory_kernel(lib, lens, hq, hk, d, sca
     check_attention(out, *R.attention(qx, b.ref, b.table, b.start, b.kv_len, scale, window), least=TENSOR)
     ws[1024:] = 255                                              # (NaN in every partial result that is not written)
     assert torch.equal(lib.kv_attention(q, cache, *b.args(), scale=scale, window=window, workspace=ws), out)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("power,window", [(118, 70), (34, 300), (30, 37)])
+def test_far_scores_in_windows_on_the_tensor_memory_kernel(lib, d, power, window):
+    """Scores past 2^20 that first show in a tile at the window's start, and go on in tiles without a masked key."""
+    lens = [(700, 1300), (140, 300)]
+    assert kv_index.tensor_units(lens, 32, 16, 16, d, window)
+    E.test_one_key_takes_all_the_weight(lib, d, lens, 32, 16, TENSOR, power, window)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_edge_cases_reach_both_kernels(lib, d):
+    assert not kv_index.tensor_units(E.FEW[0], *E.FEW[1:3], 16, d)
+    assert kv_index.tensor_units(E.MANY[0], *E.MANY[1:3], 16, d)
+    for page in (16, 32, 64, 128):
+        assert kv_index.tensor_units([(900, 1700), (1, 333)], 32, 16, page, d, 100)
