@@ -94,7 +94,8 @@ typedef struct {
  * D - rot_dim values of a head are not turned.  inv_freq is fp64 (device)
  * and carries any scaling for long contexts; `factor` multiplies cosine and
  * sine (the attention factor of such a scaling, else 1).  Angles are formed
- * in fp64.  inv_freq NULL: no rotation.  rot_dim is a multiple of 16, at
+ * in fp64 and brought within half a turn there; their sines and cosines are
+ * the hardware's, off by up to about 2^-21.  inv_freq NULL: no rotation.  rot_dim is a multiple of 16, at
  * most D.
  */
 typedef struct {
@@ -137,7 +138,8 @@ w4a8_status w4a8_qk_norm_rope(const w4a8_heads* q, const w4a8_heads* k, int64_t 
  * do not fit together (rows outside [0, tokens], more new tokens than
  * kv_len, kv_len past the table) leave that sequence out, and page ids
  * outside [0, pages) leave those tokens out; w4a8_get_device_error then
- * reports W4A8_ERR_INPUT and that sequence's results are undefined.
+ * reports W4A8_ERR_INPUT and that sequence's results are undefined (where
+ * q_start goes back, so that sequences share rows, those of all of them).
  * ------------------------------------------------------------------------ */
 typedef struct {
   int8_t* k_codes;
@@ -199,7 +201,11 @@ size_t w4a8_kv_attention_workspace_bytes(int64_t tokens, int32_t q_heads, int32_
  * them (w4a8_kv_update):
  *   out_i = sum_j softmax_j(scale q_i . K_j) V_j,  j <= position of i,
  *   and j > position - window when window > 0,
- * K, V = code * scale (a V scale below 2^-80 may count as 0).  q, out
+ * K, V = code * scale (a V scale below 2^-80 may count as 0).  Scores, the
+ * softmax's maxima and sums, and out until its one rounding are fp32 (q and the
+ * codes are exact in the products' fp16 operands); the weights are rounded to
+ * fp16 (11 bits) for the product with V, and what is below 2^-32 of a row's
+ * largest weight * V scale may count as 0.  q, out
  * [tokens][q_heads][D], q_heads a multiple of kv_heads and at most 128 of them
  * to a key head (head h reads key head h / (q_heads / kv_heads)); out may be q,
  * as in w4a8_qk_norm_rope.

@@ -808,7 +808,7 @@ __global__ void __launch_bounds__(KaCfg<D, NR>::kThreads, 1)
         if (tid == 0) p.counters[c_first] = 0u;  // ready for the next launch on this workspace
       }
     }
-    __syncthreads();  // q fragments, warp_m and the join buffer are free again
+    __syncthreads();  // q fragments, warp_z, warp_l and the join buffer are free again
     seg = nxt;
     have = more;
   }

@@ -137,6 +137,10 @@ __device__ __forceinline__ uint32_t recode4(uint32_t w, float ratio) {
 // other; the pages alone 15.2, q alone 17.0).
 // THREADS: 256, or 64 where a page gets a token or two (a decode step: the
 // CTAs of 64 sequences x 8 heads are then all resident at once).
+// Three (or twelve) CTAs an SM cap the registers at 80, of which the pages'
+// path spills 188 to 204 bytes a thread (its four rows of angles and values);
+// the cap holds for q's path too.  That the two together take nearly the sum
+// of their own times is in part this.
 template <int D, int THREADS>
 __global__ void __launch_bounds__(THREADS, 768 / THREADS) kv_update_kernel(const KvUpdateParams p) {
   constexpr int LPH = D / 8, RPP = THREADS / LPH;  // rows per pass

@@ -82,6 +82,8 @@ W4A8_HD int kv_first_key(const KvRange& r, int page_shift) { return (r.lo >> pag
 // parts of each.  Measured, streaming / tensor-memory, us: 130 new tokens of
 // 32/8 heads of 128 on 230 keys 14 / 28, 260 of 8/2 on 6000 keys 53 / 58, 500
 // of 8/2 on 6000 90 / 58, 260 of 12/1 heads of 256 on 6000 133 / 70.
+// All of them without a window: under one, both estimates take the sequence's
+// whole range of keys for each row's and each tile's, and are too long.
 constexpr int kKpMaxParts = 4;
 W4A8_HD bool kv_tiles_pay(int64_t units, int64_t row_keys, int64_t most_keys, int D, int sms) {
   if (units == 0) return false;

@@ -29,9 +29,9 @@
 // along their keys where that fills the SMs better (a rest of at most half a
 // wave, in up to four parts); the parts' O, maxima and sums meet in the
 // workspace, where the last one to arrive adds them in their order (two
-// sequences of up to 2048 new tokens on up to 8192, 32/8 heads of 128: 492 us,
-// 530 unsplit; 476 with the softmax's sums and exponents' arguments two to an
-// instruction and its maxima over three).
+// sequences of up to 2048 new tokens on up to 8192, 32/8 heads of 128, in a
+// captured stream: 492 us, 530 unsplit; 478 with the softmax's sums and
+// exponents' arguments two to an instruction and its maxima over three).
 // Slower at that size: P' in buffers of its own, so that the scores wait only
 // for the softmax (493), and tiles of 128 keys with one buffer of scores (651,
 // the scores read twice).  Without its exponentials, its expansion or its

@@ -20,7 +20,8 @@
 // in registers; a warp walks a token's heads with nothing shared and no
 // barrier.  The kernel's instructions (about 75 a lane and head) and its
 // bytes then take about the same time: 8197 tokens of 32/8 heads of 128, 168
-// MB, in 32.3 us (5.2 TB/s); 16 tokens of 24/4 heads of 256 in 2.6.
+// MB, in 32.3 us (5.2 TB/s); 16 tokens of 24/4 heads of 256 in 2.6.  Four CTAs
+// an SM cap the registers at 64; 36 to 56 bytes a thread spill.
 #pragma once
 
 #include "common.cuh"
