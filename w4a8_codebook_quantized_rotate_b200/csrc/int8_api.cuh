@@ -447,8 +447,8 @@ w4a8_status w4a8_kv_update(const w4a8_kv_cache* cache, const w4a8_kv_batch* batc
   const int threads = small ? 64 : 256;
   const int64_t q_ctas = has_q ? (batch->tokens * p.q_parts * 32 + threads - 1) / threads : 0;
   p.stride = int((page_ctas + q_ctas) / page_ctas);
-  p.checker = batch->batch > 32 ? int(page_ctas + q_ctas) : -1;
-  const dim3 grid{unsigned(page_ctas + q_ctas + (p.checker >= 0))}, block{unsigned(threads)};
+  p.rest_cta = batch->batch > 32 ? int(page_ctas + q_ctas) : -1;
+  const dim3 grid{unsigned(page_ctas + q_ctas + (p.rest_cta >= 0))}, block{unsigned(threads)};
   switch (D + small) {
     case 64: return status_of(launch_pdl(kv_update_kernel<64, 256>, grid, block, 0, s, p));
     case 65: return status_of(launch_pdl(kv_update_kernel<64, 64>, grid, block, 0, s, p));

@@ -100,7 +100,7 @@ struct KvUpdateParams {
   int page_ctas;        // units * kv_heads * 2
   int stride;           // every so many CTAs one takes a page, as far as there are any; the others take q
   int q_parts;          // warps that share a token's heads
-  int checker;          // the CTA that looks at the sequences behind the 32nd, or -1
+  int rest_cta;         // the CTA that looks at the sequences behind the 32nd, or -1
   unsigned* err;
 };
 
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) kv_update_kernel(const
   pdl_wait();
   const int g = threadIdx.x / LPH, sub = threadIdx.x & (LPH - 1);
   const int ps = p.cache.page_shift;
-  if (int(blockIdx.x) == p.checker) {
+  if (int(blockIdx.x) == p.rest_cta) {
     // The pages' search ends at the group of 32 sequences that holds its page, and reports what it sees.  Batches of more
     // have one CTA that looks at the rest, so that a bad sequence is reported wherever it stands.
 #pragma unroll 1
